@@ -14,6 +14,8 @@
 #include "ql_common.cuh"
 #include "ql_dequant.cuh"
 #include "ql_gemv.cuh"
+#include "ql_lora.cuh"
+#include "ql_norm.cuh"
 #include "ql_pack.cuh"
 #include "ql_pack_fit.cuh"
 #include "ql_prepass.cuh"
@@ -75,15 +77,21 @@ cudaError_t skinny_smem_attr() {
                                 skinny::Layout<NT, B>::kSmemBytes);
 }
 
-template <int B, bool kSwiGLU = false>
+template <int B, bool kSwiGLU = false, bool kLora = false>
 cudaError_t fused_smem_attr() {
     using FB = typename fused::PickCfg<B, true>::type;
     using FF = typename fused::PickCfg<B, false>::type;
-    const cudaError_t e = cudaFuncSetAttribute(fused::fused_gemm_kernel<true, FB, kSwiGLU>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, FB::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(fused::fused_gemm_kernel<false, FF, kSwiGLU>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, FF::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(fused::fused_gemm_kernel<true, FB, kSwiGLU, false, kLora>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, FB::kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fused::fused_gemm_kernel<false, FF, kSwiGLU, false, kLora>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, FF::kSmemBytes);
+    if constexpr (!kSwiGLU) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fused::fused_gemm_kernel<false, FF, false, true, kLora>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, FF::kSmemBytes);
+    }
+    return e;
 }
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
@@ -100,13 +108,8 @@ ql_status device_info(DeviceInfo** out) {
     }
     if (!d.fused_attr_set) {
         if (fused_smem_attr<4>() != cudaSuccess || fused_smem_attr<8>() != cudaSuccess ||
-            fused_smem_attr<4, true>() != cudaSuccess ||
-            cudaFuncSetAttribute(fused::fused_gemm_kernel<false, fused::PickCfg<4, false>::type, false, true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 fused::PickCfg<4, false>::type::kSmemBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(fused::fused_gemm_kernel<false, fused::PickCfg<8, false>::type, false, true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 fused::PickCfg<8, false>::type::kSmemBytes) != cudaSuccess)
+            fused_smem_attr<4, true>() != cudaSuccess || fused_smem_attr<4, false, true>() != cudaSuccess ||
+            fused_smem_attr<8, false, true>() != cudaSuccess || fused_smem_attr<4, true, true>() != cudaSuccess)
             return QL_ERR_CUDA;
         d.fused_attr_set = true;
     }
@@ -401,9 +404,112 @@ ql_status launch_convert_x(int bits, const __nv_bfloat16* x, __half* xh, float* 
                      : launch_dependent(convert_x_kernel<8, 256, 4>, rows, 256, 0, st, x, xh, rs, k);
 }
 
+// ------------------------------------------------------------------ low-rank adapters
+
+// The adapters of a call (pairs: 1, or 2 for a gate/up pair) and where their scratch lies in the workspace.
+struct LoraArgs {
+    const void* a[2] = {nullptr, nullptr};
+    const void* b[2] = {nullptr, nullptr};
+    const float* scale = nullptr;
+    const int* ids = nullptr;
+    int L = 0, r = 0, pairs = 1;
+};
+struct LoraPlan {
+    int S = 1, passes = 1, nt = 1, chunks = 1;      // launch shape of the shrink kernel
+    size_t off_t = 0, off_slot = 0, off_count = 0, off_list = 0, workspace = 0;
+};
+
+// The shrink kernel's tiles of 16 rows alone fill the GPU only from a few thousand rows on.  Below, a cluster of up to
+// 8 CTAs shares a tile's K range, the rank is cut into narrower chunks, and a tile's distinct adapters go to up to
+// 16 CTAs, each as far as it keeps the launch near two CTAs per SM.
+LoraPlan lora_plan(int64_t M, int64_t K, int r, int L, int pairs, bool fused_path, size_t base, int sm_count) {
+    LoraPlan lp;
+    const int64_t tiles = (M + lora::kTile - 1) / lora::kTile;
+    const int64_t want = 2 * sm_count;
+    const int r8 = r / 8;
+    lp.nt = r8 >= 8 ? 8 : r8 >= 3 ? 4 : r8;
+    int64_t ctas = tiles * pairs * ((r8 + lp.nt - 1) / lp.nt);
+    // at least two 32-column blocks of K per warp and CTA
+    while (lp.S < lora::kMaxSplit && ctas * lp.S < want && K / 32 >= 2 * lora::kWarps * 2 * lp.S) lp.S *= 2;
+    while (lp.nt > 1 && ctas * lp.S * 2 <= want) {
+        lp.nt /= 2;
+        ctas = tiles * pairs * ((r8 + lp.nt - 1) / lp.nt);
+    }
+    lp.chunks = (r8 + lp.nt - 1) / lp.nt;
+    while (lp.passes < std::min(L, lora::kTile) && ctas * lp.S * lp.passes < want) ++lp.passes;
+    if (M <= 512) lp.passes = std::min(L, lora::kTile);
+    lp.off_t = round_up(base, 256);
+    lp.off_slot = lp.off_t + round_up(static_cast<size_t>(pairs) * M * r * 4, 256);
+    lp.workspace = lp.off_slot;
+    if (fused_path) {
+        const size_t num_t = static_cast<size_t>((M + fused::BT - 1) / fused::BT);
+        lp.off_count = lp.off_slot + round_up(static_cast<size_t>(M) * 4, 256);
+        lp.off_list = lp.off_count + round_up(num_t * 4, 256);
+        lp.workspace = lp.off_list + round_up(num_t * fused::BT * 4, 256);
+    }
+    return lp;
+}
+
+// t = s x . A^T of every row's adapter, and on the fused path the token tiles' adapter lists.
+ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, int64_t M, int64_t K, uint8_t* ws,
+                        bool fused_path, bool dependent, cudaStream_t st) {
+    lora::ShrinkParams p = {};
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    for (int i = 0; i < 2; ++i) p.a[i] = static_cast<const __nv_bfloat16*>(la.a[i]);
+    p.scale = la.scale;
+    p.ids = la.ids;
+    p.t = reinterpret_cast<float*>(ws + lp.off_t);
+    p.M = static_cast<int>(M);
+    p.K = static_cast<int>(K);
+    p.r = la.r;
+    p.L = la.L;
+    p.tiles = static_cast<int>((M + lora::kTile - 1) / lora::kTile);
+    p.passes = lp.passes;
+    p.chunks = lp.chunks;
+    if (fused_path) {
+        p.row_slot = reinterpret_cast<int*>(ws + lp.off_slot);
+        p.tile_count = reinterpret_cast<int*>(ws + lp.off_count);
+        p.tile_list = reinterpret_cast<int*>(ws + lp.off_list);
+        p.num_t = static_cast<int>((M + fused::BT - 1) / fused::BT);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles) * lp.passes + p.num_t, lp.S, lp.chunks * la.pairs);
+    cfg.blockDim = dim3(lora::kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = static_cast<unsigned>(lp.S);
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 2 : 1;
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (lp.nt) {
+        case 1: e = cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<1>, p); break;
+        case 2: e = cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<2>, p); break;
+        case 4: e = cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<4>, p); break;
+        case 8: e = cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<8>, p); break;
+    }
+    return e == cudaSuccess ? QL_OK : QL_ERR_CUDA;
+}
+
+fused::LoraParams lora_params(const LoraArgs& la, const LoraPlan& lp, uint8_t* ws) {
+    fused::LoraParams q;
+    for (int i = 0; i < 2; ++i) q.b[i] = static_cast<const __nv_bfloat16*>(la.b[i]);
+    q.t = reinterpret_cast<const float*>(ws + lp.off_t);
+    q.row_slot = reinterpret_cast<const int*>(ws + lp.off_slot);
+    q.tile_count = reinterpret_cast<const int*>(ws + lp.off_count);
+    q.tile_list = reinterpret_cast<const int*>(ws + lp.off_list);
+    q.r = la.r;
+    q.chunks = la.pairs * la.r / 4;
+    return q;
+}
+
 ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
                     void* y, bool bf16_out, int64_t M, int64_t K, int64_t N, void* ws, cudaStream_t st,
-                    int sm_count) {
+                    int sm_count, const LoraArgs* la = nullptr, const LoraPlan* lp = nullptr) {
     const int64_t G = K / kGroup;
     auto* base = static_cast<uint8_t*>(ws);
     auto* xh = reinterpret_cast<__half*>(base + pl.off_xh);
@@ -446,8 +552,11 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
     transpose_params_kernel<<<tgrid, 256, 0, st>>>(static_cast<const __half*>(scales), static_cast<const __half*>(biases),
                                                    sb, static_cast<int>(N), static_cast<int>(G));
     if ((s = launch_status()) != QL_OK) return s;
+    // adapters: their first product runs between the two, beside both (its last CTA waits for the transpose)
+    if (la && (s = launch_shrink(*la, *lp, x, M, K, base, true, true, st)) != QL_OK) return s;
     if ((s = launch_convert_x(bits, static_cast<const __nv_bfloat16*>(x), xh, rs, M, K, st)) != QL_OK) return s;
-    fused::Params p;
+    fused::Params p = {};
+    if (la) p.lora = lora_params(*la, *lp, base);
     p.rowscale = rs;
     p.y = y;
     p.M = static_cast<int>(M);
@@ -463,10 +572,10 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
     using F4 = fused::PickCfg<4, false>::type;
     using F8 = fused::PickCfg<8, false>::type;
     if (split) {
-        s = bits == 4 ? launch_dependent(fused::fused_gemm_kernel<false, F4, false, true>, fgrid, fused::kThreads,
-                                         F4::kSmemBytes, st, mx, mc, mc, mp, my, p)
-                      : launch_dependent(fused::fused_gemm_kernel<false, F8, false, true>, fgrid, fused::kThreads,
-                                         F8::kSmemBytes, st, mx, mc, mc, mp, my, p);
+        auto k4 = la ? fused::fused_gemm_kernel<false, F4, false, true, true> : fused::fused_gemm_kernel<false, F4, false, true>;
+        auto k8 = la ? fused::fused_gemm_kernel<false, F8, false, true, true> : fused::fused_gemm_kernel<false, F8, false, true>;
+        s = bits == 4 ? launch_dependent(k4, fgrid, fused::kThreads, F4::kSmemBytes, st, mx, mc, mc, mp, my, p)
+                      : launch_dependent(k8, fgrid, fused::kThreads, F8::kSmemBytes, st, mx, mc, mc, mp, my, p);
         if (s != QL_OK) return s;
         prof_end(st);
         // ordered sum of the slices, rounded once (a plain launch: it reads what the kernel above wrote)
@@ -478,44 +587,45 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
             ordered_sum_kernel<false><<<blocks, 256, 0, st>>>(part, y, count, pl.split_k);
         const int nc = bits == 4 ? F4::kNC : F8::kNC;
         const int nx = bits == 4 ? F4::kNX : F8::kNX;
-        set_dispatch("path=tc_fused bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=%d launches=4 why=%s",
-                     bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, pl.split_k, pl.why);
+        set_dispatch("path=tc_fused%s bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=%d launches=%d why=%s",
+                     la ? "_lora" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, pl.split_k, la ? 5 : 4, pl.why);
         return launch_status();
     }
     using B4 = fused::PickCfg<4, true>::type;
     using B8 = fused::PickCfg<8, true>::type;
 #ifdef QL_BOUNDS_CHECK
-    if (const int v = g_ring_variant.load(); v != 0 && bits == 4 && bf16_out) {
+    if (const int v = g_ring_variant.load(); v != 0 && bits == 4 && bf16_out && !la) {
         if ((s = launch_ring_variant(v, fgrid, st, mx, mc, mp, my, p)) != QL_OK) return s;
         prof_end(st);
         set_dispatch("path=tc_fused bits=4 ring_variant=%d ctas=%d splitk=1 launches=3 why=%s", v, grid, pl.why);
         return launch_status();
     }
 #endif
+    auto b4 = la ? fused::fused_gemm_kernel<true, B4, false, false, true> : fused::fused_gemm_kernel<true, B4>;
+    auto f4 = la ? fused::fused_gemm_kernel<false, F4, false, false, true> : fused::fused_gemm_kernel<false, F4>;
+    auto b8 = la ? fused::fused_gemm_kernel<true, B8, false, false, true> : fused::fused_gemm_kernel<true, B8>;
+    auto f8 = la ? fused::fused_gemm_kernel<false, F8, false, false, true> : fused::fused_gemm_kernel<false, F8>;
     if (bits == 4) {
-        s = bf16_out ? launch_dependent(fused::fused_gemm_kernel<true, B4>, fgrid, fused::kThreads, B4::kSmemBytes, st,
-                                        mx, mc, mc, mp, my, p)
-                     : launch_dependent(fused::fused_gemm_kernel<false, F4>, fgrid, fused::kThreads, F4::kSmemBytes, st,
-                                        mx, mc, mc, mp, my, p);
+        s = bf16_out ? launch_dependent(b4, fgrid, fused::kThreads, B4::kSmemBytes, st, mx, mc, mc, mp, my, p)
+                     : launch_dependent(f4, fgrid, fused::kThreads, F4::kSmemBytes, st, mx, mc, mc, mp, my, p);
     } else {
-        s = bf16_out ? launch_dependent(fused::fused_gemm_kernel<true, B8>, fgrid, fused::kThreads, B8::kSmemBytes, st,
-                                        mx, mc, mc, mp, my, p)
-                     : launch_dependent(fused::fused_gemm_kernel<false, F8>, fgrid, fused::kThreads, F8::kSmemBytes, st,
-                                        mx, mc, mc, mp, my, p);
+        s = bf16_out ? launch_dependent(b8, fgrid, fused::kThreads, B8::kSmemBytes, st, mx, mc, mc, mp, my, p)
+                     : launch_dependent(f8, fgrid, fused::kThreads, F8::kSmemBytes, st, mx, mc, mc, mp, my, p);
     }
     if (s != QL_OK) return s;
     prof_end(st);
     const int nc = bits == 4 ? (bf16_out ? B4::kNC : F4::kNC) : (bf16_out ? B8::kNC : F8::kNC);
     const int nx = bits == 4 ? (bf16_out ? B4::kNX : F4::kNX) : (bf16_out ? B8::kNX : F8::kNX);
-    set_dispatch("path=tc_fused bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=1 launches=3 why=%s",
-                 bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, pl.why);
+    set_dispatch("path=tc_fused%s bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=1 launches=%d why=%s",
+                 la ? "_lora" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, la ? 4 : 3,
+                 pl.why);
     (void)codes;
     return launch_status();
 }
 
 ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
                      void* y, bool bf16_out, int64_t M, int64_t K, int64_t N, void* ws, cudaStream_t st,
-                     int sm_count) {
+                     int sm_count, const LoraArgs* la = nullptr, const LoraPlan* lp = nullptr) {
     const int64_t G = K / kGroup;
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     void* xp = wsb + pl.off_xp;
@@ -558,12 +668,20 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
     p.partial_elems = static_cast<int64_t>(pl.ctas) * pl.segmax * M * skinny::BW;
     // row exponents and scaled, reordered f16 activations (one cluster of CTAs per row)
     const dim3 pre_grid(static_cast<unsigned>(skinny::kPrepCluster), static_cast<unsigned>(M));
-    if (bits == 4)
+    if (la) {
+        // the adapters' first product, then the prepass beside it
+        if ((s = launch_shrink(*la, *lp, x, M, K, wsb, false, false, st)) != QL_OK) return s;
+        auto pre = bits == 4 ? skinny::skinny_prepass_kernel<4, true> : skinny::skinny_prepass_kernel<8, true>;
+        if ((s = launch_dependent(pre, pre_grid, skinny::kPrepThreads, 0, st, static_cast<const uint4*>(x),
+                                  static_cast<uint4*>(xp), rowexp, static_cast<int>(K))) != QL_OK)
+            return s;
+    } else if (bits == 4) {
         skinny::skinny_prepass_kernel<4><<<pre_grid, skinny::kPrepThreads, 0, st>>>(
             static_cast<const uint4*>(x), static_cast<uint4*>(xp), rowexp, static_cast<int>(K));
-    else
+    } else {
         skinny::skinny_prepass_kernel<8><<<pre_grid, skinny::kPrepThreads, 0, st>>>(
             static_cast<const uint4*>(x), static_cast<uint4*>(xp), rowexp, static_cast<int>(K));
+    }
     if ((s = launch_status()) != QL_OK) return s;
     prof_begin(st);
     const dim3 sgrid(static_cast<unsigned>(pl.ctas));
@@ -590,7 +708,17 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
     const float* part = p.partial;
     const int* rexp = rowexp;
     const dim3 red_grid(static_cast<unsigned>(p.num_w), static_cast<unsigned>((M + 1) / 2));
-    if (bf16_out)
+    if (la) {
+        lora::ExpandParams ep;
+        ep.b = static_cast<const __nv_bfloat16*>(la->b[0]);
+        ep.t = reinterpret_cast<const float*>(wsb + lp->off_t);
+        ep.ids = la->ids;
+        ep.r = la->r;
+        ep.L = la->L;
+        auto red = bf16_out ? lora::lora_reduce_kernel<true> : lora::lora_reduce_kernel<false>;
+        s = launch_dependent(red, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt, p.units, pl.ctas, pl.segmax,
+                             p.partial_elems, ep);
+    } else if (bf16_out)
         s = launch_dependent(skinny::skinny_reduce_kernel<true>, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt,
                              p.units, pl.ctas, pl.segmax, p.partial_elems);
     else
@@ -598,8 +726,8 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
                              p.units, pl.ctas, pl.segmax, p.partial_elems);
     if (s != QL_OK) return s;
     (void)sm_count;
-    set_dispatch("path=tc_skinny bits=%d nt=%d ctas=%d segmax=%d units=%lld launches=3 why=%s", bits, pl.nt, pl.ctas,
-                 pl.segmax, static_cast<long long>(pl.units), pl.why);
+    set_dispatch("path=tc_skinny%s bits=%d nt=%d ctas=%d segmax=%d units=%lld launches=%d why=%s", la ? "_lora" : "", bits,
+                 pl.nt, pl.ctas, pl.segmax, static_cast<long long>(pl.units), la ? 4 : 3, pl.why);
     return launch_status();
 }
 
@@ -624,7 +752,8 @@ SwigluPlan swiglu_plan(int64_t M, int64_t K, int64_t I) {
 
 ql_status run_swiglu(const SwigluPlan& pl, const void* x, const uint32_t* gc, const void* gs, const void* gb,
                      const uint32_t* uc, const void* us, const void* ub, void* h, bool bf16_out, int64_t M, int64_t K,
-                     int64_t I, void* ws, cudaStream_t st, int sm_count) {
+                     int64_t I, void* ws, cudaStream_t st, int sm_count, const LoraArgs* la = nullptr,
+                     const LoraPlan* lp = nullptr) {
     const int64_t G = K / kGroup;
     auto* base = static_cast<uint8_t*>(ws);
     auto* xh = reinterpret_cast<__half*>(base);
@@ -658,8 +787,10 @@ ql_status run_swiglu(const SwigluPlan& pl, const void* x, const uint32_t* gc, co
                                                         sb, static_cast<int>(I), static_cast<int>(G),
                                                         static_cast<int>(pl.ncols));
     if ((s = launch_status()) != QL_OK) return s;
+    if (la && (s = launch_shrink(*la, *lp, x, M, K, base, true, true, st)) != QL_OK) return s;
     if ((s = launch_convert_x(4, static_cast<const __nv_bfloat16*>(x), xh, rs, M, K, st)) != QL_OK) return s;
-    fused::Params p;
+    fused::Params p = {};
+    if (la) p.lora = lora_params(*la, *lp, base);
     p.rowscale = rs;
     p.y = h;
     p.M = static_cast<int>(M);
@@ -672,22 +803,47 @@ ql_status run_swiglu(const SwigluPlan& pl, const void* x, const uint32_t* gc, co
     const int grid = std::min(tiles, sm_count);
     const dim3 fgrid(static_cast<unsigned>(grid));
     prof_begin(st);
-    s = bf16_out ? launch_dependent(fused::fused_gemm_kernel<true, FB, true>, fgrid, fused::kThreads, FB::kSmemBytes,
-                                    st, mx, mcg, mcu, mp, my, p)
-                 : launch_dependent(fused::fused_gemm_kernel<false, FF, true>, fgrid, fused::kThreads, FF::kSmemBytes,
-                                    st, mx, mcg, mcu, mp, my, p);
+    auto kb = la ? fused::fused_gemm_kernel<true, FB, true, false, true> : fused::fused_gemm_kernel<true, FB, true>;
+    auto kf = la ? fused::fused_gemm_kernel<false, FF, true, false, true> : fused::fused_gemm_kernel<false, FF, true>;
+    s = bf16_out ? launch_dependent(kb, fgrid, fused::kThreads, FB::kSmemBytes, st, mx, mcg, mcu, mp, my, p)
+                 : launch_dependent(kf, fgrid, fused::kThreads, FF::kSmemBytes, st, mx, mcg, mcu, mp, my, p);
     if (s != QL_OK) return s;
     prof_end(st);
-    set_dispatch("path=tc_fused_swiglu bits=4 tile=%dg+%du x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d launches=3",
-                 fused::BWG, fused::BWG, fused::BT, fused::BK, bf16_out ? FB::kNX : FF::kNX,
-                 bf16_out ? FB::kNC : FF::kNC, FB::kS, fused::NA, grid);
+    set_dispatch("path=tc_fused_swiglu%s bits=4 tile=%dg+%du x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d launches=%d",
+                 la ? "_lora" : "", fused::BWG, fused::BWG, fused::BT, fused::BK, bf16_out ? FB::kNX : FF::kNX,
+                 bf16_out ? FB::kNC : FF::kNC, FB::kS, fused::NA, grid, la ? 4 : 3);
     return launch_status();
+}
+
+// Adapter arguments: ranks in steps of 8 (a 16-byte row of B), up to the shrink kernel's widest.
+ql_status check_lora(const LoraArgs& la) {
+    if (la.L < 1 || la.r < 1 || !la.ids) return QL_ERR_INVALID_ARG;
+    for (int i = 0; i < la.pairs; ++i)
+        if (!la.a[i] || !la.b[i]) return QL_ERR_INVALID_ARG;
+    if (la.r % 8 != 0 || la.r > lora::kMaxRank) return QL_ERR_UNSUPPORTED;
+    for (int i = 0; i < la.pairs; ++i)
+        if (!aligned16(la.a[i]) || !aligned16(la.b[i])) return QL_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(la.ids) & 3u) != 0 || (reinterpret_cast<uintptr_t>(la.scale) & 3u) != 0)
+        return QL_ERR_ALIGNMENT;
+    return QL_OK;
+}
+
+// Whether [p, p + n) meets any adapter tensor.
+bool lora_overlaps(const LoraArgs& la, int64_t M, int64_t K, int64_t N, const void* p, size_t n) {
+    for (int i = 0; i < la.pairs; ++i)
+        if (overlap(p, n, la.a[i], static_cast<size_t>(la.L) * la.r * K * 2) ||
+            overlap(p, n, la.b[i], static_cast<size_t>(la.L) * la.r * N * 2))
+            return true;
+    return overlap(p, n, la.ids, static_cast<size_t>(M) * 4) ||
+           (la.scale && overlap(p, n, la.scale, static_cast<size_t>(la.L) * 4));
 }
 
 ql_status swiglu_impl(const void* x, const uint32_t* gc, const void* gs, const void* gb, const uint32_t* uc,
                       const void* us, const void* ub, void* h, ql_dtype out_dtype, int64_t M, int64_t K, int64_t I,
-                      int32_t group, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+                      int32_t group, void* workspace, size_t workspace_bytes, cudaStream_t stream,
+                      const LoraArgs* la = nullptr) {
     ql_status s = check_shape(M, K, I, group);
+    if (s == QL_OK && la) s = check_lora(*la);
     if (s != QL_OK) return s;
     if (!x || !gc || !gs || !gb || !uc || !us || !ub || !h) return QL_ERR_INVALID_ARG;
     if (out_dtype != QL_BF16 && out_dtype != QL_F32) return QL_ERR_INVALID_ARG;
@@ -701,22 +857,33 @@ ql_status swiglu_impl(const void* x, const uint32_t* gc, const void* gs, const v
     const size_t in_bytes[7] = {xb, cb, pb, pb, cb, pb, pb};
     for (int i = 0; i < 7; ++i)
         if (overlap(h, hb, in[i], in_bytes[i])) return QL_ERR_INVALID_ARG;
+    if (la && lora_overlaps(*la, M, K, I, h, hb)) return QL_ERR_INVALID_ARG;
     const SwigluPlan pl = swiglu_plan(M, K, I);
-    if (!workspace || workspace_bytes < pl.workspace) return QL_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
-    if (overlap(workspace, pl.workspace, h, hb)) return QL_ERR_INVALID_ARG;
-    for (int i = 0; i < 7; ++i)
-        if (overlap(workspace, pl.workspace, in[i], in_bytes[i])) return QL_ERR_INVALID_ARG;
     DeviceInfo* dev = nullptr;
+    LoraPlan lp;
+    size_t need = pl.workspace;
+    if (la) {
+        if ((s = device_info(&dev)) != QL_OK) return s;
+        lp = lora_plan(M, K, la->r, la->L, 2, true, pl.workspace, dev->sm_count);
+        need = lp.workspace;
+    }
+    if (!workspace || workspace_bytes < need) return QL_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
+    if (overlap(workspace, need, h, hb)) return QL_ERR_INVALID_ARG;
+    for (int i = 0; i < 7; ++i)
+        if (overlap(workspace, need, in[i], in_bytes[i])) return QL_ERR_INVALID_ARG;
+    if (la && lora_overlaps(*la, M, K, I, workspace, need)) return QL_ERR_INVALID_ARG;
     if ((s = device_info(&dev)) != QL_OK) return s;
     return run_swiglu(pl, x, gc, gs, gb, uc, us, ub, h, out_dtype == QL_BF16, M, K, I, workspace, stream,
-                      dev->sm_count);
+                      dev->sm_count, la, &lp);
 }
 
 ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales, const void* biases, void* y,
                        ql_dtype out_dtype, int64_t M, int64_t K, int64_t N, int32_t group, int32_t path,
-                       int32_t split_k, void* workspace, size_t workspace_bytes, cudaStream_t stream, int bits) {
+                       int32_t split_k, void* workspace, size_t workspace_bytes, cudaStream_t stream, int bits,
+                       const LoraArgs* la = nullptr) {
     ql_status s = check_shape(M, K, N, group);
+    if (s == QL_OK && la) s = check_lora(*la);
     if (s != QL_OK) return s;
     if (!x || !codes || !scales || !biases || !y) return QL_ERR_INVALID_ARG;
     if (out_dtype != QL_BF16 && out_dtype != QL_F32) return QL_ERR_INVALID_ARG;
@@ -729,24 +896,53 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
                  yb = static_cast<size_t>(M) * N * (out_dtype == QL_BF16 ? 2 : 4);
     if (overlap(y, yb, x, xb) || overlap(y, yb, codes, cb) || overlap(y, yb, scales, pb) || overlap(y, yb, biases, pb))
         return QL_ERR_INVALID_ARG;
+    if (la && lora_overlaps(*la, M, K, N, y, yb)) return QL_ERR_INVALID_ARG;
     DeviceInfo* dev = nullptr;
     if ((s = device_info(&dev)) != QL_OK) return s;
     Plan pl;
     if ((s = make_plan(M, K, N, path, split_k, dev->sm_count, bits, &pl)) != QL_OK) return s;
-    if (pl.workspace > 0) {
-        if (!workspace || workspace_bytes < pl.workspace) return QL_ERR_WORKSPACE;
+    LoraPlan lp;
+    size_t need = pl.workspace;
+    if (la) {
+        lp = lora_plan(M, K, la->r, la->L, 1, pl.path == QL_PATH_TC_FUSED, pl.workspace, dev->sm_count);
+        need = lp.workspace;
+    }
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return QL_ERR_WORKSPACE;
         if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
-        if (overlap(workspace, pl.workspace, x, xb) || overlap(workspace, pl.workspace, y, yb) ||
-            overlap(workspace, pl.workspace, codes, cb) || overlap(workspace, pl.workspace, scales, pb) ||
-            overlap(workspace, pl.workspace, biases, pb))
+        if (overlap(workspace, need, x, xb) || overlap(workspace, need, y, yb) ||
+            overlap(workspace, need, codes, cb) || overlap(workspace, need, scales, pb) ||
+            overlap(workspace, need, biases, pb) || (la && lora_overlaps(*la, M, K, N, workspace, need)))
             return QL_ERR_INVALID_ARG;
     }
     const bool bf16 = out_dtype == QL_BF16;
     if (pl.path == QL_PATH_GEMV)
         return run_gemv(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count);
     if (pl.path == QL_PATH_TC_SKINNY)
-        return run_skinny(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count);
-    return run_fused(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count);
+        return run_skinny(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count, la, &lp);
+    return run_fused(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count, la, &lp);
+}
+
+LoraArgs lora_args(const void* a, const void* b, const float* scale, const int32_t* ids, int32_t L, int32_t r) {
+    LoraArgs la;
+    la.a[0] = a;
+    la.b[0] = b;
+    la.scale = scale;
+    la.ids = ids;
+    la.L = L;
+    la.r = r;
+    return la;
+}
+
+size_t lora_workspace_impl(int64_t M, int64_t K, int64_t N, int32_t group, int32_t L, int32_t r, int bits) {
+    if (check_shape(M, K, N, group) != QL_OK || L < 1 || r < 8 || r % 8 != 0 || r > lora::kMaxRank)
+        return static_cast<size_t>(-1);
+    DeviceInfo* dev = nullptr;
+    int sms = 148;
+    if (device_info(&dev) == QL_OK) sms = dev->sm_count;
+    Plan pl;
+    if (make_plan(M, K, N, QL_PATH_AUTO, 0, sms, bits, &pl) != QL_OK) return static_cast<size_t>(-1);
+    return lora_plan(M, K, r, L, 1, pl.path == QL_PATH_TC_FUSED, pl.workspace, sms).workspace;
 }
 
 size_t workspace_impl(int64_t M, int64_t K, int64_t N, int32_t group, int32_t path, int32_t split_k, int bits) {
@@ -826,6 +1022,115 @@ ql_status pack_impl(const float* w, const float* imatrix, int64_t K, int64_t N, 
         pack_rtn_kernel<<<blocks, 256, 0, stream>>>(w, codes, static_cast<__half*>(scales),
                                                     static_cast<__half*>(biases), groups);
     return launch_status();
+}
+
+// ------------------------------------------------------------------ norms around a block
+
+// Threads and 8-element vectors per thread of a CTA-per-row launch.  Many rows: two vectors per thread, so that
+// more rows are in flight on an SM; a few rows: one, which leaves each thread less to do in a row.
+struct NormShape {
+    int vpt, threads;
+};
+NormShape norm_shape(int64_t M, int64_t D, int sm_count) {
+    const int nv = static_cast<int>(D / 8);
+    int vpt = M > 2 * sm_count ? 2 : 1;
+    while (vpt < 4 && nv > 1024 * vpt) vpt *= 2;
+    const int per = (nv + vpt - 1) / vpt;
+    return {vpt, (per + 31) / 32 * 32};
+}
+
+template <bool kXF32, int kY>
+ql_status launch_norm(const norm::Params& p, int sm_count, cudaStream_t st) {
+    if (p.D <= norm::kWarpRowMax) {
+        const dim3 grid(static_cast<unsigned>((p.M + norm::kWarpRows - 1) / norm::kWarpRows));
+        const int nv = p.D / 8;
+        if (nv <= 32)
+            norm::norm_residual_kernel<kXF32, kY, 1, true><<<grid, 32 * norm::kWarpRows, 0, st>>>(p);
+        else if (nv <= 64)
+            norm::norm_residual_kernel<kXF32, kY, 2, true><<<grid, 32 * norm::kWarpRows, 0, st>>>(p);
+        else
+            norm::norm_residual_kernel<kXF32, kY, 4, true><<<grid, 32 * norm::kWarpRows, 0, st>>>(p);
+        return launch_status();
+    }
+    const NormShape ns = norm_shape(p.M, p.D, sm_count);
+    const dim3 grid(static_cast<unsigned>(p.M));
+    if (ns.vpt == 1)
+        norm::norm_residual_kernel<kXF32, kY, 1, false><<<grid, ns.threads, 0, st>>>(p);
+    else if (ns.vpt == 2)
+        norm::norm_residual_kernel<kXF32, kY, 2, false><<<grid, ns.threads, 0, st>>>(p);
+    else
+        norm::norm_residual_kernel<kXF32, kY, 4, false><<<grid, ns.threads, 0, st>>>(p);
+    return launch_status();
+}
+
+size_t dtype_bytes(ql_dtype t) { return t == QL_BF16 ? 2 : 4; }
+bool dtype_ok(ql_dtype t) { return t == QL_BF16 || t == QL_F32; }
+
+ql_status norm_residual_impl(const void* x, ql_dtype x_dtype, const void* y, ql_dtype y_dtype, int32_t S,
+                             int32_t post_norm, const void* post_weight, const void* gate, float residual_scale,
+                             float branch_scale, const void* pre_weight, const void* scale, const void* shift,
+                             ql_dtype param_dtype, const int32_t* segment_ids, int32_t T, float eps, void* out, void* h,
+                             int64_t M, int64_t D, cudaStream_t stream) {
+    if (M < 1 || D < 8 || D % 8 != 0 || T < 1 || M > (1ll << 31) - 1) return QL_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || eps > 3.4028235e38f) return QL_ERR_INVALID_ARG;
+    if (!x || !dtype_ok(x_dtype) || !dtype_ok(param_dtype)) return QL_ERR_INVALID_ARG;
+    if (!h && (pre_weight || scale || shift)) return QL_ERR_INVALID_ARG;
+    if (y) {
+        if (!out || !dtype_ok(y_dtype) || S < 1 || (y_dtype == QL_BF16 && S != 1)) return QL_ERR_INVALID_ARG;
+        if (post_weight && !post_norm) return QL_ERR_INVALID_ARG;
+    } else {
+        if (out || !h) return QL_ERR_INVALID_ARG;
+        S = 1;
+        post_weight = gate = nullptr;
+    }
+    if (D > QL_NORM_MAX_D) return QL_ERR_UNSUPPORTED;
+    static_assert(QL_NORM_MAX_D == norm::kMaxD, "the documented limit is the kernel's");
+    const size_t md = static_cast<size_t>(M) * D, vb = static_cast<size_t>(D) * dtype_bytes(param_dtype);
+    const void* in[8] = {x, y, post_weight, gate, pre_weight, scale, shift, segment_ids};
+    const size_t in_bytes[8] = {md * dtype_bytes(x_dtype), y ? md * S * dtype_bytes(y_dtype) : 0, vb, vb * T, vb,
+                                vb * T, vb * T, static_cast<size_t>(M) * 4};
+    for (int i = 0; i < 7; ++i)
+        if (!aligned16(in[i])) return QL_ERR_ALIGNMENT;
+    if (!aligned16(out) || !aligned16(h) || (reinterpret_cast<uintptr_t>(segment_ids) & 3u) != 0) return QL_ERR_ALIGNMENT;
+    const size_t ob = out ? md * dtype_bytes(x_dtype) : 0, hb = h ? md * 2 : 0;
+    for (int i = 0; i < 8; ++i) {
+        if (!in[i]) continue;
+        if (overlap(h, hb, in[i], in_bytes[i])) return QL_ERR_INVALID_ARG;
+        if (overlap(out, ob, in[i], in_bytes[i]) && !(i == 0 && out == x)) return QL_ERR_INVALID_ARG;
+    }
+    if (overlap(out, ob, h, hb)) return QL_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    ql_status s;
+    if ((s = device_info(&dev)) != QL_OK) return s;
+    norm::Params p;
+    p.x = x;
+    p.y = y;
+    p.r = out;
+    p.h = static_cast<__nv_bfloat16*>(h);
+    p.post_weight = post_weight;
+    p.gate = gate;
+    p.pre_weight = pre_weight;
+    p.scale = scale;
+    p.shift = shift;
+    p.seg = segment_ids;
+    p.M = M;
+    p.D = static_cast<int>(D);
+    p.S = S;
+    p.T = T;
+    p.params_f32 = param_dtype == QL_F32;
+    p.post_norm = post_norm != 0;
+    p.residual_scale = residual_scale;
+    p.branch_scale = branch_scale;
+    p.eps = eps;
+    const int sm = dev->sm_count;
+    if (x_dtype == QL_F32) {
+        if (!y) return launch_norm<true, norm::kYNone>(p, sm, stream);
+        return y_dtype == QL_F32 ? launch_norm<true, norm::kYF32>(p, sm, stream)
+                                 : launch_norm<true, norm::kYBf16>(p, sm, stream);
+    }
+    if (!y) return launch_norm<false, norm::kYNone>(p, sm, stream);
+    return y_dtype == QL_F32 ? launch_norm<false, norm::kYF32>(p, sm, stream)
+                             : launch_norm<false, norm::kYBf16>(p, sm, stream);
 }
 
 }  // namespace
@@ -935,6 +1240,67 @@ ql_status qlinear_reduce_partials(const float* partials, int32_t S, int64_t coun
     else
         ordered_sum_kernel<false><<<blocks, 256, 0, stream>>>(partials, y, count, S);
     return launch_status();
+}
+
+size_t qlinear_lora_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group, int32_t L, int32_t r) {
+    return lora_workspace_impl(M, K, N, group, L, r, 4);
+}
+
+ql_status qlinear_lora_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
+                               const void* lora_a, const void* lora_b, const float* lora_scale,
+                               const int32_t* adapter_ids, void* y, ql_dtype out_dtype, int64_t M, int64_t K, int64_t N,
+                               int32_t group, int32_t L, int32_t r, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
+    const LoraArgs la = lora_args(lora_a, lora_b, lora_scale, adapter_ids, L, r);
+    return forward_impl(x, codes, scales, biases, y, out_dtype, M, K, N, group, QL_PATH_AUTO, 0, workspace,
+                        workspace_bytes, stream, 4, &la);
+}
+
+size_t qlinear8_lora_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group, int32_t L, int32_t r) {
+    return lora_workspace_impl(M, K, N, group, L, r, 8);
+}
+
+ql_status qlinear8_lora_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
+                                const void* lora_a, const void* lora_b, const float* lora_scale,
+                                const int32_t* adapter_ids, void* y, ql_dtype out_dtype, int64_t M, int64_t K,
+                                int64_t N, int32_t group, int32_t L, int32_t r, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+    const LoraArgs la = lora_args(lora_a, lora_b, lora_scale, adapter_ids, L, r);
+    return forward_impl(x, codes, scales, biases, y, out_dtype, M, K, N, group, QL_PATH_AUTO, 0, workspace,
+                        workspace_bytes, stream, 8, &la);
+}
+
+size_t qlinear_swiglu_lora_workspace_size(int64_t M, int64_t K, int64_t I, int32_t group, int32_t L, int32_t r) {
+    if (check_shape(M, K, I, group) != QL_OK || L < 1 || r < 8 || r % 8 != 0 || r > lora::kMaxRank)
+        return static_cast<size_t>(-1);
+    DeviceInfo* dev = nullptr;
+    int sms = 148;
+    if (device_info(&dev) == QL_OK) sms = dev->sm_count;
+    return lora_plan(M, K, r, L, 2, true, swiglu_plan(M, K, I).workspace, sms).workspace;
+}
+
+ql_status qlinear_swiglu_lora_forward(const void* x, const uint32_t* gate_codes, const void* gate_scales,
+                                      const void* gate_biases, const uint32_t* up_codes, const void* up_scales,
+                                      const void* up_biases, const void* gate_lora_a, const void* gate_lora_b,
+                                      const void* up_lora_a, const void* up_lora_b, const float* lora_scale,
+                                      const int32_t* adapter_ids, void* h, ql_dtype out_dtype, int64_t M, int64_t K,
+                                      int64_t I, int32_t group, int32_t L, int32_t r, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+    LoraArgs la = lora_args(gate_lora_a, gate_lora_b, lora_scale, adapter_ids, L, r);
+    la.a[1] = up_lora_a;
+    la.b[1] = up_lora_b;
+    la.pairs = 2;
+    return swiglu_impl(x, gate_codes, gate_scales, gate_biases, up_codes, up_scales, up_biases, h, out_dtype, M, K, I,
+                       group, workspace, workspace_bytes, stream, &la);
+}
+
+ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const void* y, ql_dtype y_dtype, int32_t S,
+                                int32_t post_norm, const void* post_weight, const void* gate, float residual_scale,
+                                float branch_scale, const void* pre_weight, const void* scale, const void* shift,
+                                ql_dtype param_dtype, const int32_t* segment_ids, int32_t T, float eps, void* out,
+                                void* h, int64_t M, int64_t D, cudaStream_t stream) {
+    return norm_residual_impl(x, x_dtype, y, y_dtype, S, post_norm, post_weight, gate, residual_scale, branch_scale,
+                              pre_weight, scale, shift, param_dtype, segment_ids, T, eps, out, h, M, D, stream);
 }
 
 size_t qlinear_swiglu_workspace_size(int64_t M, int64_t K, int64_t I, int32_t group) {

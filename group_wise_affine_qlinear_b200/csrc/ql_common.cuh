@@ -90,6 +90,18 @@ __device__ __forceinline__ __half2 half2_of(uint32_t u) { return *reinterpret_ca
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
+// Two bf16 with a non-finite one replaced by zero and recorded (entries of an adapter's up projection: on the
+// fused path one would reach the rows of other adapters through 0 * inf, so no path lets it in).
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+    const bool lo = (v & 0x00007F80u) == 0x00007F80u, hi = (v & 0x7F800000u) == 0x7F800000u;
+    if (lo || hi) {
+        record_status(QL_ERR_INVALID_ARG);
+        if (lo) v &= 0xFFFF0000u;
+        if (hi) v &= 0x0000FFFFu;
+    }
+    return v;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);

@@ -1,0 +1,268 @@
+// Low-rank adapters of many requests beside a packed projection.
+//
+//   t[m][j] = s_a sum_k x[m][k] A[a][j][k]            a = ids[m], the adapter of row m
+//   y[m][n] = sum_k x[m][k] W[n][k] + sum_j t[m][j] B[a][n][j]
+//
+// A is bf16 [L][r][K], B bf16 [L][N][r], s fp32 [L]; a row with a negative id has no adapter.
+//
+// The first product ("shrink") reads every activation once more and the adapters in use; it is bound by that
+// traffic, so it runs on mma.sync straight from global memory (this file).  The second ("expand") never makes a pass
+// over y of its own: the weight-streaming path adds it in fp32 where it sums its partials (lora_reduce_kernel), and
+// the fused path appends it to the tile's K loop (ql_tc_fused.cuh), so y is rounded once.
+#pragma once
+
+#include "ql_ptx.cuh"
+#include "ql_tc_fused.cuh"
+#include "ql_tc_skinny.cuh"
+
+namespace ql {
+namespace lora {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 16;              // rows of one shrink tile (MMA M)
+constexpr int kMaxRank = 128;
+constexpr int kMaxSplit = 8;           // CTAs of a cluster that share a tile's K range
+
+struct ShrinkParams {
+    const __nv_bfloat16* x;      // [M][K]
+    const __nv_bfloat16* a[2];   // [L][r][K]; the second one of a gate/up pair
+    const float* scale;          // [L] or null (1)
+    const int* ids;              // [M]
+    float* t;                    // [pair][M][r]
+    int M, K, r, L;
+    int tiles;                   // ceil(M / 16)
+    int passes;                  // CTAs that share a tile's distinct adapters
+    int chunks;                  // CTAs along the rank: ceil(r / (8 NT))
+    // the fused path's plan (null on the weight-streaming path)
+    int* row_slot;               // [M] position of the row's adapter in its token tile's list, or -1
+    int* tile_count;             // [num_t] distinct adapters of the token tile
+    int* tile_list;              // [num_t][BT] those adapters, in order of first use
+    int num_t;
+};
+
+// D (16 x 8, fp32) += A (16 x 16, bf16) . B (16 x 8, bf16)
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The adapter of row m, -1 for none; an id outside [-1, L) is recorded and counts as none.
+__device__ __forceinline__ int adapter_of(const int* ids, int m, int L) {
+    const int a = ids[m];
+    if (a >= -1 && a < L) return a;
+    record_status(QL_ERR_INVALID_ARG);
+    return -1;
+}
+
+// One token tile of the fused kernel: its distinct adapters in order of first use, and each row's place among them.
+__device__ __forceinline__ void plan_tile(const ShrinkParams& p, int t_blk) {
+    constexpr int BT = fused::BT;
+    static_assert(BT <= kThreads, "one thread per token of a tile");
+    __shared__ int id[BT];
+    __shared__ int warp_first[kWarps];
+    const int i = threadIdx.x;
+    const int m = t_blk * BT + i;
+    const int rows = min(BT, p.M - t_blk * BT);
+    const int mine = i < rows ? adapter_of(p.ids, m, p.L) : -1;
+    if (i < BT) id[i] = mine;
+    __syncthreads();
+    int first = i;                                 // the tile's first row with this adapter
+    if (mine >= 0)
+        for (int j = 0; j < i; ++j)
+            if (id[j] == mine) { first = j; break; }
+    const bool leads = mine >= 0 && first == i;
+    const uint32_t bal = __ballot_sync(0xFFFFFFFFu, leads);
+    if ((i & 31) == 0) warp_first[i >> 5] = __popc(bal);
+    __syncthreads();
+    int place = __popc(bal & ((1u << (i & 31)) - 1u)), total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < (i >> 5)) place += warp_first[w];
+        total += warp_first[w];
+    }
+    __syncthreads();
+    if (leads) {
+        p.tile_list[t_blk * BT + place] = mine;
+        id[i] = place;                             // only this row's entry: others read id[first] below
+    }
+    __syncthreads();
+    if (i < rows) p.row_slot[m] = mine >= 0 ? id[first] : -1;
+    if (i == 0) p.tile_count[t_blk] = total;
+}
+
+// t for 16 rows.  grid: (tiles * passes + num_t, S, chunks * pair), cluster (1, S, 1).
+//
+// Each warp multiplies its share of the K range, 32 columns at a time: a lane's 16-byte loads are 8 consecutive k of
+// two activation rows and of one adapter row per n-tile, which feed two MMAs; the MMA's k order is whatever the lanes
+// hold, the same for both operands, so a dot product keeps its terms.  The warps' sums meet in shared memory, the
+// cluster's CTAs' in distributed shared memory, each added in a fixed order.
+//
+// Rows of a tile with other adapters are multiplied too and not written: a tile makes one pass per distinct adapter,
+// and its passes are spread over `passes` CTAs.
+template <int NT>
+__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkParams p) {
+    ptx::launch_dependents();
+    __shared__ float part[kWarps][kTile * NT * 8];         // [row][rank] per warp
+    const int S = static_cast<int>(gridDim.y);
+    const int rank = static_cast<int>(blockIdx.y);             // rank in the cluster (1, S, 1)
+    const int shrink_ctas = p.tiles * p.passes;
+    if (static_cast<int>(blockIdx.x) >= shrink_ctas) {
+        if (blockIdx.y == 0 && blockIdx.z == 0) plan_tile(p, static_cast<int>(blockIdx.x) - shrink_ctas);
+    } else {
+        const int tile = static_cast<int>(blockIdx.x) / p.passes, pass = static_cast<int>(blockIdx.x) % p.passes;
+        const int pair = static_cast<int>(blockIdx.z) / p.chunks, chunk = static_cast<int>(blockIdx.z) % p.chunks;
+        const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+        const int m0 = tile * kTile;
+        const int j0 = chunk * NT * 8;
+        const int mine = lane < kTile && m0 + lane < p.M ? adapter_of(p.ids, m0 + lane, p.L) : -1;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, mine);
+        uint32_t leaders = __ballot_sync(0xFFFFFFFFu, mine >= 0 && (__ffs(same) - 1) == lane);
+        const int kb_all = p.K / 32;
+        const int kb0 = static_cast<int>(static_cast<int64_t>(kb_all) * rank / S);
+        const int kb1 = static_cast<int>(static_cast<int64_t>(kb_all) * (rank + 1) / S);
+        const int g = lane >> 2, c = lane & 3;
+        // rows past M repeat the last one; their results are not written
+        const int64_t row0 = min(m0 + g, p.M - 1), row1 = min(m0 + g + 8, p.M - 1);
+        const uint4* x0 = reinterpret_cast<const uint4*>(p.x + row0 * p.K) + c;
+        const uint4* x1 = reinterpret_cast<const uint4*>(p.x + row1 * p.K) + c;
+        for (int n = 0; leaders != 0; ++n, leaders &= leaders - 1) {
+            if (n % p.passes != pass) continue;
+            const int adapter = __shfl_sync(0xFFFFFFFFu, mine, __ffs(leaders) - 1);
+            const __nv_bfloat16* a = (pair == 0 ? p.a[0] : p.a[1]) + (static_cast<int64_t>(adapter) * p.r + j0) * p.K;
+            float acc[NT][4];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+            constexpr int U = NT <= 2 ? 4 : 2;                 // column blocks in flight per warp
+            for (int kb = kb0 + warp; kb < kb1; kb += kWarps * U) {
+                uint4 vx0[U], vx1[U], va[U][NT];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int b = kb + u * kWarps;
+                    const bool in = b < kb1;
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                    vx0[u] = in ? __ldg(x0 + 4 * b) : zero;
+                    vx1[u] = in ? __ldg(x1 + 4 * b) : zero;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const bool use = in && j0 + 8 * i < p.r;
+                        va[u][i] = use ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<int64_t>(8 * i + g) * p.K) + c +
+                                               4 * b)
+                                       : zero;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        mma_bf16_16816(acc[i], vx0[u].x, vx1[u].x, vx0[u].y, vx1[u].y, va[u][i].x, va[u][i].y);
+                        mma_bf16_16816(acc[i], vx0[u].z, vx1[u].z, vx0[u].w, vx1[u].w, va[u][i].z, va[u][i].w);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int at = g * NT * 8 + 8 * i + 2 * c;
+                part[warp][at] = acc[i][0];
+                part[warp][at + 1] = acc[i][1];
+                part[warp][at + 8 * NT * 8] = acc[i][2];
+                part[warp][at + 8 * NT * 8 + 1] = acc[i][3];
+            }
+            __syncthreads();
+            for (int e = threadIdx.x; e < kTile * NT * 8; e += kThreads) {
+                float s = part[0][e];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) s += part[w][e];
+                part[0][e] = s;                             // this CTA's slice of the sum
+            }
+            if (S > 1) ptx::cluster_sync(); else __syncthreads();
+            // every CTA of the cluster finishes its share of the tile's sums
+            for (int e = threadIdx.x + rank * kThreads; e < kTile * NT * 8; e += S * kThreads) {
+                float s;
+                if (S > 1) {
+                    s = 0.0f;
+                    for (int q = 0; q < S; ++q) s += ptx::ld_shared_cluster_f32(&part[0][e], static_cast<uint32_t>(q));
+                } else {
+                    s = part[0][e];
+                }
+                const int row = e / (NT * 8), j = j0 + e % (NT * 8);
+                const int m = m0 + row;
+                if (m < p.M && j < p.r && p.ids[m] == adapter)
+                    p.t[(static_cast<int64_t>(pair) * p.M + m) * p.r + j] =
+                        s * (p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f);
+            }
+            if (S > 1) ptx::cluster_sync(); else __syncthreads();      // the sums are read before the next pass
+        }
+    }
+    // Launched behind the parameter transpose under programmatic dependent launch; as with the conversion that
+    // follows, the last CTA waits for the kernel before, so that this kernel's completion implies both.
+    if (blockIdx.x == gridDim.x - 1) ptx::grid_dependency_wait();
+}
+
+// y[t][n] = 2^rowexp[t] * (sum of the stream-K partials, as skinny_reduce_kernel) + sum_j tl[t][j] B[a][n][j],
+// the second sum in fp32 from the bf16 adapter, rounded once.  One CTA per (128-column tile, 2 tokens); a thread's
+// first kEager chunks of B are loaded before the wait for the partials.
+struct ExpandParams {
+    const __nv_bfloat16* b;      // [L][N][r]
+    const float* t;              // [M][r]
+    const int* ids;              // [M]
+    int r, L;
+};
+
+template <bool kBf16Out>
+__global__ void __launch_bounds__(256) lora_reduce_kernel(const float* __restrict__ partial,
+                                                          const int* __restrict__ rowexp, void* __restrict__ y, int M,
+                                                          int N, int cpt, int64_t units, int P, int segmax,
+                                                          int64_t partial_elems, const ExpandParams ep) {
+    __shared__ int64_t seg_base[skinny::kMaxCtas];
+    __shared__ int count;
+    constexpr int kEager = 4;
+    const int w = blockIdx.x;
+    const int t = blockIdx.y * 2 + (threadIdx.x >> 7), n = w * skinny::BW + (threadIdx.x & 127);
+    const bool live = t < M && n < N;
+    if (threadIdx.x == 0) count = skinny::list_segments(w, cpt, units, P, segmax, seg_base);
+    const int a = live ? ep.ids[t] : -1;
+    const bool with = a >= 0 && a < ep.L;                         // the shrink kernel records an id out of range
+    const int chunks = with ? ep.r / 8 : 0;
+    const uint4* b = reinterpret_cast<const uint4*>(ep.b + (static_cast<int64_t>(with ? a : 0) * N + (live ? n : 0)) * ep.r);
+    uint4 eager[kEager];
+#pragma unroll
+    for (int i = 0; i < kEager; ++i) eager[i] = i < chunks ? __ldg(b + i) : make_uint4(0u, 0u, 0u, 0u);
+    ptx::grid_dependency_wait();                                  // partials and t come from the kernels before
+    __syncthreads();
+    if (!live) return;
+    float acc = skinny::sum_segments(partial, partial_elems, seg_base, count, M, t, threadIdx.x & 127);
+    acc = ldexpf(acc, rowexp[t]);
+    const float4* tl = reinterpret_cast<const float4*>(ep.t + static_cast<int64_t>(t) * ep.r);
+    float delta = 0.0f;
+    auto add = [&](const uint4 v, int i) {
+        const float4 t0 = tl[2 * i], t1 = tl[2 * i + 1];
+        const uint32_t q[4] = {finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w)};
+        delta = fmaf(t0.x, bf16_lo(q[0]), delta);
+        delta = fmaf(t0.y, bf16_hi(q[0]), delta);
+        delta = fmaf(t0.z, bf16_lo(q[1]), delta);
+        delta = fmaf(t0.w, bf16_hi(q[1]), delta);
+        delta = fmaf(t1.x, bf16_lo(q[2]), delta);
+        delta = fmaf(t1.y, bf16_hi(q[2]), delta);
+        delta = fmaf(t1.z, bf16_lo(q[3]), delta);
+        delta = fmaf(t1.w, bf16_hi(q[3]), delta);
+    };
+#pragma unroll
+    for (int i = 0; i < kEager; ++i)
+        if (i < chunks) add(eager[i], i);
+    for (int i = kEager; i < chunks; ++i) add(__ldg(b + i), i);
+    acc += delta;
+    const int64_t e = static_cast<int64_t>(t) * N + n;
+    if constexpr (kBf16Out) {
+        reinterpret_cast<__nv_bfloat16*>(y)[e] = __float2bfloat16_rn(acc);
+    } else {
+        reinterpret_cast<float*>(y)[e] = acc;
+    }
+}
+
+}  // namespace lora
+}  // namespace ql

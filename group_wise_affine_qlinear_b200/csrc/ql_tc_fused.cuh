@@ -60,6 +60,17 @@
 // the 8 epilogue warps reads both for its lane quarter and half of the tokens and
 // writes h = silu(g) * u = g / (1 + e^-g) * u in fp32 (the exponential and the
 // division through the SFU's exp2 and reciprocal), rounded once.
+//
+// Adapter mode (kLora): y += sum_j t[m][j] B[a][n][j] for the low-rank adapter a of every row m, t = s x . A^T (an
+// earlier kernel).  The product is more K for the same accumulators: after the G quantization groups the unit that
+// owns the end of K runs extra K-steps whose weight operand is B itself (bf16, bit for bit) and whose activation
+// operand is t, scaled like the row's activations and cut into two bf16, t = hi + lo to 2^-16 relative, one column
+// each (the MMA's type is per instruction: these steps run in bf16, whose exponents cannot overflow where f16's
+// could).  A rank-r adapter thus takes 2r columns; a tile's distinct adapters lie side by side in those columns, and a
+// token's row is zero outside its own adapter's, so a tile pays for the adapters in it (one 64-column step per four
+// of rank 8, per one of rank 32) and nothing travels through memory: no pass over y, and y is rounded once.
+// In SwiGLU mode an adapter has 4r columns, the gate's hi and lo and the up's hi and lo; each row group's weight
+// operand is zero under the other's.
 #pragma once
 
 #include "ql_ptx.cuh"
@@ -129,12 +140,24 @@ template <> struct PickCfg<4, false> { using type = Cfg<4, 2, 4, 4, 1>; };
 template <> struct PickCfg<8, true> { using type = Cfg<5, 2, 8, 2, 2>; };
 template <> struct PickCfg<8, false> { using type = Cfg<4, 2, 8, 4, 1>; };
 
+// Adapter mode: operands of the extra K-steps (b[1] and the second half of t are the up projection's).
+struct LoraParams {
+    const __nv_bfloat16* b[2];   // [L][N][r]
+    const float* t;              // [pair][M][r], scaled by the adapter's factor
+    const int* row_slot;         // [M] place of the row's adapter in its token tile's list, or -1
+    const int* tile_count;       // [num_t] distinct adapters of the token tile
+    const int* tile_list;        // [num_t][BT]
+    int r;
+    int chunks;                  // 8-column chunks per adapter: 2r / 8, in SwiGLU mode 4r / 8
+};
+
 struct Params {
     float* rowscale;      // [M] 2^e_m
     void* y;              // [M][N] bf16 or fp32
     int M, N, G;
     int num_t, num_w;     // token tiles, weight tiles
     int splits;           // K slices per tile (split-K instantiations; 1 otherwise)
+    LoraParams lora;      // adapter mode only
 };
 
 __device__ __forceinline__ void tile_coords(int t, int num_w, int& t_blk, int& w_blk) {
@@ -151,11 +174,20 @@ __device__ __forceinline__ void ring_pos(uint32_t i, int& stage, uint32_t& phase
     phase = (i / N) & 1u;
 }
 
+// Two f32 as two bf16 pairs with hi + lo = v to 2^-16 relative: hi is v cut to bf16, lo the rest rounded.  A
+// non-finite v stays in hi (lo 0), so it reaches the outputs of its own row as itself.
+__device__ __forceinline__ uint32_t bf16_part(float v0, float v1, bool lo) {
+    const uint32_t u0 = __float_as_uint(v0), u1 = __float_as_uint(v1);
+    const bool f0 = (u0 & 0x7F800000u) != 0x7F800000u, f1 = (u1 & 0x7F800000u) != 0x7F800000u;
+    const float h0 = f0 ? __uint_as_float(u0 & 0xFFFF0000u) : v0, h1 = f1 ? __uint_as_float(u1 & 0xFFFF0000u) : v1;
+    return lo ? pack_bf16x2(f0 ? v0 - h0 : 0.0f, f1 ? v1 - h1 : 0.0f) : pack_bf16x2(h0, h1);
+}
+
 // map_codes2: the up weight's codes in SwiGLU mode (128-row boxes, like map_codes there); unused otherwise.
 // kSplitK: every tile's K-steps are cut into p.splits slices, each its own work unit; a unit writes the
 // fp32 partial of its slice through map_y, a 3-D map over partials [splits][M][N], and a separate
 // reduction sums the slices in order (for shapes with fewer tiles than SMs).
-template <bool kBf16Out, class C, bool kSwiGLU = false, bool kSplitK = false>
+template <bool kBf16Out, class C, bool kSwiGLU = false, bool kSplitK = false, bool kLora = false>
 __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_codes,
     const __grid_constant__ CUtensorMap map_codes2, const __grid_constant__ CUtensorMap map_params,
@@ -195,6 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
             kb0 = 0;
             kb1 = p.G;
         }
+    };
+    // Adapter mode: 8-column chunks of a unit's extra K-steps (0 unless the unit ends K), 8 chunks to a step.
+    auto lora_chunks = [&](int t_blk, int kb1) {
+        return kb1 == p.G ? p.lora.tile_count[t_blk] * p.lora.chunks : 0;
     };
     // Every role walks the same units in the same order: the X and A ring positions follow the K-step
     // count, the C ring position the code-stage count (a unit's steps in stages of kS, the last partial).
@@ -308,6 +344,120 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                     if (lane == 0) ptx::mbar_arrive(&x_full[i % NX]);   // TMEM stage of step i written
                 }
             }
+            if constexpr (kLora) {
+                ptx::grid_dependency_wait();               // the tiles' adapter lists come from an earlier kernel
+                int t_blk, w_blk;
+                tile_coords(t, p.num_w, t_blk, w_blk);
+                const int nchunks = lora_chunks(t_blk, kb1);
+                const int r8 = p.lora.r / 8;
+                const int n = kSwiGLU ? w_blk * BWG + quarter * 32 + lane : w_blk * BW + r;
+                const int* list = p.lora.tile_list + static_cast<int64_t>(t_blk) * BT;
+                const __nv_bfloat16* up = kSwiGLU && grp == 1 ? p.lora.b[1] : p.lora.b[0];
+                int slot = 0, w = 0;                       // chunk position: adapter in the list, chunk in the adapter
+                for (int c8 = 0; c8 < nchunks && ok; c8 += 8, ++i) {
+                    uint32_t a[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        // chunk w is [hi | lo] of the plain layer, [gate hi | gate lo | up hi | up lo] of the pair: B's
+                        // columns 8 (w mod r8) .. +7 under both parts, zero under the other row group's
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (c8 + c < nchunks && n < p.N && (!kSwiGLU || (w >= 2 * r8) == (grp == 1))) {
+                            const int part = w % r8;
+                            v = __ldg(reinterpret_cast<const uint4*>(
+                                up + (static_cast<int64_t>(list[slot]) * p.N + n) * p.lora.r + 8 * part));
+                        }
+                        a[4 * c] = finite_bf16x2(v.x);
+                        a[4 * c + 1] = finite_bf16x2(v.y);
+                        a[4 * c + 2] = finite_bf16x2(v.z);
+                        a[4 * c + 3] = finite_bf16x2(v.w);
+                        if (++w == p.lora.chunks) { w = 0; ++slot; }
+                    }
+                    if (i >= static_cast<uint32_t>(NA)) {
+                        int xs;
+                        uint32_t xph;
+                        ring_pos<NX>(i - NA, xs, xph);
+                        if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&x_empty[xs], xph, abort_flag))) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    ptx::tc_fence_after_sync();
+                    ptx::tmem_st_32x32b_x32(tmem_base + lane_addr + kAStageCol + 64u * static_cast<uint32_t>(i % NA) + 32u * grp, a);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&x_full[i % NX]);
+                }
+            }
+        }
+    } else if (kLora && warp == kWarpTmaX) {
+        // ---------------------------------------------------------------- activation producer, adapter mode
+        test_delay(kDelayActivations);   // the checked build can hold this role back (qlinear_test_delay)
+        // As the TMA producer below; the whole warp writes the extra K-steps' tiles (192 tokens x 64 columns of
+        // t's bf16 parts) into the same ring, in the layout the TMA writes: row-major 128-byte rows, 16-byte pieces
+        // permuted by the row's number mod 8.
+        uint32_t i = 0;
+        bool ok = true;
+        ptx::grid_dependency_wait();
+        const int r8 = p.lora.r / 8;
+        for (int un = blockIdx.x; un < num_units && ok; un += gridDim.x) {
+            int t, kb0, kb1;
+            unit(un, t, kb0, kb1);
+            int t_blk, w_blk;
+            tile_coords(t, p.num_w, t_blk, w_blk);
+            for (int kb = kb0; kb < kb1; ++kb, ++i) {
+                int s;
+                uint32_t ph;
+                ring_pos<NX>(i, s, ph);
+                if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&x_empty[s], ph ^ 1, abort_flag))) { ok = false; break; }
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&x_full[s], kXBytes);
+                    ptx::tma_load_2d(smem + C::kOffX + s * kXBytes, &map_x, &x_full[s], kb * BK, t_blk * BT);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            const int nchunks = lora_chunks(t_blk, kb1);
+            int slot = 0, w = 0;
+            for (int c8 = 0; c8 < nchunks; c8 += 8, ++i) {
+                int s;
+                uint32_t ph;
+                ring_pos<NX>(i, s, ph);
+                if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&x_empty[s], ph ^ 1, abort_flag))) { ok = false; break; }
+                uint8_t* stage = smem + C::kOffX + s * kXBytes;
+                for (int q = lane; q < BT; q += 32) {
+                    const int64_t m = static_cast<int64_t>(t_blk) * BT + q;
+                    const int own = m < p.M ? p.lora.row_slot[m] : -1;
+                    // 2^-e_m, the inverse of the row's scale (a power of two, e_m in [-115, 112])
+                    const float inv = own >= 0 ? __uint_as_float(0x7F000000u - __float_as_uint(p.rowscale[m])) : 0.0f;
+                    int sl = slot, ww = w;
+                    for (int c = 0; c < 8; ++c) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (sl == own && c8 + c < nchunks) {
+                            const int which = ww / r8, part = ww - which * r8;
+                            const float4* src = reinterpret_cast<const float4*>(
+                                p.lora.t + ((kSwiGLU && which >= 2 ? static_cast<int64_t>(p.M) : 0) + m) * p.lora.r + 8 * part);
+                            const float4 t0 = src[0], t1 = src[1];
+                            const bool lo = (which & 1) != 0;
+                            v.x = bf16_part(t0.x * inv, t0.y * inv, lo);
+                            v.y = bf16_part(t0.z * inv, t0.w * inv, lo);
+                            v.z = bf16_part(t1.x * inv, t1.y * inv, lo);
+                            v.w = bf16_part(t1.z * inv, t1.w * inv, lo);
+                        }
+                        *reinterpret_cast<uint4*>(stage + q * 128 + ((c ^ (q & 7)) << 4)) = v;
+                        if (++ww == p.lora.chunks) { ww = 0; ++sl; }
+                    }
+                }
+                for (int c = 0; c < 8; ++c)
+                    if (++w == p.lora.chunks) { w = 0; ++slot; }
+                ptx::fence_proxy_async_smem();             // visible to the MMAs' reads of shared memory
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&x_full[s]);
+            }
+        }
+        if (lane == 0) {
+            for (uint32_t j = (i > static_cast<uint32_t>(NX) ? i - NX : 0u); j < i; ++j)
+                ptx::mbar_wait(&x_full[j % NX], (j / NX) & 1u, nullptr);
         }
     } else if (warp == kWarpTmaX) {
         // ---------------------------------------------------------------- TMA producer of activation tiles
@@ -439,6 +589,27 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                     }
                     if (!ok) break;
                     ptx::mma_commit(&x_empty[xs]);         // releases the x stage and the A stage
+                }
+                if constexpr (kLora) {
+                    ptx::grid_dependency_wait();
+                    constexpr uint32_t idesc_lora = ptx::idesc_f16(BWG, BT, true);
+                    int t_blk, w_blk;
+                    tile_coords(t, p.num_w, t_blk, w_blk);
+                    const int nchunks = ok ? lora_chunks(t_blk, kb1) : 0;
+                    for (int c8 = 0; c8 < nchunks; c8 += 8, ++i) {
+                        int xs;
+                        uint32_t xph;
+                        ring_pos<NX>(i, xs, xph);
+                        if (!ptx::mbar_wait(&x_full[xs], xph, abort_flag)) { ok = false; break; }
+                        ptx::tc_fence_after_sync();
+                        const uint32_t x_addr = ptx::smem_addr(smem + C::kOffX + xs * kXBytes);
+                        const uint32_t d = tmem_base + kAccCol + static_cast<uint32_t>(gsel * BT);
+                        const uint32_t a_tm = tmem_base + kAStageCol + 64u * static_cast<uint32_t>(i % NA) + 32u * gsel;
+                        const int nu = min(BK / UK, (nchunks - c8) / 2);        // 16-column MMAs of this step
+                        for (int u = 0; u < nu; ++u)
+                            ptx::mma_f16_ts(d, a_tm + u * (UK / 2), ptx::sdesc_sw128(x_addr + u * UK * 2), idesc_lora, 1u);
+                        ptx::mma_commit(&x_empty[xs]);
+                    }
                 }
                 if (ok) ptx::mma_commit(&acc_full[0]);
             }

@@ -152,7 +152,9 @@ __device__ __forceinline__ uint4 prescale8(const uint4 v, int ex) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int kBits>
+// kChained: launched behind another kernel (the adapters' first product) under programmatic dependent launch; it runs
+// beside that kernel and its last row's CTAs wait for it, so that this kernel's completion implies both.
+template <int kBits, bool kChained = false>
 __global__ void __cluster_dims__(kPrepCluster, 1, 1) __launch_bounds__(kPrepThreads)
     skinny_prepass_kernel(const uint4* __restrict__ x, uint4* __restrict__ xp, int* __restrict__ rowexp, int K) {
     ptx::launch_dependents();
@@ -200,6 +202,9 @@ __global__ void __cluster_dims__(kPrepCluster, 1, 1) __launch_bounds__(kPrepThre
     }
     for (int c = c0 + kPrepCache * kPrepThreads + static_cast<int>(threadIdx.x); c < c1; c += kPrepThreads)
         xo[c] = prescale8<kBits>(xr[c], ex);
+    if constexpr (kChained) {
+        if (t == static_cast<int>(gridDim.y) - 1) ptx::grid_dependency_wait();
+    }
 }
 
 template <int NT, int B>
@@ -550,6 +555,37 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
     }
 }
 
+// The CTAs whose runs of chunks [first(c), first(c+1)) meet tile w's [w*cpt, (w+1)*cpt), in CTA order: their segment
+// bases go to seg_base (in units of one [M][128] partial), their number is returned.
+__device__ __forceinline__ int list_segments(int w, int cpt, int64_t units, int P, int segmax, int64_t* seg_base) {
+    const int64_t lo = static_cast<int64_t>(w) * cpt, hi = lo + cpt;
+    int c = static_cast<int>((lo * P) / units);
+    while (c > 0 && run_first(units, P, c) > lo) --c;
+    while (c + 1 <= P && run_first(units, P, c + 1) <= lo) ++c;
+    int k = 0;
+    int64_t f0 = run_first(units, P, c);
+    for (; c < P && f0 < hi; ++c) {
+        const int64_t f1 = run_first(units, P, c + 1);
+        if (f1 > f0) {                                        // non-empty run
+            const int w_first = static_cast<int>(f0 / cpt);
+            seg_base[k++] = static_cast<int64_t>(c) * segmax + (w - w_first);
+        }
+        f0 = f1;
+    }
+    return k;
+}
+
+// The partials of row r of the tile and token t, summed in CTA order.
+__device__ __forceinline__ float sum_segments(const float* __restrict__ partial, int64_t partial_elems,
+                                              const int64_t* seg_base, int count, int M, int t, int r) {
+    float acc = 0.0f;
+    for (int k = 0; k < count; ++k) {
+        const int64_t at = (seg_base[k] * M + t) * BW + r;
+        if (in_bounds(at, partial_elems)) acc += partial[at];
+    }
+    return acc;
+}
+
 // y[t][n] = 2^rowexp[t] * (sum over the CTAs whose runs cover tile n/128, in CTA order, of their
 // partials for that tile).  One CTA per (tile, 2 tokens): thread 0 lists the covering CTAs' segment
 // bases once, the other threads only load and add.
@@ -561,35 +597,13 @@ __global__ void __launch_bounds__(256) skinny_reduce_kernel(const float* __restr
     __shared__ int64_t seg_base[kMaxCtas];
     __shared__ int count;
     const int w = blockIdx.x;
-    if (threadIdx.x == 0) {
-        // CTAs whose run of chunks [first(c), first(c+1)) meets [w*cpt, (w+1)*cpt), in CTA order
-        const int64_t lo = static_cast<int64_t>(w) * cpt, hi = lo + cpt;
-        int c = static_cast<int>((lo * P) / units);
-        while (c > 0 && run_first(units, P, c) > lo) --c;
-        while (c + 1 <= P && run_first(units, P, c + 1) <= lo) ++c;
-        int k = 0;
-        int64_t f0 = run_first(units, P, c);
-        for (; c < P && f0 < hi; ++c) {
-            const int64_t f1 = run_first(units, P, c + 1);
-            if (f1 > f0) {                                        // non-empty run
-                const int w_first = static_cast<int>(f0 / cpt);
-                seg_base[k++] = static_cast<int64_t>(c) * segmax + (w - w_first);
-            }
-            f0 = f1;
-        }
-        count = k;
-    }
+    if (threadIdx.x == 0) count = list_segments(w, cpt, units, P, segmax, seg_base);
     ptx::grid_dependency_wait();                                  // partials come from the kernel before
     __syncthreads();
     const int t = blockIdx.y * 2 + (threadIdx.x >> 7), r = threadIdx.x & 127;
     const int n = w * BW + r;
     if (t >= M || n >= N) return;
-    float acc = 0.0f;
-    const int k_end = count;
-    for (int k = 0; k < k_end; ++k) {
-        const int64_t at = (seg_base[k] * M + t) * BW + r;
-        if (in_bounds(at, partial_elems)) acc += partial[at];
-    }
+    float acc = sum_segments(partial, partial_elems, seg_base, count, M, t, r);
     acc = ldexpf(acc, rowexp[t]);
     const int64_t e = static_cast<int64_t>(t) * N + n;
     if constexpr (kBf16Out) {

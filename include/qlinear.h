@@ -328,6 +328,96 @@ QL_API ql_status qlinear_reduce_partials(const float* partials, int32_t S, int64
                                          ql_dtype out_dtype, cudaStream_t stream);
 
 /*
+ * Low-rank adapters of many requests beside a packed projection:
+ *   t[m][j] = s[a] * sum_k x[m][k] * A[a][j][k],   a = adapter_ids[m]
+ *   y[m][n] = sum_k x[m][k] * W[n][k] + sum_j t[m][j] * B[a][n][j]
+ * x, codes, scales, biases, y and the arithmetic of the packed product as in qlinear_forward (QL_F32: y in fp32);
+ * the adapters' products accumulate in fp32 too and y is rounded once.
+ *
+ *   lora_a        bf16 [L][r][K]     the L loaded adapters' down projections
+ *   lora_b        bf16 [L][N][r]     their up projections
+ *   lora_scale    fp32 [L]           s (e.g. alpha / rank); NULL: 1
+ *   adapter_ids   int32 [M]          on the device: each row's adapter; -1: none, the row is qlinear_forward's.  Rows
+ *                                    may carry their ids in any order.  An id outside [-1, L) counts as -1 and the
+ *                                    device status word records QL_ERR_INVALID_ARG.
+ *
+ * Adapters of a lower rank than r are padded with zeros.  Preconditions and errors as in qlinear_forward, and L >= 1
+ * and non-null lora_a, lora_b, adapter_ids (else QL_ERR_INVALID_ARG); r % 8 == 0 and r <= 128 (else
+ * QL_ERR_UNSUPPORTED); lora_a and lora_b 16-byte, lora_scale and adapter_ids 4-byte aligned; y and the workspace
+ * overlap no adapter tensor.  `workspace` holds qlinear_lora_workspace_size(M, K, N, group, L, r) bytes.
+ * Non-finite activations and entries of lora_a reach the outputs of their own rows only.  A non-finite entry of
+ * lora_b counts as zero and is recorded as QL_ERR_INVALID_ARG in the device status word: rows of several adapters
+ * share a tensor-core tile, where it would reach the others' outputs.
+ *
+ * Up to 64 rows the weights are streamed as in qlinear_forward and the adapters are added where the partial sums
+ * meet; above, they are extra K-steps of the fused kernel, one 64-column step per 32 / r distinct adapters of each
+ * 192-row tile, so rows of one adapter are best kept together.
+ */
+QL_API size_t qlinear_lora_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group, int32_t L, int32_t r);
+QL_API ql_status qlinear_lora_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
+                                      const void* lora_a, const void* lora_b, const float* lora_scale,
+                                      const int32_t* adapter_ids, void* y, ql_dtype out_dtype, int64_t M, int64_t K,
+                                      int64_t N, int32_t group, int32_t L, int32_t r, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream);
+/* The same with 8-bit codes (uint32 [N][K/4], as qlinear8_forward). */
+QL_API size_t qlinear8_lora_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group, int32_t L, int32_t r);
+QL_API ql_status qlinear8_lora_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
+                                       const void* lora_a, const void* lora_b, const float* lora_scale,
+                                       const int32_t* adapter_ids, void* y, ql_dtype out_dtype, int64_t M, int64_t K,
+                                       int64_t N, int32_t group, int32_t L, int32_t r, void* workspace,
+                                       size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The SwiGLU pair with adapters: h = silu(g) * u, where g and u are the projections of x by the gate and the up
+ * weight, each with its own down and up projection of row m's adapter (one id and one scale for both):
+ *   gate_lora_a, up_lora_a   bf16 [L][r][K]        gate_lora_b, up_lora_b   bf16 [L][I][r]
+ * Everything else as in qlinear_swiglu_forward and qlinear_lora_forward.
+ */
+QL_API size_t qlinear_swiglu_lora_workspace_size(int64_t M, int64_t K, int64_t I, int32_t group, int32_t L, int32_t r);
+QL_API ql_status qlinear_swiglu_lora_forward(const void* x, const uint32_t* gate_codes, const void* gate_scales,
+                                             const void* gate_biases, const uint32_t* up_codes, const void* up_scales,
+                                             const void* up_biases, const void* gate_lora_a, const void* gate_lora_b,
+                                             const void* up_lora_a, const void* up_lora_b, const float* lora_scale,
+                                             const int32_t* adapter_ids, void* h, ql_dtype out_dtype, int64_t M,
+                                             int64_t K, int64_t I, int32_t group, int32_t L, int32_t r, void* workspace,
+                                             size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The norms after and before a block, fused with its gate and the residual update between them:
+ *   v = sum_{z<S} y[z]                                  the block's output, partials summed in z order
+ *   v = v / sqrt(mean_d v^2 + eps) * post_weight        when post_norm != 0
+ *   r = residual_scale * x + branch_scale * gate[seg] * v
+ *   h = r / sqrt(mean_d r^2 + eps) * pre_weight * (1 + scale[seg]) + shift[seg]       when h != NULL
+ * with seg = segment_ids[m] and the means over the D entries of row m.  All of it in fp32; r and h are rounded once
+ * each, h from the unrounded r.
+ *
+ *   x              [M][D] of x_dtype (QL_BF16 or QL_F32), the residual stream
+ *   y              y_dtype QL_BF16: bf16 [M][D] (S = 1); QL_F32: fp32 [S][M][D], e.g. the gathered partial outputs of
+ *                  a row-parallel projection, which this call then combines as qlinear_reduce_partials does.
+ *                  NULL: r is x itself, only h is written (out must be NULL; S, y_dtype, post_*, gate are not looked at)
+ *   out            [M][D] of x_dtype: r.  May be x (the update in place); other overlaps are refused
+ *   h              bf16 [M][D], or NULL (no pre norm; pre_weight, scale and shift must then be NULL)
+ *   post_weight, pre_weight   [D] of param_dtype; NULL: 1 (post_weight needs post_norm)
+ *   gate           [T][D] of param_dtype; NULL: 1
+ *   scale, shift   [T][D] of param_dtype; NULL: 0
+ *   segment_ids    int32 [M] on the device; NULL: segment 0 for every row.  A row with a negative segment is padding:
+ *                  it is not read, and its rows of out and h are left as they were.  A row with a segment >= T is
+ *                  left alone too, and the device status word records QL_ERR_INVALID_ARG.
+ *
+ * Required (QL_ERR_INVALID_ARG): M >= 1, D >= 8, D % 8 == 0, T >= 1, S >= 1 (S == 1 for bf16 y), eps >= 0 and finite,
+ * at least one output.  D <= QL_NORM_MAX_D (QL_ERR_UNSUPPORTED above).  All pointers 16-byte aligned except
+ * segment_ids (4).  No workspace.  The mean squares are fp32 sums: a row whose sum of squares leaves fp32's range
+ * normalizes by infinity.
+ */
+#define QL_NORM_MAX_D 32768
+QL_API ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const void* y, ql_dtype y_dtype, int32_t S,
+                                       int32_t post_norm, const void* post_weight, const void* gate,
+                                       float residual_scale, float branch_scale, const void* pre_weight,
+                                       const void* scale, const void* shift, ql_dtype param_dtype,
+                                       const int32_t* segment_ids, int32_t T, float eps, void* out, void* h,
+                                       int64_t M, int64_t D, cudaStream_t stream);
+
+/*
  * Self-test of the bounded waits inside the library's kernels.  Enqueues one small kernel that waits
  * on a barrier nothing ever completes, with the same bounded wait every pipeline role uses: it gives
  * up after the library's wait limit (about one second), records QL_ERR_DEVICE_TIMEOUT in the device

@@ -614,3 +614,54 @@ def swiglu_tolerance(h, g_ref, u_ref, bf16_output: bool = True) -> dict:
     relF = float(np.linalg.norm(h - h_ref) / ref_norm) if ref_norm > 0 else float(np.linalg.norm(h - h_ref))
     max_ratio = float(ratio.max(initial=0.0))
     return {"relF": relF, "max_ratio": max_ratio, "ok": bool(relF <= 8e-3 and max_ratio <= 1.0)}
+
+
+# --------------------------------------------------------------------------
+# Low-rank adapters beside the packed layer, and the norms around a block
+# --------------------------------------------------------------------------
+
+def lora_delta(x_bits, a_bits, b_bits, scale, ids) -> np.ndarray:
+    """delta[m][n] = s_a sum_j (sum_k x[m][k] A[a][j][k]) B[a][n][j], a = ids[m]; zero for a negative id.
+
+    x bf16 bits [M][K], A bf16 bits [L][r][K], B bf16 bits [L][N][r], scale [L] or None (1); float64.
+    """
+    x, a, b = decode_bf16(x_bits), decode_bf16(a_bits), decode_bf16(b_bits)
+    out = np.zeros((x.shape[0], b.shape[1]), dtype=np.float64)
+    for i in range(a.shape[0]):
+        rows = np.flatnonzero(np.asarray(ids) == i)
+        s = 1.0 if scale is None else float(scale[i])
+        out[rows] = s * (x[rows] @ a[i].T) @ b[i].T
+    return out
+
+
+def rms_normed(v, eps: float) -> np.ndarray:
+    """v / sqrt(mean v^2 + eps) along the last axis, float64."""
+    v = np.asarray(v, dtype=np.float64)
+    return v / np.sqrt(np.mean(v * v, axis=-1, keepdims=True) + eps)
+
+
+def norm_residual_ref(x, y=None, post_norm=True, post_weight=None, gate=None, residual_scale=1.0, branch_scale=1.0,
+                      pre_norm=True, pre_weight=None, scale=None, shift=None, seg=None, eps=1e-6):
+    """(r, h) of the norms after and before a block, float64; every argument float64 arrays, y [S][M][D]."""
+    x = np.asarray(x, dtype=np.float64)
+    seg = np.zeros(x.shape[0], dtype=np.int64) if seg is None else np.maximum(np.asarray(seg), 0)
+    r = x
+    if y is not None:
+        v = np.asarray(y, dtype=np.float64).sum(axis=0)
+        if post_norm:
+            v = rms_normed(v, eps)
+        if post_weight is not None:
+            v = v * post_weight
+        if gate is not None:
+            v = v * np.asarray(gate)[seg]
+        r = residual_scale * x + branch_scale * v
+    if not pre_norm:
+        return r, None
+    h = rms_normed(r, eps)
+    if pre_weight is not None:
+        h = h * pre_weight
+    if scale is not None:
+        h = h * (1.0 + np.asarray(scale)[seg])
+    if shift is not None:
+        h = h + np.asarray(shift)[seg]
+    return r, h

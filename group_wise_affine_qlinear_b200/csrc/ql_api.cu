@@ -419,26 +419,28 @@ struct LoraPlan {
     size_t off_t = 0, off_slot = 0, off_count = 0, off_list = 0, workspace = 0;
 };
 
-// The shrink kernel's tiles of 16 rows alone fill the GPU only from a few thousand rows on.  Below, a cluster of up to
-// 8 CTAs shares a tile's K range, the rank is cut into narrower chunks, and a tile's distinct adapters go to up to
-// 16 CTAs, each as far as it keeps the launch near two CTAs per SM.
+// The shrink kernel's tiles of 16 rows (32 on the fused path) alone fill the GPU only from a few thousand rows on.
+// Below, a cluster of up to 8 CTAs shares a tile's K range, on the weight-streaming path the rank is cut into narrower
+// chunks, and a tile's distinct adapters go to up to 16 CTAs, each as far as it keeps the launch near two CTAs per SM.
 LoraPlan lora_plan(int64_t M, int64_t K, int r, int L, int pairs, bool fused_path, size_t base, int sm_count) {
     LoraPlan lp;
-    const int64_t tiles = (M + lora::kTile - 1) / lora::kTile;
+    const int rows = fused_path ? 2 * lora::kTile : lora::kTile;
+    const int64_t tiles = (M + rows - 1) / rows;
     const int64_t want = 2 * sm_count;
     const int r8 = r / 8;
-    lp.nt = r8 >= 8 ? 8 : r8 >= 3 ? 4 : r8;
+    lp.nt = r8 >= 3 ? 4 : r8;
     int64_t ctas = tiles * pairs * ((r8 + lp.nt - 1) / lp.nt);
     // at least two 32-column blocks of K per warp and CTA
     while (lp.S < lora::kMaxSplit && ctas * lp.S < want && K / 32 >= 2 * lora::kWarps * 2 * lp.S) lp.S *= 2;
-    while (lp.nt > 1 && ctas * lp.S * 2 <= want) {
+    while (!fused_path && lp.nt > 1 && ctas * lp.S * 2 <= want) {
         lp.nt /= 2;
         ctas = tiles * pairs * ((r8 + lp.nt - 1) / lp.nt);
     }
     lp.chunks = (r8 + lp.nt - 1) / lp.nt;
-    while (lp.passes < std::min(L, lora::kTile) && ctas * lp.S * lp.passes < want) ++lp.passes;
+    while (lp.passes < std::min(L, rows) && ctas * lp.S * lp.passes < want) ++lp.passes;
     if (M <= 512) lp.passes = std::min(L, lora::kTile);
     lp.off_t = round_up(base, 256);
+    // t: fp32 [M][r], or on the fused path two bf16 parts per pair member
     lp.off_slot = lp.off_t + round_up(static_cast<size_t>(pairs) * M * r * 4, 256);
     lp.workspace = lp.off_slot;
     if (fused_path) {
@@ -450,27 +452,44 @@ LoraPlan lora_plan(int64_t M, int64_t K, int r, int L, int pairs, bool fused_pat
     return lp;
 }
 
-// t = s x . A^T of every row's adapter, and on the fused path the token tiles' adapter lists.
+template <int MT, bool kConvert>
+cudaError_t launch_shrink_nt(int nt, const cudaLaunchConfig_t& cfg, const lora::ShrinkParams& p) {
+    switch (nt) {
+        case 1: return cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<1, MT, kConvert>, p);
+        case 2: return cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<2, MT, kConvert>, p);
+        default: return cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<4, MT, kConvert>, p);
+    }
+}
+
+// t = s x . A^T of every row's adapter.  xh != null: the fused path's form, which also converts the activations and
+// lists the token tiles' adapters, launched behind the parameter transpose under programmatic dependent launch.
 ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, int64_t M, int64_t K, uint8_t* ws,
-                        bool fused_path, bool dependent, cudaStream_t st) {
+                        __half* xh, float* rowscale, int bits, cudaStream_t st) {
     lora::ShrinkParams p = {};
     p.x = static_cast<const __nv_bfloat16*>(x);
     for (int i = 0; i < 2; ++i) p.a[i] = static_cast<const __nv_bfloat16*>(la.a[i]);
     p.scale = la.scale;
     p.ids = la.ids;
-    p.t = reinterpret_cast<float*>(ws + lp.off_t);
     p.M = static_cast<int>(M);
     p.K = static_cast<int>(K);
     p.r = la.r;
     p.L = la.L;
-    p.tiles = static_cast<int>((M + lora::kTile - 1) / lora::kTile);
     p.passes = lp.passes;
     p.chunks = lp.chunks;
-    if (fused_path) {
+    p.pairs = la.pairs;
+    const int rows = xh ? 2 * lora::kTile : lora::kTile;
+    p.tiles = static_cast<int>((M + rows - 1) / rows);
+    if (xh) {
+        p.tw = reinterpret_cast<__nv_bfloat16*>(ws + lp.off_t);
+        p.xh = xh;
+        p.rowscale = rowscale;
+        p.bits = bits;
         p.row_slot = reinterpret_cast<int*>(ws + lp.off_slot);
         p.tile_count = reinterpret_cast<int*>(ws + lp.off_count);
         p.tile_list = reinterpret_cast<int*>(ws + lp.off_list);
         p.num_t = static_cast<int>((M + fused::BT - 1) / fused::BT);
+    } else {
+        p.t = reinterpret_cast<float*>(ws + lp.off_t);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.tiles) * lp.passes + p.num_t, lp.S, lp.chunks * la.pairs);
@@ -484,27 +503,38 @@ ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, i
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 2 : 1;
-    cudaError_t e = cudaErrorInvalidValue;
-    switch (lp.nt) {
-        case 1: e = cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<1>, p); break;
-        case 2: e = cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<2>, p); break;
-        case 4: e = cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<4>, p); break;
-        case 8: e = cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<8>, p); break;
-    }
+    cfg.numAttrs = xh ? 2 : 1;
+    const cudaError_t e = xh ? launch_shrink_nt<2, true>(lp.nt, cfg, p) : launch_shrink_nt<1, false>(lp.nt, cfg, p);
     return e == cudaSuccess ? QL_OK : QL_ERR_CUDA;
 }
 
-fused::LoraParams lora_params(const LoraArgs& la, const LoraPlan& lp, uint8_t* ws) {
-    fused::LoraParams q;
-    for (int i = 0; i < 2; ++i) q.b[i] = static_cast<const __nv_bfloat16*>(la.b[i]);
-    q.t = reinterpret_cast<const float*>(ws + lp.off_t);
-    q.row_slot = reinterpret_cast<const int*>(ws + lp.off_slot);
-    q.tile_count = reinterpret_cast<const int*>(ws + lp.off_count);
-    q.tile_list = reinterpret_cast<const int*>(ws + lp.off_list);
-    q.r = la.r;
-    q.chunks = la.pairs * la.r / 4;
-    return q;
+// Fills the adapter mode's parameters; n_box: rows of a box of B (a tile's, or half of them for a pair).
+ql_status lora_params(const LoraArgs& la, const LoraPlan& lp, uint8_t* ws, int64_t M, int64_t N, int n_box,
+                      fused::LoraParams* q) {
+    q->r8 = la.r / 8;
+    q->parts = la.pairs * q->r8;
+    q->tw = reinterpret_cast<const __nv_bfloat16*>(ws + lp.off_t);
+    q->row_slot = reinterpret_cast<const int*>(ws + lp.off_slot);
+    q->tile_count = reinterpret_cast<const int*>(ws + lp.off_count);
+    q->tile_list = reinterpret_cast<const int*>(ws + lp.off_list);
+    ql_status s;
+    for (int i = 0; i < la.pairs; ++i)
+        if ((s = encode_3d(&q->map_b[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, la.b[i], la.r, N, la.L, la.r * 2,
+                           static_cast<uint64_t>(N) * la.r * 2, fused::part_cols(q->r8), n_box)) != QL_OK)
+            return s;
+    return encode_2d(&q->map_tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q->tw, 16 * q->parts, M, 32 * q->parts, 64, 8,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Launches the fused kernel of a template configuration, with or without adapters.
+template <bool kBf16Out, class FC, bool kSwiGLU, bool kSplitK>
+ql_status launch_fused(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& mc, const CUtensorMap& mc2,
+                       const CUtensorMap& mp, const CUtensorMap& my, const fused::LoraParams& p, bool with_lora) {
+    if (with_lora)
+        return launch_dependent(fused::fused_gemm_kernel<kBf16Out, FC, kSwiGLU, kSplitK, true>, grid, fused::kThreads,
+                                FC::kSmemBytes, st, mx, mc, mc2, mp, my, p);
+    return launch_dependent(fused::fused_gemm_kernel<kBf16Out, FC, kSwiGLU, kSplitK>, grid, fused::kThreads,
+                            FC::kSmemBytes, st, mx, mc, mc2, mp, my, static_cast<const fused::Params&>(p));
 }
 
 ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
@@ -552,11 +582,12 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
     transpose_params_kernel<<<tgrid, 256, 0, st>>>(static_cast<const __half*>(scales), static_cast<const __half*>(biases),
                                                    sb, static_cast<int>(N), static_cast<int>(G));
     if ((s = launch_status()) != QL_OK) return s;
-    // adapters: their first product runs between the two, beside both (its last CTA waits for the transpose)
-    if (la && (s = launch_shrink(*la, *lp, x, M, K, base, true, true, st)) != QL_OK) return s;
-    if ((s = launch_convert_x(bits, static_cast<const __nv_bfloat16*>(x), xh, rs, M, K, st)) != QL_OK) return s;
-    fused::Params p = {};
-    if (la) p.lora = lora_params(*la, *lp, base);
+    // with adapters their first product converts the activations on its way
+    s = la ? launch_shrink(*la, *lp, x, M, K, base, xh, rs, bits, st)
+           : launch_convert_x(bits, static_cast<const __nv_bfloat16*>(x), xh, rs, M, K, st);
+    if (s != QL_OK) return s;
+    fused::LoraParams p = {};
+    if (la && (s = lora_params(*la, *lp, base, M, N, fused::BW, &p)) != QL_OK) return s;
     p.rowscale = rs;
     p.y = y;
     p.M = static_cast<int>(M);
@@ -572,10 +603,8 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
     using F4 = fused::PickCfg<4, false>::type;
     using F8 = fused::PickCfg<8, false>::type;
     if (split) {
-        auto k4 = la ? fused::fused_gemm_kernel<false, F4, false, true, true> : fused::fused_gemm_kernel<false, F4, false, true>;
-        auto k8 = la ? fused::fused_gemm_kernel<false, F8, false, true, true> : fused::fused_gemm_kernel<false, F8, false, true>;
-        s = bits == 4 ? launch_dependent(k4, fgrid, fused::kThreads, F4::kSmemBytes, st, mx, mc, mc, mp, my, p)
-                      : launch_dependent(k8, fgrid, fused::kThreads, F8::kSmemBytes, st, mx, mc, mc, mp, my, p);
+        s = bits == 4 ? launch_fused<false, F4, false, true>(fgrid, st, mx, mc, mc, mp, my, p, la != nullptr)
+                      : launch_fused<false, F8, false, true>(fgrid, st, mx, mc, mc, mp, my, p, la != nullptr);
         if (s != QL_OK) return s;
         prof_end(st);
         // ordered sum of the slices, rounded once (a plain launch: it reads what the kernel above wrote)
@@ -588,7 +617,7 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
         const int nc = bits == 4 ? F4::kNC : F8::kNC;
         const int nx = bits == 4 ? F4::kNX : F8::kNX;
         set_dispatch("path=tc_fused%s bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=%d launches=%d why=%s",
-                     la ? "_lora" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, pl.split_k, la ? 5 : 4, pl.why);
+                     la ? "_lora" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, pl.split_k, 4, pl.why);
         return launch_status();
     }
     using B4 = fused::PickCfg<4, true>::type;
@@ -601,23 +630,20 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
         return launch_status();
     }
 #endif
-    auto b4 = la ? fused::fused_gemm_kernel<true, B4, false, false, true> : fused::fused_gemm_kernel<true, B4>;
-    auto f4 = la ? fused::fused_gemm_kernel<false, F4, false, false, true> : fused::fused_gemm_kernel<false, F4>;
-    auto b8 = la ? fused::fused_gemm_kernel<true, B8, false, false, true> : fused::fused_gemm_kernel<true, B8>;
-    auto f8 = la ? fused::fused_gemm_kernel<false, F8, false, false, true> : fused::fused_gemm_kernel<false, F8>;
+    const bool lo = la != nullptr;
     if (bits == 4) {
-        s = bf16_out ? launch_dependent(b4, fgrid, fused::kThreads, B4::kSmemBytes, st, mx, mc, mc, mp, my, p)
-                     : launch_dependent(f4, fgrid, fused::kThreads, F4::kSmemBytes, st, mx, mc, mc, mp, my, p);
+        s = bf16_out ? launch_fused<true, B4, false, false>(fgrid, st, mx, mc, mc, mp, my, p, lo)
+                     : launch_fused<false, F4, false, false>(fgrid, st, mx, mc, mc, mp, my, p, lo);
     } else {
-        s = bf16_out ? launch_dependent(b8, fgrid, fused::kThreads, B8::kSmemBytes, st, mx, mc, mc, mp, my, p)
-                     : launch_dependent(f8, fgrid, fused::kThreads, F8::kSmemBytes, st, mx, mc, mc, mp, my, p);
+        s = bf16_out ? launch_fused<true, B8, false, false>(fgrid, st, mx, mc, mc, mp, my, p, lo)
+                     : launch_fused<false, F8, false, false>(fgrid, st, mx, mc, mc, mp, my, p, lo);
     }
     if (s != QL_OK) return s;
     prof_end(st);
     const int nc = bits == 4 ? (bf16_out ? B4::kNC : F4::kNC) : (bf16_out ? B8::kNC : F8::kNC);
     const int nx = bits == 4 ? (bf16_out ? B4::kNX : F4::kNX) : (bf16_out ? B8::kNX : F8::kNX);
     set_dispatch("path=tc_fused%s bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=1 launches=%d why=%s",
-                 la ? "_lora" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, la ? 4 : 3,
+                 la ? "_lora" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, 3,
                  pl.why);
     (void)codes;
     return launch_status();
@@ -670,7 +696,7 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
     const dim3 pre_grid(static_cast<unsigned>(skinny::kPrepCluster), static_cast<unsigned>(M));
     if (la) {
         // the adapters' first product, then the prepass beside it
-        if ((s = launch_shrink(*la, *lp, x, M, K, wsb, false, false, st)) != QL_OK) return s;
+        if ((s = launch_shrink(*la, *lp, x, M, K, wsb, nullptr, nullptr, bits, st)) != QL_OK) return s;
         auto pre = bits == 4 ? skinny::skinny_prepass_kernel<4, true> : skinny::skinny_prepass_kernel<8, true>;
         if ((s = launch_dependent(pre, pre_grid, skinny::kPrepThreads, 0, st, static_cast<const uint4*>(x),
                                   static_cast<uint4*>(xp), rowexp, static_cast<int>(K))) != QL_OK)
@@ -787,10 +813,11 @@ ql_status run_swiglu(const SwigluPlan& pl, const void* x, const uint32_t* gc, co
                                                         sb, static_cast<int>(I), static_cast<int>(G),
                                                         static_cast<int>(pl.ncols));
     if ((s = launch_status()) != QL_OK) return s;
-    if (la && (s = launch_shrink(*la, *lp, x, M, K, base, true, true, st)) != QL_OK) return s;
-    if ((s = launch_convert_x(4, static_cast<const __nv_bfloat16*>(x), xh, rs, M, K, st)) != QL_OK) return s;
-    fused::Params p = {};
-    if (la) p.lora = lora_params(*la, *lp, base);
+    s = la ? launch_shrink(*la, *lp, x, M, K, base, xh, rs, 4, st)
+           : launch_convert_x(4, static_cast<const __nv_bfloat16*>(x), xh, rs, M, K, st);
+    if (s != QL_OK) return s;
+    fused::LoraParams p = {};
+    if (la && (s = lora_params(*la, *lp, base, M, I, fused::BWG, &p)) != QL_OK) return s;
     p.rowscale = rs;
     p.y = h;
     p.M = static_cast<int>(M);
@@ -803,15 +830,13 @@ ql_status run_swiglu(const SwigluPlan& pl, const void* x, const uint32_t* gc, co
     const int grid = std::min(tiles, sm_count);
     const dim3 fgrid(static_cast<unsigned>(grid));
     prof_begin(st);
-    auto kb = la ? fused::fused_gemm_kernel<true, FB, true, false, true> : fused::fused_gemm_kernel<true, FB, true>;
-    auto kf = la ? fused::fused_gemm_kernel<false, FF, true, false, true> : fused::fused_gemm_kernel<false, FF, true>;
-    s = bf16_out ? launch_dependent(kb, fgrid, fused::kThreads, FB::kSmemBytes, st, mx, mcg, mcu, mp, my, p)
-                 : launch_dependent(kf, fgrid, fused::kThreads, FF::kSmemBytes, st, mx, mcg, mcu, mp, my, p);
+    s = bf16_out ? launch_fused<true, FB, true, false>(fgrid, st, mx, mcg, mcu, mp, my, p, la != nullptr)
+                 : launch_fused<false, FF, true, false>(fgrid, st, mx, mcg, mcu, mp, my, p, la != nullptr);
     if (s != QL_OK) return s;
     prof_end(st);
     set_dispatch("path=tc_fused_swiglu%s bits=4 tile=%dg+%du x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d launches=%d",
                  la ? "_lora" : "", fused::BWG, fused::BWG, fused::BT, fused::BK, bf16_out ? FB::kNX : FF::kNX,
-                 bf16_out ? FB::kNC : FF::kNC, FB::kS, fused::NA, grid, la ? 4 : 3);
+                 bf16_out ? FB::kNC : FF::kNC, FB::kS, fused::NA, grid, 3);
     return launch_status();
 }
 

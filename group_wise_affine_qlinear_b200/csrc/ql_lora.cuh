@@ -11,6 +11,7 @@
 // the fused path appends it to the tile's K loop (ql_tc_fused.cuh), so y is rounded once.
 #pragma once
 
+#include "ql_prepass.cuh"
 #include "ql_ptx.cuh"
 #include "ql_tc_fused.cuh"
 #include "ql_tc_skinny.cuh"
@@ -29,12 +30,16 @@ struct ShrinkParams {
     const __nv_bfloat16* a[2];   // [L][r][K]; the second one of a gate/up pair
     const float* scale;          // [L] or null (1)
     const int* ids;              // [M]
-    float* t;                    // [pair][M][r]
+    float* t;                    // weight-streaming path: [M][r]
     int M, K, r, L;
-    int tiles;                   // ceil(M / 16)
+    int tiles;                   // ceil(M / (16 MT))
     int passes;                  // CTAs that share a tile's distinct adapters
     int chunks;                  // CTAs along the rank: ceil(r / (8 NT))
-    // the fused path's plan (null on the weight-streaming path)
+    // fused path (null on the weight-streaming path)
+    __nv_bfloat16* tw;           // [M][pairs][r / 8][hi 8 | lo 8]: t 2^-e_m in two bf16 parts
+    __half* xh;                  // [M][K]: x 2^-e_m in the dequantizer's k order
+    float* rowscale;             // [M]: 2^e_m
+    int bits, pairs;
     int* row_slot;               // [M] position of the row's adapter in its token tile's list, or -1
     int* tile_count;             // [num_t] distinct adapters of the token tile
     int* tile_list;              // [num_t][BT] those adapters, in order of first use
@@ -94,19 +99,36 @@ __device__ __forceinline__ void plan_tile(const ShrinkParams& p, int t_blk) {
     if (i == 0) p.tile_count[t_blk] = total;
 }
 
-// t for 16 rows.  grid: (tiles * passes + num_t, S, chunks * pair), cluster (1, S, 1).
+// The conversion's row scale (convert_x_kernel): 2^e with the row's largest magnitude in [2^15, 2^16) after division,
+// 1 for a zero or non-finite row.  amax: the largest bf16 bit pattern without its sign.
+__device__ __forceinline__ float row_scale(uint32_t amax) {
+    const uint32_t ex = amax >> 7;                 // biased exponent
+    if (amax == 0 || ex == 0xFF) return 1.0f;
+    const int e = max(static_cast<int>(ex) - 127, -100) - 15;
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// t for 16 MT rows.  grid: (tiles * passes + num_t, S, chunks * pairs), cluster (1, S, 1).
 //
 // Each warp multiplies its share of the K range, 32 columns at a time: a lane's 16-byte loads are 8 consecutive k of
-// two activation rows and of one adapter row per n-tile, which feed two MMAs; the MMA's k order is whatever the lanes
-// hold, the same for both operands, so a dot product keeps its terms.  The warps' sums meet in shared memory, the
-// cluster's CTAs' in distributed shared memory, each added in a fixed order.
+// the tile's activation rows and of one adapter row per n-tile, which feed two MMAs per row block; the MMA's k order
+// is whatever the lanes hold, the same for both operands, so a dot product keeps its terms.  The warps' sums meet in
+// shared memory, the cluster's CTAs' in distributed shared memory, each added in a fixed order.
 //
 // Rows of a tile with other adapters are multiplied too and not written: a tile makes one pass per distinct adapter,
 // and its passes are spread over `passes` CTAs.
-template <int NT>
-__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkParams p) {
+//
+// kConvert (fused path): the same kernel converts the activations (as convert_x_kernel), whose row scale its extra
+// K-steps share, so x comes from DRAM once: the maxima are taken from the registers that feed the MMAs, and the first
+// pass's CTAs then read their rows again, from L2, to convert them.
+template <int NT, int MT, bool kConvert>
+__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkParams p) {
     ptx::launch_dependents();
-    __shared__ float part[kWarps][kTile * NT * 8];         // [row][rank] per warp
+    constexpr int kRows = kTile * MT;
+    constexpr int kSums = kRows * NT * 8;
+    __shared__ float part[kWarps][kSums];          // [row][rank] per warp
+    __shared__ uint32_t amax[kWarps][kRows];
+    __shared__ float scale_s[kRows];
     const int S = static_cast<int>(gridDim.y);
     const int rank = static_cast<int>(blockIdx.y);             // rank in the cluster (1, S, 1)
     const int shrink_ctas = p.tiles * p.passes;
@@ -115,91 +137,181 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkParam
     } else {
         const int tile = static_cast<int>(blockIdx.x) / p.passes, pass = static_cast<int>(blockIdx.x) % p.passes;
         const int pair = static_cast<int>(blockIdx.z) / p.chunks, chunk = static_cast<int>(blockIdx.z) % p.chunks;
+        const bool converts = kConvert && pass == 0 && blockIdx.z == 0;
         const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
-        const int m0 = tile * kTile;
+        const int m0 = tile * kRows;
         const int j0 = chunk * NT * 8;
-        const int mine = lane < kTile && m0 + lane < p.M ? adapter_of(p.ids, m0 + lane, p.L) : -1;
+        const int mine = lane < kRows && m0 + lane < p.M ? adapter_of(p.ids, m0 + lane, p.L) : -1;
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, mine);
         uint32_t leaders = __ballot_sync(0xFFFFFFFFu, mine >= 0 && (__ffs(same) - 1) == lane);
         const int kb_all = p.K / 32;
         const int kb0 = static_cast<int>(static_cast<int64_t>(kb_all) * rank / S);
         const int kb1 = static_cast<int>(static_cast<int64_t>(kb_all) * (rank + 1) / S);
         const int g = lane >> 2, c = lane & 3;
-        // rows past M repeat the last one; their results are not written
-        const int64_t row0 = min(m0 + g, p.M - 1), row1 = min(m0 + g + 8, p.M - 1);
-        const uint4* x0 = reinterpret_cast<const uint4*>(p.x + row0 * p.K) + c;
-        const uint4* x1 = reinterpret_cast<const uint4*>(p.x + row1 * p.K) + c;
-        for (int n = 0; leaders != 0; ++n, leaders &= leaders - 1) {
-            if (n % p.passes != pass) continue;
-            const int adapter = __shfl_sync(0xFFFFFFFFu, mine, __ffs(leaders) - 1);
-            const __nv_bfloat16* a = (pair == 0 ? p.a[0] : p.a[1]) + (static_cast<int64_t>(adapter) * p.r + j0) * p.K;
-            float acc[NT][4];
+        const uint4* xr[2 * MT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+        for (int q = 0; q < 2 * MT; ++q) {         // rows past M repeat the last one; their results are not written
+            const int64_t row = min(m0 + g + 8 * q, p.M - 1);
+            xr[q] = reinterpret_cast<const uint4*>(p.x + row * p.K) + c;
+        }
+        bool first = true;                         // the pass that also takes the rows' maxima
+        for (int n = 0; leaders != 0 || (converts && first); ++n, leaders &= leaders - 1) {
+            if (leaders != 0 && n % p.passes != pass) continue;
+            const bool with = leaders != 0;        // false: a converting CTA without an adapter in its rows
+            const int adapter = with ? __shfl_sync(0xFFFFFFFFu, mine, __ffs(leaders) - 1) : -1;
+            const __nv_bfloat16* a = (pair == 0 ? p.a[0] : p.a[1]) + (static_cast<int64_t>(with ? adapter : 0) * p.r + j0) * p.K;
+            const int nt_live = with ? min(NT, p.r / 8 - chunk * NT) : 0;
+            float acc[MT][NT][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
-            constexpr int U = NT <= 2 ? 4 : 2;                 // column blocks in flight per warp
+            for (int q = 0; q < MT; ++q)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[q][i][e] = 0.0f;
+            uint32_t mx[2 * MT];
+#pragma unroll
+            for (int q = 0; q < 2 * MT; ++q) mx[q] = 0u;
+            constexpr int U = NT * MT <= 2 ? 4 : 2;            // column blocks in flight per warp
             for (int kb = kb0 + warp; kb < kb1; kb += kWarps * U) {
-                uint4 vx0[U], vx1[U], va[U][NT];
+                uint4 vx[U][2 * MT], va[U][NT];
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int b = kb + u * kWarps;
                     const bool in = b < kb1;
-                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                    vx0[u] = in ? __ldg(x0 + 4 * b) : zero;
-                    vx1[u] = in ? __ldg(x1 + 4 * b) : zero;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const bool use = in && j0 + 8 * i < p.r;
-                        va[u][i] = use ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<int64_t>(8 * i + g) * p.K) + c +
-                                               4 * b)
+                    for (int q = 0; q < 2 * MT; ++q) vx[u][q] = in ? __ldg(xr[q] + 4 * b) : zero;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        va[u][i] = in && i < nt_live
+                                       ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<int64_t>(8 * i + g) * p.K) + c + 4 * b)
                                        : zero;
-                    }
                 }
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u) {
+                    if constexpr (kConvert) {
+                        if (first) {
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        mma_bf16_16816(acc[i], vx0[u].x, vx1[u].x, vx0[u].y, vx1[u].y, va[u][i].x, va[u][i].y);
-                        mma_bf16_16816(acc[i], vx0[u].z, vx1[u].z, vx0[u].w, vx1[u].w, va[u][i].z, va[u][i].w);
+                            for (int q = 0; q < 2 * MT; ++q) {
+                                const uint4 v = vx[u][q];
+                                mx[q] = __vmaxu2(mx[q], __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                                                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+                            }
+                        }
                     }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int q = 0; q < MT; ++q) {
+                            mma_bf16_16816(acc[q][i], vx[u][2 * q].x, vx[u][2 * q + 1].x, vx[u][2 * q].y, vx[u][2 * q + 1].y,
+                                           va[u][i].x, va[u][i].y);
+                            mma_bf16_16816(acc[q][i], vx[u][2 * q].z, vx[u][2 * q + 1].z, vx[u][2 * q].w, vx[u][2 * q + 1].w,
+                                           va[u][i].z, va[u][i].w);
+                        }
+                }
             }
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int at = g * NT * 8 + 8 * i + 2 * c;
-                part[warp][at] = acc[i][0];
-                part[warp][at + 1] = acc[i][1];
-                part[warp][at + 8 * NT * 8] = acc[i][2];
-                part[warp][at + 8 * NT * 8 + 1] = acc[i][3];
+            for (int q = 0; q < MT; ++q)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int at = (16 * q + g) * NT * 8 + 8 * i + 2 * c;
+                    *reinterpret_cast<float2*>(&part[warp][at]) = make_float2(acc[q][i][0], acc[q][i][1]);
+                    *reinterpret_cast<float2*>(&part[warp][at + 8 * NT * 8]) = make_float2(acc[q][i][2], acc[q][i][3]);
+                }
+            if (kConvert && first) {
+#pragma unroll
+                for (int q = 0; q < 2 * MT; ++q) {
+                    uint32_t v = max(mx[q] & 0xFFFFu, mx[q] >> 16);
+                    v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+                    v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+                    if (c == 0) amax[warp][g + 8 * q] = v;
+                }
             }
             __syncthreads();
-            for (int e = threadIdx.x; e < kTile * NT * 8; e += kThreads) {
+            for (int e = threadIdx.x; e < kSums; e += kThreads) {
                 float s = part[0][e];
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) s += part[w][e];
-                part[0][e] = s;                             // this CTA's slice of the sum
+                part[0][e] = s;                                // this CTA's slice of the sum
+            }
+            if (kConvert && first && threadIdx.x < kRows) {
+                uint32_t v = amax[0][threadIdx.x];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) v = max(v, amax[w][threadIdx.x]);
+                amax[0][threadIdx.x] = v;
             }
             if (S > 1) ptx::cluster_sync(); else __syncthreads();
-            // every CTA of the cluster finishes its share of the tile's sums
-            for (int e = threadIdx.x + rank * kThreads; e < kTile * NT * 8; e += S * kThreads) {
-                float s;
+            if (kConvert && first) {
+                if (threadIdx.x < kRows) {
+                    uint32_t v = amax[0][threadIdx.x];
+                    for (int q = 0; S > 1 && q < S; ++q)
+                        v = max(v, __float_as_uint(ptx::ld_shared_cluster_f32(&amax[0][threadIdx.x], static_cast<uint32_t>(q))));
+                    const float sc = row_scale(v);
+                    scale_s[threadIdx.x] = sc;
+                    if (converts && rank == 0 && m0 + static_cast<int>(threadIdx.x) < p.M) p.rowscale[m0 + threadIdx.x] = sc;
+                }
+                __syncthreads();
+            }
+            // every CTA of the cluster finishes its share of the tile's sums, two ranks at a time
+            for (int e = 2 * (static_cast<int>(threadIdx.x) + rank * kThreads); with && e < kSums; e += 2 * S * kThreads) {
+                float s0 = part[0][e], s1 = part[0][e + 1];
                 if (S > 1) {
-                    s = 0.0f;
-                    for (int q = 0; q < S; ++q) s += ptx::ld_shared_cluster_f32(&part[0][e], static_cast<uint32_t>(q));
-                } else {
-                    s = part[0][e];
+                    s0 = s1 = 0.0f;
+                    for (int q = 0; q < S; ++q) {
+                        s0 += ptx::ld_shared_cluster_f32(&part[0][e], static_cast<uint32_t>(q));
+                        s1 += ptx::ld_shared_cluster_f32(&part[0][e + 1], static_cast<uint32_t>(q));
+                    }
                 }
                 const int row = e / (NT * 8), j = j0 + e % (NT * 8);
                 const int m = m0 + row;
-                if (m < p.M && j < p.r && p.ids[m] == adapter)
-                    p.t[(static_cast<int64_t>(pair) * p.M + m) * p.r + j] =
-                        s * (p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f);
+                if (m < p.M && j < p.r && p.ids[m] == adapter) {
+                    const float sc = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
+                    s0 *= sc;
+                    s1 *= sc;
+                    if constexpr (kConvert) {
+                        const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));   // 2^-e_m
+                        __nv_bfloat16* o = p.tw + (static_cast<int64_t>(m) * p.pairs + pair) * 2 * p.r + 16 * (j / 8) + j % 8;
+                        *reinterpret_cast<uint32_t*>(o) = fused::bf16_part(s0 * inv, s1 * inv, false);
+                        *reinterpret_cast<uint32_t*>(o + 8) = fused::bf16_part(s0 * inv, s1 * inv, true);
+                    } else {
+                        *reinterpret_cast<float2*>(p.t + static_cast<int64_t>(m) * p.r + j) = make_float2(s0, s1);
+                    }
+                }
             }
             if (S > 1) ptx::cluster_sync(); else __syncthreads();      // the sums are read before the next pass
+            first = false;
+            if (!with) break;
+        }
+        if (converts) {
+            if (rank == 0) {
+                // rows without an adapter: zeros in tw, so that a tile's box of it needs no mask
+                const int pieces = p.pairs * p.r / 4;
+                for (int row = warp; row < kRows && m0 + row < p.M; row += kWarps) {
+                    if (__shfl_sync(0xFFFFFFFFu, mine, row) >= 0) continue;
+                    uint4* o = reinterpret_cast<uint4*>(p.tw) + static_cast<int64_t>(m0 + row) * pieces;
+                    for (int i = lane; i < pieces; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            // the CTA's columns of its rows, a row per warp at a time
+            const int c0 = 4 * kb0, c1 = 4 * kb1;
+            for (int row = warp; row < kRows && m0 + row < p.M; row += kWarps) {
+                const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));
+                const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(m0 + row) * p.K);
+                uint4* dst = reinterpret_cast<uint4*>(p.xh + static_cast<int64_t>(m0 + row) * p.K);
+                for (int i = c0 + lane; i < c1; i += 32 * 4) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i + 32 * u < c1) v[u] = __ldg(src + i + 32 * u);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i + 32 * u < c1) dst[i + 32 * u] = p.bits == 4 ? convert8<4>(v[u], inv) : convert8<8>(v[u], inv);
+                }
+            }
         }
     }
-    // Launched behind the parameter transpose under programmatic dependent launch; as with the conversion that
-    // follows, the last CTA waits for the kernel before, so that this kernel's completion implies both.
+    // Launched behind the parameter transpose under programmatic dependent launch; as with the conversion of the
+    // plain layer, the last CTA waits for it, so that this kernel's completion implies both.
     if (blockIdx.x == gridDim.x - 1) ptx::grid_dependency_wait();
 }
 

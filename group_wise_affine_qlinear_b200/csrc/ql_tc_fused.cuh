@@ -64,13 +64,13 @@
 // Adapter mode (kLora): y += sum_j t[m][j] B[a][n][j] for the low-rank adapter a of every row m, t = s x . A^T (an
 // earlier kernel).  The product is more K for the same accumulators: after the G quantization groups the unit that
 // owns the end of K runs extra K-steps whose weight operand is B itself (bf16, bit for bit) and whose activation
-// operand is t, scaled like the row's activations and cut into two bf16, t = hi + lo to 2^-16 relative, one column
-// each (the MMA's type is per instruction: these steps run in bf16, whose exponents cannot overflow where f16's
-// could).  A rank-r adapter thus takes 2r columns; a tile's distinct adapters lie side by side in those columns, and a
-// token's row is zero outside its own adapter's, so a tile pays for the adapters in it (one 64-column step per four
-// of rank 8, per one of rank 32) and nothing travels through memory: no pass over y, and y is rounded once.
-// In SwiGLU mode an adapter has 4r columns, the gate's hi and lo and the up's hi and lo; each row group's weight
-// operand is zero under the other's.
+// operand is t, scaled like the row's activations and cut into two bf16, t = hi + lo to 2^-16 relative (the MMA's
+// type is per instruction: these steps run in bf16, whose exponents cannot overflow where f16's could).  A "part" is 8
+// columns of B under 16 of t's, [hi 8 | lo 8]; a tile's distinct adapters lie side by side, r / 8 parts each (in
+// SwiGLU mode the gate's r / 8, then the up's, each zero under the other row group), four parts to a step; a token's
+// row is zero outside its own adapter's parts.  So a tile pays for the adapters in it (one step per 32 / r of them),
+// nothing travels through memory a second time, and y is rounded once.  B comes by TMA through the code ring (a code
+// stage per extra step), t by TMA too, eight rows at a time, but for the eights that meet several adapters.
 #pragma once
 
 #include "ql_ptx.cuh"
@@ -140,25 +140,29 @@ template <> struct PickCfg<4, false> { using type = Cfg<4, 2, 4, 4, 1>; };
 template <> struct PickCfg<8, true> { using type = Cfg<5, 2, 8, 2, 2>; };
 template <> struct PickCfg<8, false> { using type = Cfg<4, 2, 8, 4, 1>; };
 
-// Adapter mode: operands of the extra K-steps (b[1] and the second half of t are the up projection's).
-struct LoraParams {
-    const __nv_bfloat16* b[2];   // [L][N][r]
-    const float* t;              // [pair][M][r], scaled by the adapter's factor
-    const int* row_slot;         // [M] place of the row's adapter in its token tile's list, or -1
-    const int* tile_count;       // [num_t] distinct adapters of the token tile
-    const int* tile_list;        // [num_t][BT]
-    int r;
-    int chunks;                  // 8-column chunks per adapter: 2r / 8, in SwiGLU mode 4r / 8
-};
-
 struct Params {
     float* rowscale;      // [M] 2^e_m
     void* y;              // [M][N] bf16 or fp32
     int M, N, G;
     int num_t, num_w;     // token tiles, weight tiles
     int splits;           // K slices per tile (split-K instantiations; 1 otherwise)
-    LoraParams lora;      // adapter mode only
 };
+
+// Adapter mode: the operands of the extra K-steps.
+struct LoraParams : Params {
+    CUtensorMap map_b[2];        // B of the layer (of gate and up) as (r, N, L), boxes of part_cols(r8) columns
+    CUtensorMap map_tw;          // tw as [M][16 parts], boxes of 64 columns x 8 rows
+    const __nv_bfloat16* tw;     // [M][parts][hi 8 | lo 8]: t 2^-e_m, zeros for a row without an adapter
+    const int* row_slot;         // [M] place of the row's adapter in its token tile's list, or -1
+    const int* tile_count;       // [num_t] distinct adapters of the token tile
+    const int* tile_list;        // [num_t][BT]
+    int r8;                      // r / 8
+    int parts;                   // parts per adapter: r8, in SwiGLU mode 2 r8
+};
+// Columns of a box of B: an extra step needs at most four parts of an adapter.
+__host__ __device__ constexpr int part_cols(int r8) { return r8 < 4 ? 8 * r8 : 32; }
+template <bool kLora> struct PickParams { using type = Params; };
+template <> struct PickParams<true> { using type = LoraParams; };
 
 __device__ __forceinline__ void tile_coords(int t, int num_w, int& t_blk, int& w_blk) {
     // weight tiles fastest: a wave of CTAs shares one or two activation row blocks
@@ -191,7 +195,7 @@ template <bool kBf16Out, class C, bool kSwiGLU = false, bool kSplitK = false, bo
 __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_codes,
     const __grid_constant__ CUtensorMap map_codes2, const __grid_constant__ CUtensorMap map_params,
-    const __grid_constant__ CUtensorMap map_y, const Params p) {
+    const __grid_constant__ CUtensorMap map_y, const __grid_constant__ typename PickParams<kLora>::type p) {
     constexpr int NX = C::kNX, NC = C::kNC;
     static_assert(!kSwiGLU || C::kBits == 4, "the SwiGLU pair is built for 4-bit codes");
     static_assert(!kSplitK || (!kSwiGLU && !kBf16Out), "split-K units write fp32 partials of a plain layer");
@@ -228,9 +232,18 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
             kb1 = p.G;
         }
     };
-    // Adapter mode: 8-column chunks of a unit's extra K-steps (0 unless the unit ends K), 8 chunks to a step.
-    auto lora_chunks = [&](int t_blk, int kb1) {
-        return kb1 == p.G ? p.lora.tile_count[t_blk] * p.lora.chunks : 0;
+    // Adapter mode: the extra K-steps of unit u are the parts [p0, p1) of its token tile, four to a step.  A tile's
+    // slices share them out like the groups of K.
+    auto lora_parts = [&](int u, int t_blk, int& p0, int& p1) {
+        p0 = p1 = 0;
+        if constexpr (kLora) {
+            p1 = p.tile_count[t_blk] * p.parts;
+            if constexpr (kSplitK) {
+                const int z = u / num_tiles, steps = (p1 + 3) / 4;
+                p0 = 4 * static_cast<int>((static_cast<int64_t>(z) * steps) / p.splits);
+                p1 = min(p1, 4 * static_cast<int>((static_cast<int64_t>(z + 1) * steps) / p.splits));
+            }
+        }
     };
     // Every role walks the same units in the same order: the X and A ring positions follow the K-step
     // count, the C ring position the code-stage count (a unit's steps in stages of kS, the last partial).
@@ -345,33 +358,45 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                 }
             }
             if constexpr (kLora) {
+                // extra K-steps: a code stage holds the step's boxes of B, one per adapter (and projection) that the
+                // step meets, each [256 rows][cols]; a thread's row gives 8 columns per part, twice (under hi and lo)
                 ptx::grid_dependency_wait();               // the tiles' adapter lists come from an earlier kernel
                 int t_blk, w_blk;
                 tile_coords(t, p.num_w, t_blk, w_blk);
-                const int nchunks = lora_chunks(t_blk, kb1);
-                const int r8 = p.lora.r / 8;
-                const int n = kSwiGLU ? w_blk * BWG + quarter * 32 + lane : w_blk * BW + r;
-                const int* list = p.lora.tile_list + static_cast<int64_t>(t_blk) * BT;
-                const __nv_bfloat16* up = kSwiGLU && grp == 1 ? p.lora.b[1] : p.lora.b[0];
-                int slot = 0, w = 0;                       // chunk position: adapter in the list, chunk in the adapter
-                for (int c8 = 0; c8 < nchunks && ok; c8 += 8, ++i) {
+                int p0, p1;
+                lora_parts(un, t_blk, p0, p1);
+                const int cols = part_cols(p.r8);
+                const bool inside = (kSwiGLU ? w_blk * BWG + quarter * 32 + lane : w_blk * BW + r) < p.N;
+                for (; p0 < p1 && ok; p0 += 4, ++i, ++ci) {
+                    int cs;
+                    uint32_t cph;
+                    ring_pos<NC>(ci, cs, cph);
+                    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&c_full[cs], cph, abort_flag))) { ok = false; break; }
+                    const uint8_t* box = smem + C::kOffC + cs * C::kCBytes + r * cols * 2;
+                    int seg = p0 / p.r8, part = p0 - seg * p.r8, skip = part;
                     uint32_t a[32];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        // chunk w is [hi | lo] of the plain layer, [gate hi | gate lo | up hi | up lo] of the pair: B's
-                        // columns 8 (w mod r8) .. +7 under both parts, zero under the other row group's
+                    for (int c = 0; c < 4; ++c) {
                         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (c8 + c < nchunks && n < p.N && (!kSwiGLU || (w >= 2 * r8) == (grp == 1))) {
-                            const int part = w % r8;
-                            v = __ldg(reinterpret_cast<const uint4*>(
-                                up + (static_cast<int64_t>(list[slot]) * p.N + n) * p.lora.r + 8 * part));
+                        if (inside && p0 + c < p1 && (!kSwiGLU || (seg & 1) == grp)) {
+                            v = *reinterpret_cast<const uint4*>(box + 16 * (part - skip));
+                            v.x = finite_bf16x2(v.x);
+                            v.y = finite_bf16x2(v.y);
+                            v.z = finite_bf16x2(v.z);
+                            v.w = finite_bf16x2(v.w);
                         }
-                        a[4 * c] = finite_bf16x2(v.x);
-                        a[4 * c + 1] = finite_bf16x2(v.y);
-                        a[4 * c + 2] = finite_bf16x2(v.z);
-                        a[4 * c + 3] = finite_bf16x2(v.w);
-                        if (++w == p.lora.chunks) { w = 0; ++slot; }
+                        a[8 * c] = a[8 * c + 4] = v.x;
+                        a[8 * c + 1] = a[8 * c + 5] = v.y;
+                        a[8 * c + 2] = a[8 * c + 6] = v.z;
+                        a[8 * c + 3] = a[8 * c + 7] = v.w;
+                        if (++part == p.r8) {              // on to the next adapter's box
+                            part = skip = 0;
+                            ++seg;
+                            box += BW * cols * 2;
+                        }
                     }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&c_empty[cs]);
                     if (i >= static_cast<uint32_t>(NA)) {
                         int xs;
                         uint32_t xph;
@@ -393,71 +418,89 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
     } else if (kLora && warp == kWarpTmaX) {
         // ---------------------------------------------------------------- activation producer, adapter mode
         test_delay(kDelayActivations);   // the checked build can hold this role back (qlinear_test_delay)
-        // As the TMA producer below; the whole warp writes the extra K-steps' tiles (192 tokens x 64 columns of
-        // t's bf16 parts) into the same ring, in the layout the TMA writes: row-major 128-byte rows, 16-byte pieces
-        // permuted by the row's number mod 8.
-        uint32_t i = 0;
-        bool ok = true;
-        ptx::grid_dependency_wait();
-        const int r8 = p.lora.r / 8;
-        for (int un = blockIdx.x; un < num_units && ok; un += gridDim.x) {
-            int t, kb0, kb1;
-            unit(un, t, kb0, kb1);
-            int t_blk, w_blk;
-            tile_coords(t, p.num_w, t_blk, w_blk);
-            for (int kb = kb0; kb < kb1; ++kb, ++i) {
-                int s;
-                uint32_t ph;
-                ring_pos<NX>(i, s, ph);
-                if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&x_empty[s], ph ^ 1, abort_flag))) { ok = false; break; }
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&x_full[s], kXBytes);
-                    ptx::tma_load_2d(smem + C::kOffX + s * kXBytes, &map_x, &x_full[s], kb * BK, t_blk * BT);
+        // As the TMA producer below, by a whole warp.  An extra K-step's tile is 192 tokens x 64 columns: a row's own
+        // parts of tw at its adapter's place in the tile's list, zero elsewhere.  Eight rows of one adapter (or none,
+        // whose tw is zero) are a box of tw shifted by that place, and the TMA's fill past either end of tw's row gives
+        // the zeros; 24 lanes issue a box each.  Eights with several adapters (where two requests meet, or tokens in
+        // no order) are copied by the warp, in the layout the TMA writes: 128-byte rows, 16-byte pieces permuted by
+        // the row's number mod 8.
+        if constexpr (kLora) {
+            constexpr int kEights = BT / 8;
+            uint32_t i = 0;
+            bool ok = true;
+            ptx::grid_dependency_wait();
+            const int width = 2 * p.parts;                     // 16-byte pieces of a row of tw
+            for (int un = blockIdx.x; un < num_units && ok; un += gridDim.x) {
+                int t, kb0, kb1, p0, p1;
+                unit(un, t, kb0, kb1);
+                int t_blk, w_blk;
+                tile_coords(t, p.num_w, t_blk, w_blk);
+                lora_parts(un, t_blk, p0, p1);
+                int own[BT / 32];                              // place of the adapter of row 32 j + lane, or -1
+                int eight = -1;                                // lane l < 24: the place shared by rows 8 l .. 8 l + 7
+                uint32_t mixed = 0;                            // the eights without one
+#pragma unroll
+                for (int j = 0; j < BT / 32; ++j) {
+                    const int m = t_blk * BT + 32 * j + lane;
+                    own[j] = p0 < p1 && m < p.M ? p.row_slot[m] : -1;
+                    int top = own[j];
+                    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    const uint32_t differ = __ballot_sync(0xFFFFFFFFu, own[j] >= 0 && own[j] != top);
+                    const int of_lane = __shfl_sync(0xFFFFFFFFu, top, 8 * (lane & 3));
+                    if ((lane >> 2) == j) eight = of_lane;
+                    for (int o = 0; o < 4; ++o)
+                        if ((differ >> (8 * o)) & 0xFFu) mixed |= 1u << (4 * j + o);
                 }
-                __syncwarp();
-            }
-            if (!ok) break;
-            const int nchunks = lora_chunks(t_blk, kb1);
-            int slot = 0, w = 0;
-            for (int c8 = 0; c8 < nchunks; c8 += 8, ++i) {
-                int s;
-                uint32_t ph;
-                ring_pos<NX>(i, s, ph);
-                if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&x_empty[s], ph ^ 1, abort_flag))) { ok = false; break; }
-                uint8_t* stage = smem + C::kOffX + s * kXBytes;
-                for (int q = lane; q < BT; q += 32) {
-                    const int64_t m = static_cast<int64_t>(t_blk) * BT + q;
-                    const int own = m < p.M ? p.lora.row_slot[m] : -1;
-                    // 2^-e_m, the inverse of the row's scale (a power of two, e_m in [-115, 112])
-                    const float inv = own >= 0 ? __uint_as_float(0x7F000000u - __float_as_uint(p.rowscale[m])) : 0.0f;
-                    int sl = slot, ww = w;
-                    for (int c = 0; c < 8; ++c) {
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (sl == own && c8 + c < nchunks) {
-                            const int which = ww / r8, part = ww - which * r8;
-                            const float4* src = reinterpret_cast<const float4*>(
-                                p.lora.t + ((kSwiGLU && which >= 2 ? static_cast<int64_t>(p.M) : 0) + m) * p.lora.r + 8 * part);
-                            const float4 t0 = src[0], t1 = src[1];
-                            const bool lo = (which & 1) != 0;
-                            v.x = bf16_part(t0.x * inv, t0.y * inv, lo);
-                            v.y = bf16_part(t0.z * inv, t0.w * inv, lo);
-                            v.z = bf16_part(t1.x * inv, t1.y * inv, lo);
-                            v.w = bf16_part(t1.z * inv, t1.w * inv, lo);
-                        }
-                        *reinterpret_cast<uint4*>(stage + q * 128 + ((c ^ (q & 7)) << 4)) = v;
-                        if (++ww == p.lora.chunks) { ww = 0; ++sl; }
+                for (int kb = kb0; kb < kb1; ++kb, ++i) {
+                    int s;
+                    uint32_t ph;
+                    ring_pos<NX>(i, s, ph);
+                    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&x_empty[s], ph ^ 1, abort_flag))) { ok = false; break; }
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(&x_full[s], kXBytes);
+                        ptx::tma_load_2d(smem + C::kOffX + s * kXBytes, &map_x, &x_full[s], kb * BK, t_blk * BT);
                     }
+                    __syncwarp();
                 }
-                for (int c = 0; c < 8; ++c)
-                    if (++w == p.lora.chunks) { w = 0; ++slot; }
-                ptx::fence_proxy_async_smem();             // visible to the MMAs' reads of shared memory
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&x_full[s]);
+                if (!ok) break;
+                for (; p0 < p1; p0 += 4, ++i) {
+                    int s;
+                    uint32_t ph;
+                    ring_pos<NX>(i, s, ph);
+                    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&x_empty[s], ph ^ 1, abort_flag))) { ok = false; break; }
+                    uint8_t* stage = smem + C::kOffX + s * kXBytes;
+                    if (lane == 0) ptx::mbar_expect_tx(&x_full[s], 1024u * static_cast<uint32_t>(kEights - __popc(mixed)));
+                    __syncwarp();
+                    if (lane < kEights && !((mixed >> lane) & 1u))
+                        ptx::tma_load_2d(stage + 1024 * lane, &p.map_tw, &x_full[s], 16 * p0 - 8 * width * max(eight, 0),
+                                         t_blk * BT + 8 * lane);
+                    const int c = lane & 7;
+                    for (uint32_t left = mixed; left != 0; left &= left - 1) {
+                        const int e = __ffs(left) - 1;
+                        int o = own[0];
+#pragma unroll
+                        for (int j = 1; j < BT / 32; ++j) o = (e >> 2) == j ? own[j] : o;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {          // four rows at a time, eight lanes each
+                            const int q = 8 * e + 4 * h + (lane >> 3);
+                            const int slot = __shfl_sync(0xFFFFFFFFu, o, q & 31);
+                            const int rel = 2 * p0 + c - slot * width;
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (slot >= 0 && static_cast<uint32_t>(rel) < static_cast<uint32_t>(width))
+                                v = __ldg(reinterpret_cast<const uint4*>(p.tw) +
+                                          (static_cast<int64_t>(t_blk) * BT + q) * width + rel);
+                            *reinterpret_cast<uint4*>(stage + q * 128 + ((c ^ (q & 7)) << 4)) = v;
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();             // visible to the MMAs' reads of shared memory
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&x_full[s]);
+                }
             }
-        }
-        if (lane == 0) {
-            for (uint32_t j = (i > static_cast<uint32_t>(NX) ? i - NX : 0u); j < i; ++j)
-                ptx::mbar_wait(&x_full[j % NX], (j / NX) & 1u, nullptr);
+            if (lane == 0) {
+                for (uint32_t j = (i > static_cast<uint32_t>(NX) ? i - NX : 0u); j < i; ++j)
+                    ptx::mbar_wait(&x_full[j % NX], (j / NX) & 1u, nullptr);
+            }
         }
     } else if (warp == kWarpTmaX) {
         // ---------------------------------------------------------------- TMA producer of activation tiles
@@ -508,6 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
             uint32_t ci = 0;
             bool ok = true, waited = false;
             int first_kc[NC], first_w[NC];
+            auto late_params = [&] {
+                ptx::grid_dependency_wait();
+#pragma unroll
+                for (int e = 0; e < NC; ++e)
+                    if (static_cast<uint32_t>(e) < ci)
+                        ptx::tma_load_2d(smem + C::kOffP + e * C::kPBytes, &map_params, &c_full[e], first_w[e] * BW,
+                                         first_kc[e]);
+                waited = true;
+            };
             for (int un = blockIdx.x; un < num_units && ok; un += gridDim.x) {
                 int t, kb0, kb1;
                 unit(un, t, kb0, kb1);
@@ -540,15 +592,31 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                         }
                     }
                 }
+                if constexpr (kLora) {
+                    // a code stage per extra K-step: a box of B for each adapter (and projection) the step meets
+                    if (!waited) late_params();
+                    int p0, p1;
+                    lora_parts(un, t_blk, p0, p1);
+                    const int cols = part_cols(p.r8);
+                    for (; ok && p0 < p1; p0 += 4, ++ci) {
+                        int s;
+                        uint32_t ph;
+                        ring_pos<NC>(ci, s, ph);
+                        const int seg0 = p0 / p.r8, seg1 = (min(p0 + 4, p1) - 1) / p.r8;
+                        const uint32_t box_bytes = static_cast<uint32_t>((kSwiGLU ? BWG : BW) * cols * 2);
+                        if (!ptx::mbar_wait(&c_empty[s], ph ^ 1, abort_flag)) { ok = false; break; }
+                        ptx::mbar_arrive_expect_tx(&c_full[s], (seg1 - seg0 + 1) * box_bytes);
+                        for (int seg = seg0; seg <= seg1; ++seg) {
+                            const int up = kSwiGLU ? seg & 1 : 0;
+                            const int adapter = p.tile_list[t_blk * BT + (kSwiGLU ? seg >> 1 : seg)];
+                            uint8_t* dst = smem + C::kOffC + s * C::kCBytes + (seg - seg0) * (BW * cols * 2) + up * box_bytes;
+                            ptx::tma_load_3d(dst, &p.map_b[up], &c_full[s], seg == seg0 ? 8 * (p0 - seg0 * p.r8) : 0,
+                                             w_blk * (kSwiGLU ? BWG : BW), adapter);
+                        }
+                    }
+                }
             }
-            if (!waited) {                             // fewer than NC stages in all
-                ptx::grid_dependency_wait();
-#pragma unroll
-                for (int e = 0; e < NC; ++e)
-                    if (static_cast<uint32_t>(e) < ci)
-                        ptx::tma_load_2d(smem + C::kOffP + e * C::kPBytes, &map_params, &c_full[e], first_w[e] * BW,
-                                         first_kc[e]);
-            }
+            if (!waited) late_params();                // fewer than NC stages in all
             for (uint32_t j = (ci > static_cast<uint32_t>(NC) ? ci - NC : 0u); j < ci; ++j)
                 ptx::mbar_wait(&c_full[j % NC], (j / NC) & 1u, nullptr);
         }
@@ -595,8 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                     constexpr uint32_t idesc_lora = ptx::idesc_f16(BWG, BT, true);
                     int t_blk, w_blk;
                     tile_coords(t, p.num_w, t_blk, w_blk);
-                    const int nchunks = ok ? lora_chunks(t_blk, kb1) : 0;
-                    for (int c8 = 0; c8 < nchunks; c8 += 8, ++i) {
+                    int p0, p1;
+                    lora_parts(un, t_blk, p0, p1);
+                    for (; ok && p0 < p1; p0 += 4, ++i) {
                         int xs;
                         uint32_t xph;
                         ring_pos<NX>(i, xs, xph);
@@ -605,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                         const uint32_t x_addr = ptx::smem_addr(smem + C::kOffX + xs * kXBytes);
                         const uint32_t d = tmem_base + kAccCol + static_cast<uint32_t>(gsel * BT);
                         const uint32_t a_tm = tmem_base + kAStageCol + 64u * static_cast<uint32_t>(i % NA) + 32u * gsel;
-                        const int nu = min(BK / UK, (nchunks - c8) / 2);        // 16-column MMAs of this step
+                        const int nu = min(BK / UK, p1 - p0);               // one 16-column MMA per part
                         for (int u = 0; u < nu; ++u)
                             ptx::mma_f16_ts(d, a_tm + u * (UK / 2), ptx::sdesc_sw128(x_addr + u * UK * 2), idesc_lora, 1u);
                         ptx::mma_commit(&x_empty[xs]);

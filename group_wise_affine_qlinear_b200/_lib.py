@@ -1,7 +1,6 @@
 """ctypes marshalling for libqlinear.so (see include/qlinear.h for the contract)."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -329,41 +328,48 @@ def swiglu(x: torch.Tensor, gate, up, out: torch.Tensor | None = None, workspace
     return out
 
 
+def _fit(dev: int, *specs) -> bool:
+    """Whether every tensor of the (tensor, dtype, shape) specs is contiguous, of that type and shape, on CUDA device
+    `dev`: the one pass of a call whose arguments are right.  Where it fails, the checks by name say what is wrong."""
+    for t, dtype, shape in specs:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
 def _same_device(dev: torch.device, tensors) -> None:
     for name, t in tensors:
         if t is not None and t.device != dev:
             raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
-@contextlib.contextmanager
-def _call_context(dev: torch.device, stream):
-    """The call's device made current, its stream made current too: a buffer allocated inside belongs to it."""
+def _on_stream(dev: int, stream, call):
+    """call(raw stream handle) with device `dev` current; a given stream is current too, so that a buffer allocated
+    inside belongs to it."""
+    if stream is None and torch.cuda.current_device() == dev:
+        return call(torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
-        st = torch.cuda.current_stream() if stream is None else stream
         if stream is None:
-            yield st.cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield st.cuda_stream
+            return call(torch._C._cuda_getCurrentRawStream(dev))
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
-def _workspace(workspace: torch.Tensor | None, need: int, dev: torch.device) -> torch.Tensor:
+def _need_workspace(workspace: torch.Tensor | None, dev: torch.device) -> None:
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if not workspace.is_cuda or workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
+        return
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev:
+        raise ValueError(f"workspace must be a tensor on {dev}")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace
 
 
-def _need_adapters(a: torch.Tensor, b: torch.Tensor, K: int, N: int, what: str = "lora") -> tuple[int, int]:
+def _adapter_shape(a: torch.Tensor, b: torch.Tensor, what: str) -> tuple[int, int]:
+    """(adapters, rank) of lora_a [L][r][K] and lora_b [L][N][r]."""
     for name, t in ((what + "_a", a), (what + "_b", b)):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             raise ValueError(f"{name} must be a tensor of three dimensions")
-    n, r = a.shape[0], a.shape[1]
-    _need_cuda(a, what + "_a", torch.bfloat16, (n, r, K))
-    _need_cuda(b, what + "_b", torch.bfloat16, (n, N, r))
+    n, r, _ = a.shape
     if n < 1 or r < 8 or r % 8 or r > LORA_MAX_RANK:
         raise ValueError(f"{what}_a: at least one adapter, of a rank that is a multiple of 8 up to {LORA_MAX_RANK}")
     return n, r
@@ -411,30 +417,40 @@ def _forward_lora(x, codes, scales, biases, lora_a, lora_b, ids, lora_scale, out
     L = lib()
     N, K = _weights_shape(codes, scales, bits)
     M = x.shape[0]
-    _need_cuda(x, "x", torch.bfloat16, (M, K))
-    _need_cuda(codes, "codes", torch.int32, (N, K * bits // 32))
-    _need_cuda(scales, "scales", torch.float16, (N, K // GROUP))
-    _need_cuda(biases, "biases", torch.float16, (N, K // GROUP))
-    n, r = _need_adapters(lora_a, lora_b, K, N)
-    _need_rows(ids, lora_scale, M, n)
+    n, r = _adapter_shape(lora_a, lora_b, "lora")
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out_dtype must be bfloat16 or float32")
-    if out is not None:
-        _need_cuda(out, "out", out_dtype, (M, N))
-    dev = x.device
-    _same_device(dev, (("codes", codes), ("scales", scales), ("biases", biases), ("lora_a", lora_a),
-                       ("lora_b", lora_b), ("adapter_ids", ids), ("lora_scale", lora_scale), ("out", out)))
+    dev = x.get_device()
+    if not (dev >= 0 and _fit(dev, (x, torch.bfloat16, (M, K)), (codes, torch.int32, (N, K * bits // 32)),
+                              (scales, torch.float16, (N, K // GROUP)), (biases, torch.float16, (N, K // GROUP)),
+                              (lora_a, torch.bfloat16, (n, r, K)), (lora_b, torch.bfloat16, (n, N, r)),
+                              (ids, torch.int32, (M,))) and
+            (out is None or _fit(dev, (out, out_dtype, (M, N)))) and
+            (lora_scale is None or _fit(dev, (lora_scale, torch.float32, (n,))))):
+        _need_cuda(x, "x", torch.bfloat16, (M, K))
+        _need_cuda(codes, "codes", torch.int32, (N, K * bits // 32))
+        _need_cuda(scales, "scales", torch.float16, (N, K // GROUP))
+        _need_cuda(biases, "biases", torch.float16, (N, K // GROUP))
+        _need_cuda(lora_a, "lora_a", torch.bfloat16, (n, r, K))
+        _need_cuda(lora_b, "lora_b", torch.bfloat16, (n, N, r))
+        _need_rows(ids, lora_scale, M, n)
+        if out is not None:
+            _need_cuda(out, "out", out_dtype, (M, N))
+        _same_device(x.device, (("codes", codes), ("scales", scales), ("biases", biases), ("lora_a", lora_a),
+                                ("lora_b", lora_b), ("adapter_ids", ids), ("lora_scale", lora_scale), ("out", out)))
+    _need_workspace(workspace, x.device)
     name = "qlinear_lora_forward" if bits == 4 else "qlinear8_lora_forward"
-    with _call_context(dev, stream) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        ws = _workspace(workspace, lora_workspace_size(M, K, N, n, r, bits) if workspace is None else 0, dev)
-        s = getattr(L, name)(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(), lora_a.data_ptr(),
-                             lora_b.data_ptr(), _ptr(lora_scale), ids.data_ptr(), out.data_ptr(),
-                             _BF16 if out_dtype == torch.bfloat16 else _F32, M, K, N, GROUP, n, r, ws.data_ptr(),
-                             ws.numel() * ws.element_size(), st)
-    _check(s, name)
-    return out
+
+    def call(st):
+        y = x.new_empty((M, N), dtype=out_dtype) if out is None else out
+        ws = (x.new_empty(lora_workspace_size(M, K, N, n, r, bits), dtype=torch.uint8) if workspace is None
+              else workspace)
+        _check(getattr(L, name)(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(),
+                                lora_a.data_ptr(), lora_b.data_ptr(), _ptr(lora_scale), ids.data_ptr(), y.data_ptr(),
+                                _BF16 if out_dtype == torch.bfloat16 else _F32, M, K, N, GROUP, n, r, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), st), name)
+        return y
+    return _on_stream(dev, stream, call)
 
 
 def swiglu_lora_workspace_size(M: int, K: int, I: int, adapters: int, rank: int) -> int:
@@ -460,35 +476,47 @@ def swiglu_lora(x: torch.Tensor, gate, up, gate_lora, up_lora, adapter_ids: torc
     ua, ubb = up_lora
     I, K = _weights_shape(gc, gs)
     M = x.shape[0]
-    _need_cuda(x, "x", torch.bfloat16, (M, K))
-    for name, c, s, b in (("gate", gc, gs, gb), ("up", uc, us, ub)):
-        _need_cuda(c, name + " codes", torch.int32, (I, K // 8))
-        _need_cuda(s, name + " scales", torch.float16, (I, K // GROUP))
-        _need_cuda(b, name + " biases", torch.float16, (I, K // GROUP))
-    n, r = _need_adapters(ga, gbb, K, I, "gate_lora")
-    if _need_adapters(ua, ubb, K, I, "up_lora") != (n, r):
-        raise ValueError("gate_lora and up_lora must hold the same number of adapters of the same rank")
-    _need_rows(adapter_ids, lora_scale, M, n)
+    n, r = _adapter_shape(ga, gbb, "gate_lora")
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out_dtype must be bfloat16 or float32")
-    if out is not None:
-        _need_cuda(out, "out", out_dtype, (M, I))
-    dev = x.device
-    _same_device(dev, (("gate codes", gc), ("gate scales", gs), ("gate biases", gb), ("up codes", uc),
-                       ("up scales", us), ("up biases", ub), ("gate_lora_a", ga), ("gate_lora_b", gbb),
-                       ("up_lora_a", ua), ("up_lora_b", ubb), ("adapter_ids", adapter_ids),
-                       ("lora_scale", lora_scale), ("out", out)))
-    with _call_context(dev, stream) as st:
-        if out is None:
-            out = torch.empty((M, I), dtype=out_dtype, device=dev)
-        ws = _workspace(workspace, swiglu_lora_workspace_size(M, K, I, n, r) if workspace is None else 0, dev)
-        s = L.qlinear_swiglu_lora_forward(x.data_ptr(), gc.data_ptr(), gs.data_ptr(), gb.data_ptr(), uc.data_ptr(),
-                                          us.data_ptr(), ub.data_ptr(), ga.data_ptr(), gbb.data_ptr(), ua.data_ptr(),
-                                          ubb.data_ptr(), _ptr(lora_scale), adapter_ids.data_ptr(), out.data_ptr(),
-                                          _BF16 if out_dtype == torch.bfloat16 else _F32, M, K, I, GROUP, n, r,
-                                          ws.data_ptr(), ws.numel() * ws.element_size(), st)
-    _check(s, "qlinear_swiglu_lora_forward")
-    return out
+    dev = x.get_device()
+    wc, wp = (I, K // 8), (I, K // GROUP)
+    if not (dev >= 0 and _fit(dev, (x, torch.bfloat16, (M, K)), (gc, torch.int32, wc), (gs, torch.float16, wp),
+                              (gb, torch.float16, wp), (uc, torch.int32, wc), (us, torch.float16, wp),
+                              (ub, torch.float16, wp), (ga, torch.bfloat16, (n, r, K)), (gbb, torch.bfloat16, (n, I, r)),
+                              (ua, torch.bfloat16, (n, r, K)), (ubb, torch.bfloat16, (n, I, r)),
+                              (adapter_ids, torch.int32, (M,))) and
+            (out is None or _fit(dev, (out, out_dtype, (M, I)))) and
+            (lora_scale is None or _fit(dev, (lora_scale, torch.float32, (n,))))):
+        _need_cuda(x, "x", torch.bfloat16, (M, K))
+        for name, c, s, b in (("gate", gc, gs, gb), ("up", uc, us, ub)):
+            _need_cuda(c, name + " codes", torch.int32, wc)
+            _need_cuda(s, name + " scales", torch.float16, wp)
+            _need_cuda(b, name + " biases", torch.float16, wp)
+        for name, a, b in (("gate_lora", ga, gbb), ("up_lora", ua, ubb)):
+            _need_cuda(a, name + "_a", torch.bfloat16, (n, r, K))
+            _need_cuda(b, name + "_b", torch.bfloat16, (n, I, r))
+        _need_rows(adapter_ids, lora_scale, M, n)
+        if out is not None:
+            _need_cuda(out, "out", out_dtype, (M, I))
+        _same_device(x.device, (("gate codes", gc), ("gate scales", gs), ("gate biases", gb), ("up codes", uc),
+                                ("up scales", us), ("up biases", ub), ("gate_lora_a", ga), ("gate_lora_b", gbb),
+                                ("up_lora_a", ua), ("up_lora_b", ubb), ("adapter_ids", adapter_ids),
+                                ("lora_scale", lora_scale), ("out", out)))
+    _need_workspace(workspace, x.device)
+
+    def call(st):
+        h = x.new_empty((M, I), dtype=out_dtype) if out is None else out
+        ws = (x.new_empty(swiglu_lora_workspace_size(M, K, I, n, r), dtype=torch.uint8) if workspace is None
+              else workspace)
+        _check(L.qlinear_swiglu_lora_forward(x.data_ptr(), gc.data_ptr(), gs.data_ptr(), gb.data_ptr(), uc.data_ptr(),
+                                             us.data_ptr(), ub.data_ptr(), ga.data_ptr(), gbb.data_ptr(), ua.data_ptr(),
+                                             ubb.data_ptr(), _ptr(lora_scale), adapter_ids.data_ptr(), h.data_ptr(),
+                                             _BF16 if out_dtype == torch.bfloat16 else _F32, M, K, I, GROUP, n, r,
+                                             ws.data_ptr(), ws.numel() * ws.element_size(), st),
+               "qlinear_swiglu_lora_forward")
+        return h
+    return _on_stream(dev, stream, call)
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
@@ -517,8 +545,8 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: 
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a tensor [M][D]")
     M, D = x.shape
+    xd = x.dtype
     xt = _dtype_code(x, "x")
-    _need_cuda(x, "x", x.dtype, (M, D))
     S, yt = 1, _BF16
     if y is not None:
         if not isinstance(y, torch.Tensor) or y.dim() not in (2, 3):
@@ -528,47 +556,58 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: 
             if yt == _BF16:
                 raise ValueError("partials y [S][M][D] must be float32")
             S = y.shape[0]
-        _need_cuda(y, "y", y.dtype, (M, D) if y.dim() == 2 else (S, M, D))
     elif post_weight is not None or gate is not None or out is not None:
         raise ValueError("post_weight, gate and out need y")
     if not post_norm and post_weight is not None:
         raise ValueError("post_weight needs post_norm")
-    if not pre_norm and not (pre_weight is None and scale is None and shift is None and h is None):
-        raise ValueError("pre_weight, scale, shift and h need pre_norm")
-    if y is None and not pre_norm:
-        raise ValueError("nothing to compute: no y and no pre_norm")
-    vectors = [(n, t) for n, t in (("post_weight", post_weight), ("pre_weight", pre_weight), ("gate", gate),
-                                   ("scale", scale), ("shift", shift)) if t is not None]
-    pt = _dtype_code(vectors[0][1], vectors[0][0]) if vectors else _BF16
-    T = None
-    for name, t in vectors:
-        if name.endswith("weight"):
-            _need_cuda(t, name, vectors[0][1].dtype, (D,))
+    if not pre_norm:
+        if not (pre_weight is None and scale is None and shift is None and h is None):
+            raise ValueError("pre_weight, scale, shift and h need pre_norm")
+        if y is None:
+            raise ValueError("nothing to compute: no y and no pre_norm")
+    # (name, tensor, dtype, shape) of everything given; T is the number of segments, P the vectors' type
+    T = P = None
+    given = [("x", x, xd, (M, D))]
+    if y is not None:
+        given.append(("y", y, y.dtype, (M, D) if y.dim() == 2 else (S, M, D)))
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight), ("gate", gate), ("scale", scale),
+                    ("shift", shift)):
+        if t is None:
+            continue
+        if P is None:
+            P = t.dtype
+            pt = _dtype_code(t, name)
+        if name[-6:] == "weight":
+            given.append((name, t, P, (D,)))
         else:
-            T = t.shape[0] if T is None else T
-            _need_cuda(t, name, vectors[0][1].dtype, (T, D))
+            if T is None:
+                T = t.shape[0]
+            given.append((name, t, P, (T, D)))
     if segment_ids is not None:
-        _need_cuda(segment_ids, "segment_ids", torch.int32, (M,))
+        given.append(("segment_ids", segment_ids, torch.int32, (M,)))
     elif T is not None and T != 1:
         raise ValueError("gate, scale and shift of several segments need segment_ids")
     if out is not None:
-        _need_cuda(out, "out", x.dtype, (M, D))
+        given.append(("out", out, xd, (M, D)))
     if h is not None:
-        _need_cuda(h, "h", torch.bfloat16, (M, D))
-    dev = x.device
-    _same_device(dev, vectors + [("y", y), ("segment_ids", segment_ids), ("out", out), ("h", h)])
-    with _call_context(dev, stream) as st:
-        if y is not None and out is None:
-            out = torch.empty_like(x)
-        if pre_norm and h is None:
-            h = torch.empty((M, D), dtype=torch.bfloat16, device=dev)
+        given.append(("h", h, torch.bfloat16, (M, D)))
+    dev = x.get_device()
+    for name, t, dtype, shape in given:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            _need_cuda(t, name, dtype, shape)
+            _same_device(x.device, ((name, t),))
+
+    def call(st):
+        r = x.new_empty((M, D)) if y is not None and out is None else out
+        n = x.new_empty((M, D), dtype=torch.bfloat16) if pre_norm and h is None else h
         # without per-segment vectors every segment is as good as any other
-        s = L.qlinear_norm_residual(x.data_ptr(), xt, _ptr(y), yt, S, int(post_norm), _ptr(post_weight), _ptr(gate),
-                                    residual_scale, branch_scale, _ptr(pre_weight), _ptr(scale), _ptr(shift), pt,
-                                    _ptr(segment_ids), 2 ** 31 - 1 if T is None else T, eps, _ptr(out), _ptr(h), M, D,
-                                    st)
-    _check(s, "qlinear_norm_residual")
-    return (x if y is None else out), h
+        _check(L.qlinear_norm_residual(x.data_ptr(), xt, _ptr(y), yt, S, 1 if post_norm else 0, _ptr(post_weight),
+                                       _ptr(gate), residual_scale, branch_scale, _ptr(pre_weight), _ptr(scale),
+                                       _ptr(shift), _BF16 if P is None else pt, _ptr(segment_ids),
+                                       2 ** 31 - 1 if T is None else T, eps, _ptr(r), _ptr(n), M, D, st),
+               "qlinear_norm_residual")
+        return (x if y is None else r), n
+    return _on_stream(dev, stream, call)
 
 
 def reduce_partials(partials: torch.Tensor, out: torch.Tensor | None = None, out_dtype=torch.bfloat16,

@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "ql_common.cuh"
 #include "ql_dequant.cuh"
@@ -73,7 +74,10 @@ struct DeviceInfo {
 
 template <int NT, int B>
 cudaError_t skinny_smem_attr() {
-    return cudaFuncSetAttribute(skinny::skinny_kernel<NT, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(skinny::skinny_kernel<NT, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               skinny::Layout<NT, B>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(skinny::skinny_kernel<NT, B, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 skinny::Layout<NT, B>::kSmemBytes);
 }
 
@@ -415,54 +419,56 @@ struct LoraArgs {
     int L = 0, r = 0, pairs = 1;
 };
 struct LoraPlan {
-    int S = 1, passes = 1, nt = 1, chunks = 1;      // launch shape of the shrink kernel
+    int S = 1, passes = 1, nt = 1, chunks = 1;      // fused path: launch shape of the first product's kernel
+    int per_tile = 1, slices = 1;                   // weight-streaming path: its tasks
     size_t off_t = 0, off_slot = 0, off_count = 0, off_list = 0, workspace = 0;
 };
 
-// The shrink kernel's tiles of 16 rows (32 on the fused path) alone fill the GPU only from a few thousand rows on.
-// Below, a cluster of up to 8 CTAs shares a tile's K range, on the weight-streaming path the rank is cut into narrower
-// chunks, and a tile's distinct adapters go to up to 16 CTAs, each as far as it keeps the launch near two CTAs per SM.
-LoraPlan lora_plan(int64_t M, int64_t K, int r, int L, int pairs, bool fused_path, size_t base, int sm_count) {
+// Weight-streaming path: about as many one-warp tasks as the main kernel has drain warps (4 per SM), by cutting K into
+// up to 32 slices of at least four 32-column blocks.
+LoraPlan lora_plan_streaming(int64_t M, int64_t K, int r, int L, size_t base, int sm_count) {
     LoraPlan lp;
-    const int rows = fused_path ? 2 * lora::kTile : lora::kTile;
+    const int64_t tiles = (M + lora::kTile - 1) / lora::kTile;
+    lp.per_tile = static_cast<int>(std::min<int64_t>(std::min<int64_t>(L, M), lora::kTile));
+    lp.chunks = (r + 15) / 16;
+    const int64_t tasks = tiles * lp.per_tile * lp.chunks;
+    lp.slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({32, 4 * sm_count / tasks, K / 128})));
+    lp.off_t = round_up(base, 256);
+    lp.workspace = lp.off_t + round_up(static_cast<size_t>(lp.slices) * M * r * 4, 256);
+    return lp;
+}
+
+// Fused path: the first product's tiles of 32 rows alone fill the GPU only from a few thousand rows on.  Below, a
+// cluster of up to 8 CTAs shares a tile's K range, and a tile's distinct adapters go to up to 16 CTAs.
+LoraPlan lora_plan_fused(int64_t M, int64_t K, int r, int L, int pairs, size_t base, int sm_count) {
+    LoraPlan lp;
+    const int rows = 2 * lora::kTile;
     const int64_t tiles = (M + rows - 1) / rows;
     const int64_t want = 2 * sm_count;
     const int r8 = r / 8;
     lp.nt = r8 >= 3 ? 4 : r8;
-    int64_t ctas = tiles * pairs * ((r8 + lp.nt - 1) / lp.nt);
+    lp.chunks = (r8 + lp.nt - 1) / lp.nt;
+    const int64_t ctas = tiles * pairs * lp.chunks;
     // at least two 32-column blocks of K per warp and CTA
     while (lp.S < lora::kMaxSplit && ctas * lp.S < want && K / 32 >= 2 * lora::kWarps * 2 * lp.S) lp.S *= 2;
-    while (!fused_path && lp.nt > 1 && ctas * lp.S * 2 <= want) {
-        lp.nt /= 2;
-        ctas = tiles * pairs * ((r8 + lp.nt - 1) / lp.nt);
-    }
-    lp.chunks = (r8 + lp.nt - 1) / lp.nt;
     while (lp.passes < std::min(L, rows) && ctas * lp.S * lp.passes < want) ++lp.passes;
     if (M <= 512) lp.passes = std::min(L, lora::kTile);
     lp.off_t = round_up(base, 256);
-    // t: fp32 [M][r], or on the fused path two bf16 parts per pair member
-    lp.off_slot = lp.off_t + round_up(static_cast<size_t>(pairs) * M * r * 4, 256);
-    lp.workspace = lp.off_slot;
-    if (fused_path) {
-        const size_t num_t = static_cast<size_t>((M + fused::BT - 1) / fused::BT);
-        lp.off_count = lp.off_slot + round_up(static_cast<size_t>(M) * 4, 256);
-        lp.off_list = lp.off_count + round_up(num_t * 4, 256);
-        lp.workspace = lp.off_list + round_up(num_t * fused::BT * 4, 256);
-    }
+    const size_t num_t = static_cast<size_t>((M + fused::BT - 1) / fused::BT);
+    lp.off_slot = lp.off_t + round_up(static_cast<size_t>(pairs) * M * r * 4, 256);     // two bf16 parts of t
+    lp.off_count = lp.off_slot + round_up(static_cast<size_t>(M) * 4, 256);
+    lp.off_list = lp.off_count + round_up(num_t * 4, 256);
+    lp.workspace = lp.off_list + round_up(num_t * fused::BT * 4, 256);
     return lp;
 }
 
-template <int MT, bool kConvert>
-cudaError_t launch_shrink_nt(int nt, const cudaLaunchConfig_t& cfg, const lora::ShrinkParams& p) {
-    switch (nt) {
-        case 1: return cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<1, MT, kConvert>, p);
-        case 2: return cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<2, MT, kConvert>, p);
-        default: return cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<4, MT, kConvert>, p);
-    }
+LoraPlan lora_plan(const Plan& pl, int64_t M, int64_t K, int r, int L, int sm_count) {
+    return pl.path == QL_PATH_TC_FUSED ? lora_plan_fused(M, K, r, L, 1, pl.workspace, sm_count)
+                                       : lora_plan_streaming(M, K, r, L, pl.workspace, sm_count);
 }
 
-// t = s x . A^T of every row's adapter.  xh != null: the fused path's form, which also converts the activations and
-// lists the token tiles' adapters, launched behind the parameter transpose under programmatic dependent launch.
+// Fused path: t of every row's adapter, the converted activations and the token tiles' adapter lists, launched behind
+// the parameter transpose under programmatic dependent launch.
 ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, int64_t M, int64_t K, uint8_t* ws,
                         __half* xh, float* rowscale, int bits, cudaStream_t st) {
     lora::ShrinkParams p = {};
@@ -477,20 +483,15 @@ ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, i
     p.passes = lp.passes;
     p.chunks = lp.chunks;
     p.pairs = la.pairs;
-    const int rows = xh ? 2 * lora::kTile : lora::kTile;
-    p.tiles = static_cast<int>((M + rows - 1) / rows);
-    if (xh) {
-        p.tw = reinterpret_cast<__nv_bfloat16*>(ws + lp.off_t);
-        p.xh = xh;
-        p.rowscale = rowscale;
-        p.bits = bits;
-        p.row_slot = reinterpret_cast<int*>(ws + lp.off_slot);
-        p.tile_count = reinterpret_cast<int*>(ws + lp.off_count);
-        p.tile_list = reinterpret_cast<int*>(ws + lp.off_list);
-        p.num_t = static_cast<int>((M + fused::BT - 1) / fused::BT);
-    } else {
-        p.t = reinterpret_cast<float*>(ws + lp.off_t);
-    }
+    p.tiles = static_cast<int>((M + 2 * lora::kTile - 1) / (2 * lora::kTile));
+    p.tw = reinterpret_cast<__nv_bfloat16*>(ws + lp.off_t);
+    p.xh = xh;
+    p.rowscale = rowscale;
+    p.bits = bits;
+    p.row_slot = reinterpret_cast<int*>(ws + lp.off_slot);
+    p.tile_count = reinterpret_cast<int*>(ws + lp.off_count);
+    p.tile_list = reinterpret_cast<int*>(ws + lp.off_list);
+    p.num_t = static_cast<int>((M + fused::BT - 1) / fused::BT);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.tiles) * lp.passes + p.num_t, lp.S, lp.chunks * la.pairs);
     cfg.blockDim = dim3(lora::kThreads);
@@ -503,8 +504,10 @@ ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, i
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = xh ? 2 : 1;
-    const cudaError_t e = xh ? launch_shrink_nt<2, true>(lp.nt, cfg, p) : launch_shrink_nt<1, false>(lp.nt, cfg, p);
+    cfg.numAttrs = 2;
+    const cudaError_t e = lp.nt == 1   ? cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<1>, p)
+                          : lp.nt == 2 ? cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<2>, p)
+                                       : cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<4>, p);
     return e == cudaSuccess ? QL_OK : QL_ERR_CUDA;
 }
 
@@ -649,6 +652,17 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
     return launch_status();
 }
 
+// Launches the weight-streaming kernel, with or without adapters.
+template <int NT, int B>
+ql_status launch_skinny(dim3 grid, cudaStream_t st, const CUtensorMap& mc, const CUtensorMap& mx, const CUtensorMap& ms,
+                        const CUtensorMap& mb, const skinny::LoraParams& p, bool with_lora) {
+    if (with_lora)
+        return launch_dependent(skinny::skinny_kernel<NT, B, true>, grid, skinny::kThreads,
+                                skinny::Layout<NT, B>::kSmemBytes, st, mc, mx, ms, mb, p);
+    return launch_dependent(skinny::skinny_kernel<NT, B>, grid, skinny::kThreads, skinny::Layout<NT, B>::kSmemBytes, st,
+                            mc, mx, ms, mb, static_cast<const skinny::Params&>(p));
+}
+
 ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
                      void* y, bool bf16_out, int64_t M, int64_t K, int64_t N, void* ws, cudaStream_t st,
                      int sm_count, const LoraArgs* la = nullptr, const LoraPlan* lp = nullptr) {
@@ -678,7 +692,11 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
                            CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK)
             return s;
     }
-    skinny::Params p;
+    skinny::LoraParams p = {};
+    if (la)
+        p.dot = {static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(la->a[0]), la->ids,
+                 reinterpret_cast<float*>(wsb + lp->off_t), static_cast<int>(M), static_cast<int>(K), la->r, la->L,
+                 lp->per_tile, lp->chunks, lp->slices};
     p.param_tma = param_tma ? 1 : 0;
     p.partial = reinterpret_cast<float*>(wsb);
     p.scales = static_cast<const __half*>(scales);
@@ -694,41 +712,25 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
     p.partial_elems = static_cast<int64_t>(pl.ctas) * pl.segmax * M * skinny::BW;
     // row exponents and scaled, reordered f16 activations (one cluster of CTAs per row)
     const dim3 pre_grid(static_cast<unsigned>(skinny::kPrepCluster), static_cast<unsigned>(M));
-    if (la) {
-        // the adapters' first product, then the prepass beside it
-        if ((s = launch_shrink(*la, *lp, x, M, K, wsb, nullptr, nullptr, bits, st)) != QL_OK) return s;
-        auto pre = bits == 4 ? skinny::skinny_prepass_kernel<4, true> : skinny::skinny_prepass_kernel<8, true>;
-        if ((s = launch_dependent(pre, pre_grid, skinny::kPrepThreads, 0, st, static_cast<const uint4*>(x),
-                                  static_cast<uint4*>(xp), rowexp, static_cast<int>(K))) != QL_OK)
-            return s;
-    } else if (bits == 4) {
+    if (bits == 4)
         skinny::skinny_prepass_kernel<4><<<pre_grid, skinny::kPrepThreads, 0, st>>>(
             static_cast<const uint4*>(x), static_cast<uint4*>(xp), rowexp, static_cast<int>(K));
-    } else {
+    else
         skinny::skinny_prepass_kernel<8><<<pre_grid, skinny::kPrepThreads, 0, st>>>(
             static_cast<const uint4*>(x), static_cast<uint4*>(xp), rowexp, static_cast<int>(K));
-    }
     if ((s = launch_status()) != QL_OK) return s;
     prof_begin(st);
     const dim3 sgrid(static_cast<unsigned>(pl.ctas));
-    if (bits == 4 && pl.nt == 16)
-        s = launch_dependent(skinny::skinny_kernel<16, 4>, sgrid, skinny::kThreads, skinny::Layout<16, 4>::kSmemBytes, st,
-                             mc, mx, ms, mb, p);
-    else if (bits == 4 && pl.nt == 32)
-        s = launch_dependent(skinny::skinny_kernel<32, 4>, sgrid, skinny::kThreads, skinny::Layout<32, 4>::kSmemBytes, st,
-                             mc, mx, ms, mb, p);
-    else if (bits == 4)
-        s = launch_dependent(skinny::skinny_kernel<64, 4>, sgrid, skinny::kThreads, skinny::Layout<64, 4>::kSmemBytes, st,
-                             mc, mx, ms, mb, p);
-    else if (pl.nt == 16)
-        s = launch_dependent(skinny::skinny_kernel<16, 8>, sgrid, skinny::kThreads, skinny::Layout<16, 8>::kSmemBytes, st,
-                             mc, mx, ms, mb, p);
-    else if (pl.nt == 32)
-        s = launch_dependent(skinny::skinny_kernel<32, 8>, sgrid, skinny::kThreads, skinny::Layout<32, 8>::kSmemBytes, st,
-                             mc, mx, ms, mb, p);
-    else
-        s = launch_dependent(skinny::skinny_kernel<64, 8>, sgrid, skinny::kThreads, skinny::Layout<64, 8>::kSmemBytes, st,
-                             mc, mx, ms, mb, p);
+    auto launch = [&](auto nt, auto b) {
+        return launch_skinny<decltype(nt)::value, decltype(b)::value>(sgrid, st, mc, mx, ms, mb, p, la != nullptr);
+    };
+    using std::integral_constant;
+    const auto launch_bits = [&](auto nt) {
+        return bits == 4 ? launch(nt, integral_constant<int, 4>{}) : launch(nt, integral_constant<int, 8>{});
+    };
+    s = pl.nt == 16   ? launch_bits(integral_constant<int, 16>{})
+        : pl.nt == 32 ? launch_bits(integral_constant<int, 32>{})
+                      : launch_bits(integral_constant<int, 64>{});
     if (s != QL_OK) return s;
     prof_end(st);
     const float* part = p.partial;
@@ -737,7 +739,9 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
     if (la) {
         lora::ExpandParams ep;
         ep.b = static_cast<const __nv_bfloat16*>(la->b[0]);
-        ep.t = reinterpret_cast<const float*>(wsb + lp->off_t);
+        ep.scale = la->scale;
+        ep.tp = reinterpret_cast<const float*>(wsb + lp->off_t);
+        ep.slices = lp->slices;
         ep.ids = la->ids;
         ep.r = la->r;
         ep.L = la->L;
@@ -752,8 +756,8 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
                              p.units, pl.ctas, pl.segmax, p.partial_elems);
     if (s != QL_OK) return s;
     (void)sm_count;
-    set_dispatch("path=tc_skinny%s bits=%d nt=%d ctas=%d segmax=%d units=%lld launches=%d why=%s", la ? "_lora" : "", bits,
-                 pl.nt, pl.ctas, pl.segmax, static_cast<long long>(pl.units), la ? 4 : 3, pl.why);
+    set_dispatch("path=tc_skinny%s bits=%d nt=%d ctas=%d segmax=%d units=%lld launches=3 why=%s", la ? "_lora" : "", bits,
+                 pl.nt, pl.ctas, pl.segmax, static_cast<long long>(pl.units), pl.why);
     return launch_status();
 }
 
@@ -889,7 +893,7 @@ ql_status swiglu_impl(const void* x, const uint32_t* gc, const void* gs, const v
     size_t need = pl.workspace;
     if (la) {
         if ((s = device_info(&dev)) != QL_OK) return s;
-        lp = lora_plan(M, K, la->r, la->L, 2, true, pl.workspace, dev->sm_count);
+        lp = lora_plan_fused(M, K, la->r, la->L, 2, pl.workspace, dev->sm_count);
         need = lp.workspace;
     }
     if (!workspace || workspace_bytes < need) return QL_ERR_WORKSPACE;
@@ -929,7 +933,7 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
     LoraPlan lp;
     size_t need = pl.workspace;
     if (la) {
-        lp = lora_plan(M, K, la->r, la->L, 1, pl.path == QL_PATH_TC_FUSED, pl.workspace, dev->sm_count);
+        lp = lora_plan(pl, M, K, la->r, la->L, dev->sm_count);
         need = lp.workspace;
     }
     if (need > 0) {
@@ -967,7 +971,7 @@ size_t lora_workspace_impl(int64_t M, int64_t K, int64_t N, int32_t group, int32
     if (device_info(&dev) == QL_OK) sms = dev->sm_count;
     Plan pl;
     if (make_plan(M, K, N, QL_PATH_AUTO, 0, sms, bits, &pl) != QL_OK) return static_cast<size_t>(-1);
-    return lora_plan(M, K, r, L, 1, pl.path == QL_PATH_TC_FUSED, pl.workspace, sms).workspace;
+    return lora_plan(pl, M, K, r, L, sms).workspace;
 }
 
 size_t workspace_impl(int64_t M, int64_t K, int64_t N, int32_t group, int32_t path, int32_t split_k, int bits) {
@@ -1301,7 +1305,7 @@ size_t qlinear_swiglu_lora_workspace_size(int64_t M, int64_t K, int64_t I, int32
     DeviceInfo* dev = nullptr;
     int sms = 148;
     if (device_info(&dev) == QL_OK) sms = dev->sm_count;
-    return lora_plan(M, K, r, L, 2, true, swiglu_plan(M, K, I).workspace, sms).workspace;
+    return lora_plan_fused(M, K, r, L, 2, swiglu_plan(M, K, I).workspace, sms).workspace;
 }
 
 ql_status qlinear_swiglu_lora_forward(const void* x, const uint32_t* gate_codes, const void* gate_scales,

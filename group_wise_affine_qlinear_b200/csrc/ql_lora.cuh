@@ -6,11 +6,13 @@
 // A is bf16 [L][r][K], B bf16 [L][N][r], s fp32 [L]; a row with a negative id has no adapter.
 //
 // The first product ("shrink") reads every activation once more and the adapters in use; it is bound by that
-// traffic, so it runs on mma.sync straight from global memory (this file).  The second ("expand") never makes a pass
-// over y of its own: the weight-streaming path adds it in fp32 where it sums its partials (lora_reduce_kernel), and
-// the fused path appends it to the tile's K loop (ql_tc_fused.cuh), so y is rounded once.
+// traffic, so it runs on mma.sync straight from global memory (ql_lora_dot.cuh): on the fused path in the kernel below,
+// which converts the activations on the way, on the weight-streaming path in that kernel's idle warps.  The second
+// ("expand") never makes a pass over y of its own: the weight-streaming path adds it in fp32 where it sums its partials
+// (lora_reduce_kernel), the fused path appends it to the tile's K loop (ql_tc_fused.cuh), so y is rounded once.
 #pragma once
 
+#include "ql_lora_dot.cuh"
 #include "ql_prepass.cuh"
 #include "ql_ptx.cuh"
 #include "ql_tc_fused.cuh"
@@ -21,8 +23,6 @@ namespace lora {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 16;              // rows of one shrink tile (MMA M)
-constexpr int kMaxRank = 128;
 constexpr int kMaxSplit = 8;           // CTAs of a cluster that share a tile's K range
 
 struct ShrinkParams {
@@ -30,12 +30,10 @@ struct ShrinkParams {
     const __nv_bfloat16* a[2];   // [L][r][K]; the second one of a gate/up pair
     const float* scale;          // [L] or null (1)
     const int* ids;              // [M]
-    float* t;                    // weight-streaming path: [M][r]
     int M, K, r, L;
-    int tiles;                   // ceil(M / (16 MT))
+    int tiles;                   // ceil(M / 32)
     int passes;                  // CTAs that share a tile's distinct adapters
     int chunks;                  // CTAs along the rank: ceil(r / (8 NT))
-    // fused path (null on the weight-streaming path)
     __nv_bfloat16* tw;           // [M][pairs][r / 8][hi 8 | lo 8]: t 2^-e_m in two bf16 parts
     __half* xh;                  // [M][K]: x 2^-e_m in the dequantizer's k order
     float* rowscale;             // [M]: 2^e_m
@@ -45,24 +43,6 @@ struct ShrinkParams {
     int* tile_list;              // [num_t][BT] those adapters, in order of first use
     int num_t;
 };
-
-// D (16 x 8, fp32) += A (16 x 16, bf16) . B (16 x 8, bf16)
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The adapter of row m, -1 for none; an id outside [-1, L) is recorded and counts as none.
-__device__ __forceinline__ int adapter_of(const int* ids, int m, int L) {
-    const int a = ids[m];
-    if (a >= -1 && a < L) return a;
-    record_status(QL_ERR_INVALID_ARG);
-    return -1;
-}
 
 // One token tile of the fused kernel: its distinct adapters in order of first use, and each row's place among them.
 __device__ __forceinline__ void plan_tile(const ShrinkParams& p, int t_blk) {
@@ -108,23 +88,22 @@ __device__ __forceinline__ float row_scale(uint32_t amax) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// t for 16 MT rows.  grid: (tiles * passes + num_t, S, chunks * pairs), cluster (1, S, 1).
+// The first product and the conversion for tiles of 32 rows.  grid: (tiles * passes + num_t, S, chunks * pairs),
+// cluster (1, S, 1).
 //
-// Each warp multiplies its share of the K range, 32 columns at a time: a lane's 16-byte loads are 8 consecutive k of
-// the tile's activation rows and of one adapter row per n-tile, which feed two MMAs per row block; the MMA's k order
-// is whatever the lanes hold, the same for both operands, so a dot product keeps its terms.  The warps' sums meet in
-// shared memory, the cluster's CTAs' in distributed shared memory, each added in a fixed order.
+// Each warp multiplies its share of the K range, 32 columns at a time (dot_block).  The warps' sums meet in shared
+// memory, the cluster's CTAs' in distributed shared memory, each added in a fixed order.
 //
 // Rows of a tile with other adapters are multiplied too and not written: a tile makes one pass per distinct adapter,
 // and its passes are spread over `passes` CTAs.
 //
-// kConvert (fused path): the same kernel converts the activations (as convert_x_kernel), whose row scale its extra
-// K-steps share, so x comes from DRAM once: the maxima are taken from the registers that feed the MMAs, and the first
-// pass's CTAs then read their rows again, from L2, to convert them.
-template <int NT, int MT, bool kConvert>
+// The same kernel converts the activations (as convert_x_kernel), whose row scale the extra K-steps share, so x comes
+// from DRAM once: the maxima are taken from the registers that feed the MMAs, and the first pass's CTAs then read their
+// rows again, from L2, to convert them.
+template <int NT>
 __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkParams p) {
     ptx::launch_dependents();
-    constexpr int kRows = kTile * MT;
+    constexpr int MT = 2, kRows = kTile * MT;
     constexpr int kSums = kRows * NT * 8;
     __shared__ float part[kWarps][kSums];          // [row][rank] per warp
     __shared__ uint32_t amax[kWarps][kRows];
@@ -137,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkPa
     } else {
         const int tile = static_cast<int>(blockIdx.x) / p.passes, pass = static_cast<int>(blockIdx.x) % p.passes;
         const int pair = static_cast<int>(blockIdx.z) / p.chunks, chunk = static_cast<int>(blockIdx.z) % p.chunks;
-        const bool converts = kConvert && pass == 0 && blockIdx.z == 0;
+        const bool converts = pass == 0 && blockIdx.z == 0;
         const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
         const int m0 = tile * kRows;
         const int j0 = chunk * NT * 8;
@@ -171,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkPa
             uint32_t mx[2 * MT];
 #pragma unroll
             for (int q = 0; q < 2 * MT; ++q) mx[q] = 0u;
-            constexpr int U = NT * MT <= 2 ? 4 : 2;            // column blocks in flight per warp
+            constexpr int U = NT == 1 ? 4 : 2;                 // column blocks in flight per warp
             for (int kb = kb0 + warp; kb < kb1; kb += kWarps * U) {
                 uint4 vx[U][2 * MT], va[U][NT];
                 const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -189,25 +168,18 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkPa
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if constexpr (kConvert) {
-                        if (first) {
+                    if (first) {
 #pragma unroll
-                            for (int q = 0; q < 2 * MT; ++q) {
-                                const uint4 v = vx[u][q];
-                                mx[q] = __vmaxu2(mx[q], __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                                                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-                            }
+                        for (int q = 0; q < 2 * MT; ++q) {
+                            const uint4 v = vx[u][q];
+                            mx[q] = __vmaxu2(mx[q], __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                                             __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
 #pragma unroll
-                        for (int q = 0; q < MT; ++q) {
-                            mma_bf16_16816(acc[q][i], vx[u][2 * q].x, vx[u][2 * q + 1].x, vx[u][2 * q].y, vx[u][2 * q + 1].y,
-                                           va[u][i].x, va[u][i].y);
-                            mma_bf16_16816(acc[q][i], vx[u][2 * q].z, vx[u][2 * q + 1].z, vx[u][2 * q].w, vx[u][2 * q + 1].w,
-                                           va[u][i].z, va[u][i].w);
-                        }
+                        for (int q = 0; q < MT; ++q) dot_block(acc[q][i], vx[u][2 * q], vx[u][2 * q + 1], va[u][i]);
                 }
             }
 #pragma unroll
@@ -218,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkPa
                     *reinterpret_cast<float2*>(&part[warp][at]) = make_float2(acc[q][i][0], acc[q][i][1]);
                     *reinterpret_cast<float2*>(&part[warp][at + 8 * NT * 8]) = make_float2(acc[q][i][2], acc[q][i][3]);
                 }
-            if (kConvert && first) {
+            if (first) {
 #pragma unroll
                 for (int q = 0; q < 2 * MT; ++q) {
                     uint32_t v = max(mx[q] & 0xFFFFu, mx[q] >> 16);
@@ -234,14 +206,14 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkPa
                 for (int w = 1; w < kWarps; ++w) s += part[w][e];
                 part[0][e] = s;                                // this CTA's slice of the sum
             }
-            if (kConvert && first && threadIdx.x < kRows) {
+            if (first && threadIdx.x < kRows) {
                 uint32_t v = amax[0][threadIdx.x];
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) v = max(v, amax[w][threadIdx.x]);
                 amax[0][threadIdx.x] = v;
             }
             if (S > 1) ptx::cluster_sync(); else __syncthreads();
-            if (kConvert && first) {
+            if (first) {
                 if (threadIdx.x < kRows) {
                     uint32_t v = amax[0][threadIdx.x];
                     for (int q = 0; S > 1 && q < S; ++q)
@@ -268,14 +240,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkPa
                     const float sc = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
                     s0 *= sc;
                     s1 *= sc;
-                    if constexpr (kConvert) {
-                        const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));   // 2^-e_m
-                        __nv_bfloat16* o = p.tw + (static_cast<int64_t>(m) * p.pairs + pair) * 2 * p.r + 16 * (j / 8) + j % 8;
-                        *reinterpret_cast<uint32_t*>(o) = fused::bf16_part(s0 * inv, s1 * inv, false);
-                        *reinterpret_cast<uint32_t*>(o + 8) = fused::bf16_part(s0 * inv, s1 * inv, true);
-                    } else {
-                        *reinterpret_cast<float2*>(p.t + static_cast<int64_t>(m) * p.r + j) = make_float2(s0, s1);
-                    }
+                    const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));       // 2^-e_m
+                    __nv_bfloat16* o = p.tw + (static_cast<int64_t>(m) * p.pairs + pair) * 2 * p.r + 16 * (j / 8) + j % 8;
+                    *reinterpret_cast<uint32_t*>(o) = fused::bf16_part(s0 * inv, s1 * inv, false);
+                    *reinterpret_cast<uint32_t*>(o + 8) = fused::bf16_part(s0 * inv, s1 * inv, true);
                 }
             }
             if (S > 1) ptx::cluster_sync(); else __syncthreads();      // the sums are read before the next pass
@@ -315,14 +283,15 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkPa
     if (blockIdx.x == gridDim.x - 1) ptx::grid_dependency_wait();
 }
 
-// y[t][n] = 2^rowexp[t] * (sum of the stream-K partials, as skinny_reduce_kernel) + sum_j tl[t][j] B[a][n][j],
-// the second sum in fp32 from the bf16 adapter, rounded once.  One CTA per (128-column tile, 2 tokens); a thread's
-// first kEager chunks of B are loaded before the wait for the partials.
+// y[t][n] = 2^rowexp[t] * (sum of the stream-K partials, as skinny_reduce_kernel) + sum_j t[t][j] B[a][n][j] with
+// t = s sum_z tp[z], all in fp32 from the bf16 adapter, rounded once.  One CTA per (128-column tile, 2 tokens); a
+// thread's first kEager chunks of B are loaded before the wait for the partials.
 struct ExpandParams {
     const __nv_bfloat16* b;      // [L][N][r]
-    const float* t;              // [M][r]
+    const float* scale;          // [L] or null (1)
+    const float* tp;             // [slices][M][r]
     const int* ids;              // [M]
-    int r, L;
+    int r, L, slices;
 };
 
 template <bool kBf16Out>
@@ -332,27 +301,48 @@ __global__ void __launch_bounds__(256) lora_reduce_kernel(const float* __restric
                                                           int64_t partial_elems, const ExpandParams ep) {
     __shared__ int64_t seg_base[skinny::kMaxCtas];
     __shared__ int count;
+    __shared__ float ps[2][128];
+    __shared__ __align__(16) float tl[2][kMaxRank];
     constexpr int kEager = 4;
     const int w = blockIdx.x;
     const int t = blockIdx.y * 2 + (threadIdx.x >> 7), n = w * skinny::BW + (threadIdx.x & 127);
     const bool live = t < M && n < N;
     if (threadIdx.x == 0) count = skinny::list_segments(w, cpt, units, P, segmax, seg_base);
-    const int a = live ? ep.ids[t] : -1;
-    const bool with = a >= 0 && a < ep.L;                         // the shrink kernel records an id out of range
-    const int chunks = with ? ep.r / 8 : 0;
+    const int a = t < M ? ep.ids[t] : -1;
+    const bool with = a >= 0 && a < ep.L;                         // the first product records an id out of range
+    const int chunks = with && live ? ep.r / 8 : 0;
     const uint4* b = reinterpret_cast<const uint4*>(ep.b + (static_cast<int64_t>(with ? a : 0) * N + (live ? n : 0)) * ep.r);
     uint4 eager[kEager];
 #pragma unroll
     for (int i = 0; i < kEager; ++i) eager[i] = i < chunks ? __ldg(b + i) : make_uint4(0u, 0u, 0u, 0u);
-    ptx::grid_dependency_wait();                                  // partials and t come from the kernels before
+    const float sc = with && ep.scale != nullptr ? __ldg(ep.scale + a) : 1.0f;
+    __syncthreads();
+    ptx::grid_dependency_wait();                                  // partials and tp come from the kernel before
+    // t of the CTA's two tokens: a token's 128 threads share out the slices, then add their sums in order
+    const int half = threadIdx.x >> 7, i128 = threadIdx.x & 127;
+    const int groups = 128 / ep.r, j = i128 % ep.r, group = i128 / ep.r;
+    if (with && group < groups) {
+        const float* tp = ep.tp + static_cast<int64_t>(t) * ep.r + j;
+        const int64_t step = static_cast<int64_t>(M) * ep.r;
+        float sum = 0.0f;
+#pragma unroll 8
+        for (int z = group; z < ep.slices; z += groups) sum += tp[z * step];
+        ps[half][i128] = sum;
+    }
+    float acc = live ? skinny::sum_segments(partial, partial_elems, seg_base, count, M, t, i128) : 0.0f;
+    __syncthreads();
+    if (with && i128 < ep.r) {
+        float sum = ps[half][i128];
+        for (int q = 1; q < groups; ++q) sum += ps[half][i128 + q * ep.r];
+        tl[half][i128] = sc * sum;
+    }
     __syncthreads();
     if (!live) return;
-    float acc = skinny::sum_segments(partial, partial_elems, seg_base, count, M, t, threadIdx.x & 127);
     acc = ldexpf(acc, rowexp[t]);
-    const float4* tl = reinterpret_cast<const float4*>(ep.t + static_cast<int64_t>(t) * ep.r);
+    const float4* tt = reinterpret_cast<const float4*>(tl[half]);
     float delta = 0.0f;
     auto add = [&](const uint4 v, int i) {
-        const float4 t0 = tl[2 * i], t1 = tl[2 * i + 1];
+        const float4 t0 = tt[2 * i], t1 = tt[2 * i + 1];
         const uint32_t q[4] = {finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w)};
         delta = fmaf(t0.x, bf16_lo(q[0]), delta);
         delta = fmaf(t0.y, bf16_hi(q[0]), delta);

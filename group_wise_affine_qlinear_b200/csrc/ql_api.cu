@@ -1055,40 +1055,81 @@ ql_status pack_impl(const float* w, const float* imatrix, int64_t K, int64_t N, 
 
 // ------------------------------------------------------------------ norms around a block
 
-// Threads and 8-element vectors per thread of a CTA-per-row launch.  Many rows: two vectors per thread, so that
-// more rows are in flight on an SM; a few rows: one, which leaves each thread less to do in a row.
-struct NormShape {
-    int vpt, threads;
+// A ring launch: the first configuration whose threads cover the row's pieces of 8 elements, `stages`
+// rows of shared memory per CTA, and as many CTAs per SM as shared memory (two rows at least) and threads allow.
+struct RingShape {
+    int cfg = -1, threads = 0, stages = 0, ctas = 0;   // cfg -1: the row does not fit
+    uint32_t smem = 0;
 };
-NormShape norm_shape(int64_t M, int64_t D, int sm_count) {
-    const int nv = static_cast<int>(D / 8);
-    int vpt = M > 2 * sm_count ? 2 : 1;
-    while (vpt < 4 && nv > 1024 * vpt) vpt *= 2;
-    const int per = (nv + vpt - 1) / vpt;
-    return {vpt, (per + 31) / 32 * 32};
+template <int kCfg>
+bool ring_fits(RingShape* rs, int64_t M, int nv, uint32_t stage, int sm_count) {
+    using C = norm::RingCfg<kCfg>;
+    constexpr uint32_t kSmSmem = 226 * 1024, kReserved = 2048;         // per CTA: static shared memory and the driver's
+    if (nv > C::kVpt * C::kThreads) return false;
+    rs->threads = ((nv + C::kVpt - 1) / C::kVpt + 31) / 32 * 32;
+    // the registers of kCtas CTAs of the full size hold proportionally more of smaller ones
+    int ctas = C::kCtas * C::kThreads / rs->threads;
+    while (ctas > 1 && static_cast<uint32_t>(ctas) * (2 * stage + kReserved) > kSmSmem) --ctas;
+    if (2 * stage + kReserved > kSmSmem) return false;
+    rs->cfg = kCfg;
+    rs->stages = static_cast<int>(std::min<uint32_t>(norm::kMaxStages, (kSmSmem / ctas - kReserved) / stage));
+    rs->smem = rs->stages * stage;
+    rs->ctas = static_cast<int>(std::min<int64_t>(M, static_cast<int64_t>(ctas) * sm_count));
+    return true;
+}
+
+template <bool kXF32, int kY, int kCfg>
+ql_status launch_norm_ring(const RingShape& rs, const norm::Params& p, cudaStream_t st) {
+    auto k = norm::norm_ring_kernel<kXF32, kY, kCfg>;
+    static std::atomic<uint64_t> ready{0};             // devices on which the kernel may use the largest ring
+    int dev = 0;
+    static_assert(kMaxDevices <= 64, "one bit per device");
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QL_ERR_CUDA;
+    if (((ready.load() >> dev) & 1u) == 0) {
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024 - 2048) != cudaSuccess)
+            return QL_ERR_CUDA;
+        ready.fetch_or(1ull << dev);
+    }
+    k<<<rs.ctas, rs.threads, rs.smem, st>>>(p, rs.stages);
+    return launch_status();
 }
 
 template <bool kXF32, int kY>
 ql_status launch_norm(const norm::Params& p, int sm_count, cudaStream_t st) {
-    if (p.D <= norm::kWarpRowMax) {
-        const dim3 grid(static_cast<unsigned>((p.M + norm::kWarpRows - 1) / norm::kWarpRows));
-        const int nv = p.D / 8;
+    const int nv = p.D / 8;
+    if (p.D <= norm::kGroupMax) {
+        const int G = nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
+        const int64_t rows = 32 / G;
+        // up to 16 warps per SM; fewer rows than that: one step per warp
+        const int64_t warps = std::min<int64_t>((p.M + rows - 1) / rows, 16ll * sm_count);
+        const int64_t per_warp = ((p.M + warps - 1) / warps + rows - 1) / rows * rows;
+        const int64_t used = (p.M + per_warp - 1) / per_warp;
+        const dim3 grid(static_cast<unsigned>((used + norm::kGroupWarps - 1) / norm::kGroupWarps));
         if (nv <= 32)
-            norm::norm_residual_kernel<kXF32, kY, 1, true><<<grid, 32 * norm::kWarpRows, 0, st>>>(p);
-        else if (nv <= 64)
-            norm::norm_residual_kernel<kXF32, kY, 2, true><<<grid, 32 * norm::kWarpRows, 0, st>>>(p);
+            norm::norm_group_kernel<kXF32, kY, 1><<<grid, 32 * norm::kGroupWarps, 0, st>>>(p, G, per_warp);
         else
-            norm::norm_residual_kernel<kXF32, kY, 4, true><<<grid, 32 * norm::kWarpRows, 0, st>>>(p);
+            norm::norm_group_kernel<kXF32, kY, 2><<<grid, 32 * norm::kGroupWarps, 0, st>>>(p, G, per_warp);
         return launch_status();
     }
-    const NormShape ns = norm_shape(p.M, p.D, sm_count);
+    if (p.M > 2 * sm_count) {
+        constexpr int kYB = kY == norm::kYNone ? 0 : kY == norm::kYF32 ? 4 : 2;
+        const uint32_t stage = norm::stage_bytes(p.D, kXF32 ? 4 : 2, kYB, kYB ? p.S : 0);
+        RingShape rs;
+        if (ring_fits<0>(&rs, p.M, nv, stage, sm_count)) return launch_norm_ring<kXF32, kY, 0>(rs, p, st);
+        if (ring_fits<1>(&rs, p.M, nv, stage, sm_count)) return launch_norm_ring<kXF32, kY, 1>(rs, p, st);
+        if (ring_fits<2>(&rs, p.M, nv, stage, sm_count)) return launch_norm_ring<kXF32, kY, 2>(rs, p, st);
+        if (ring_fits<3>(&rs, p.M, nv, stage, sm_count)) return launch_norm_ring<kXF32, kY, 3>(rs, p, st);
+    }
+    int vpt = 1;
+    while (vpt < 4 && nv > 1024 * vpt) vpt *= 2;
     const dim3 grid(static_cast<unsigned>(p.M));
-    if (ns.vpt == 1)
-        norm::norm_residual_kernel<kXF32, kY, 1, false><<<grid, ns.threads, 0, st>>>(p);
-    else if (ns.vpt == 2)
-        norm::norm_residual_kernel<kXF32, kY, 2, false><<<grid, ns.threads, 0, st>>>(p);
+    const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+    if (vpt == 1)
+        norm::norm_row_kernel<kXF32, kY, 1><<<grid, threads, 0, st>>>(p);
+    else if (vpt == 2)
+        norm::norm_row_kernel<kXF32, kY, 2><<<grid, threads, 0, st>>>(p);
     else
-        norm::norm_residual_kernel<kXF32, kY, 4, false><<<grid, ns.threads, 0, st>>>(p);
+        norm::norm_row_kernel<kXF32, kY, 4><<<grid, threads, 0, st>>>(p);
     return launch_status();
 }
 
@@ -1151,6 +1192,7 @@ ql_status norm_residual_impl(const void* x, ql_dtype x_dtype, const void* y, ql_
     p.residual_scale = residual_scale;
     p.branch_scale = branch_scale;
     p.eps = eps;
+    p.inv_d = 1.0f / static_cast<float>(D);
     const int sm = dev->sm_count;
     if (x_dtype == QL_F32) {
         if (!y) return launch_norm<true, norm::kYNone>(p, sm, stream);

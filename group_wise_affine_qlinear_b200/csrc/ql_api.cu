@@ -97,6 +97,13 @@ cudaError_t fused_smem_attr() {
     }
     return e;
 }
+
+template <int NT>
+cudaError_t prepare_smem_attr() {
+    return cudaFuncSetAttribute(lora::lora_prepare_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                lora::shrink_smem(NT));
+}
+
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
@@ -113,7 +120,9 @@ ql_status device_info(DeviceInfo** out) {
     if (!d.fused_attr_set) {
         if (fused_smem_attr<4>() != cudaSuccess || fused_smem_attr<8>() != cudaSuccess ||
             fused_smem_attr<4, true>() != cudaSuccess || fused_smem_attr<4, false, true>() != cudaSuccess ||
-            fused_smem_attr<8, false, true>() != cudaSuccess || fused_smem_attr<4, true, true>() != cudaSuccess)
+            fused_smem_attr<8, false, true>() != cudaSuccess || fused_smem_attr<4, true, true>() != cudaSuccess ||
+            prepare_smem_attr<1>() != cudaSuccess || prepare_smem_attr<2>() != cudaSuccess ||
+            prepare_smem_attr<4>() != cudaSuccess)
             return QL_ERR_CUDA;
         d.fused_attr_set = true;
     }
@@ -161,7 +170,8 @@ ql_status encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, 
 
 // 3-D row-major tensor map: extents (cols, rows, planes) in elements, row and plane pitches in bytes.
 ql_status encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t cols, uint64_t rows,
-                    uint64_t planes, uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols, uint32_t box_rows) {
+                    uint64_t planes, uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols, uint32_t box_rows,
+                    CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE) {
     PFN_cuTensorMapEncodeTiled_v12000 enc;
     if (get_encoder(&enc) != QL_OK) return QL_ERR_CUDA;
     const cuuint64_t dims[3] = {cols, rows, planes};
@@ -169,7 +179,7 @@ ql_status encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, 
     const cuuint32_t box[3] = {box_cols, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? QL_OK : QL_ERR_CUDA;
 }
@@ -438,20 +448,18 @@ LoraPlan lora_plan_streaming(int64_t M, int64_t K, int r, int L, size_t base, in
     return lp;
 }
 
-// Fused path: the first product's tiles of 32 rows alone fill the GPU only from a few thousand rows on.  Below, a
-// cluster of up to 8 CTAs shares a tile's K range, and a tile's distinct adapters go to up to 16 CTAs.
+// Fused path: tiles of 32 rows.  Where they are few, a cluster of up to 8 CTAs shares a tile's K range, each warp with
+// two 64-column chunks at least, and a tile's distinct adapters go to up to 16 CTAs.
 LoraPlan lora_plan_fused(int64_t M, int64_t K, int r, int L, int pairs, size_t base, int sm_count) {
     LoraPlan lp;
-    const int rows = 2 * lora::kTile;
-    const int64_t tiles = (M + rows - 1) / rows;
-    const int64_t want = 2 * sm_count;
+    const int64_t tiles = (M + lora::kRows - 1) / lora::kRows;
     const int r8 = r / 8;
     lp.nt = r8 >= 3 ? 4 : r8;
     lp.chunks = (r8 + lp.nt - 1) / lp.nt;
     const int64_t ctas = tiles * pairs * lp.chunks;
-    // at least two 32-column blocks of K per warp and CTA
-    while (lp.S < lora::kMaxSplit && ctas * lp.S < want && K / 32 >= 2 * lora::kWarps * 2 * lp.S) lp.S *= 2;
-    while (lp.passes < std::min(L, rows) && ctas * lp.S * lp.passes < want) ++lp.passes;
+    const int64_t want = 2 * sm_count;                         // the first product's CTAs that fit the GPU at once
+    while (2 * lp.S <= lora::kMaxSplit && 2 * ctas * lp.S <= want && K / lora::kCols >= 2 * lora::kWarps * 2 * lp.S) lp.S *= 2;
+    while (lp.passes < std::min(L, lora::kRows) && ctas * lp.S * lp.passes < want) ++lp.passes;
     if (M <= 512) lp.passes = std::min(L, lora::kTile);
     lp.off_t = round_up(base, 256);
     const size_t num_t = static_cast<size_t>((M + fused::BT - 1) / fused::BT);
@@ -469,11 +477,19 @@ LoraPlan lora_plan(const Plan& pl, int64_t M, int64_t K, int r, int L, int sm_co
 
 // Fused path: t of every row's adapter, the converted activations and the token tiles' adapter lists, launched behind
 // the parameter transpose under programmatic dependent launch.
-ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, int64_t M, int64_t K, uint8_t* ws,
+ql_status launch_prepare(const LoraArgs& la, const LoraPlan& lp, const void* x, int64_t M, int64_t K, uint8_t* ws,
                         __half* xh, float* rowscale, int bits, cudaStream_t st) {
     lora::ShrinkParams p = {};
+    CUtensorMap mx, ma[2];
+    ql_status s;
+    if ((s = encode_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, K * 2, lora::kCols, lora::kRows,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) != QL_OK)
+        return s;
+    for (int i = 0; i < 2; ++i)
+        if ((s = encode_3d(&ma[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, la.a[i < la.pairs ? i : 0], K, la.r, la.L, K * 2,
+                           static_cast<uint64_t>(la.r) * K * 2, lora::kCols, 8 * lp.nt, CU_TENSOR_MAP_SWIZZLE_128B)) != QL_OK)
+            return s;
     p.x = static_cast<const __nv_bfloat16*>(x);
-    for (int i = 0; i < 2; ++i) p.a[i] = static_cast<const __nv_bfloat16*>(la.a[i]);
     p.scale = la.scale;
     p.ids = la.ids;
     p.M = static_cast<int>(M);
@@ -483,7 +499,6 @@ ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, i
     p.passes = lp.passes;
     p.chunks = lp.chunks;
     p.pairs = la.pairs;
-    p.tiles = static_cast<int>((M + 2 * lora::kTile - 1) / (2 * lora::kTile));
     p.tw = reinterpret_cast<__nv_bfloat16*>(ws + lp.off_t);
     p.xh = xh;
     p.rowscale = rowscale;
@@ -493,8 +508,13 @@ ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, i
     p.tile_list = reinterpret_cast<int*>(ws + lp.off_list);
     p.num_t = static_cast<int>((M + fused::BT - 1) / fused::BT);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles) * lp.passes + p.num_t, lp.S, lp.chunks * la.pairs);
-    cfg.blockDim = dim3(lora::kThreads);
+    const int64_t tiles = (M + lora::kRows - 1) / lora::kRows;
+    p.plan_x = (p.num_t + lp.S - 1) / lp.S;
+    const int64_t columns = p.plan_x + tiles * lp.passes * lp.chunks * la.pairs;
+    if (columns > (1ll << 31) - 1) return QL_ERR_UNSUPPORTED;
+    cfg.gridDim = dim3(static_cast<unsigned>(columns), lp.S);
+    cfg.blockDim = dim3(lora::kBlock);
+    cfg.dynamicSmemBytes = lora::shrink_smem(lp.nt);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -505,9 +525,9 @@ ql_status launch_shrink(const LoraArgs& la, const LoraPlan& lp, const void* x, i
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = lp.nt == 1   ? cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<1>, p)
-                          : lp.nt == 2 ? cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<2>, p)
-                                       : cudaLaunchKernelEx(&cfg, lora::lora_shrink_kernel<4>, p);
+    const cudaError_t e = lp.nt == 1   ? cudaLaunchKernelEx(&cfg, lora::lora_prepare_kernel<1>, mx, ma[0], ma[1], p)
+                          : lp.nt == 2 ? cudaLaunchKernelEx(&cfg, lora::lora_prepare_kernel<2>, mx, ma[0], ma[1], p)
+                                       : cudaLaunchKernelEx(&cfg, lora::lora_prepare_kernel<4>, mx, ma[0], ma[1], p);
     return e == cudaSuccess ? QL_OK : QL_ERR_CUDA;
 }
 
@@ -586,7 +606,7 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
                                                    sb, static_cast<int>(N), static_cast<int>(G));
     if ((s = launch_status()) != QL_OK) return s;
     // with adapters their first product converts the activations on its way
-    s = la ? launch_shrink(*la, *lp, x, M, K, base, xh, rs, bits, st)
+    s = la ? launch_prepare(*la, *lp, x, M, K, base, xh, rs, bits, st)
            : launch_convert_x(bits, static_cast<const __nv_bfloat16*>(x), xh, rs, M, K, st);
     if (s != QL_OK) return s;
     fused::LoraParams p = {};
@@ -817,7 +837,7 @@ ql_status run_swiglu(const SwigluPlan& pl, const void* x, const uint32_t* gc, co
                                                         sb, static_cast<int>(I), static_cast<int>(G),
                                                         static_cast<int>(pl.ncols));
     if ((s = launch_status()) != QL_OK) return s;
-    s = la ? launch_shrink(*la, *lp, x, M, K, base, xh, rs, 4, st)
+    s = la ? launch_prepare(*la, *lp, x, M, K, base, xh, rs, 4, st)
            : launch_convert_x(4, static_cast<const __nv_bfloat16*>(x), xh, rs, M, K, st);
     if (s != QL_OK) return s;
     fused::LoraParams p = {};

@@ -21,19 +21,29 @@
 namespace ql {
 namespace lora {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;          // of the first product
 constexpr int kWarps = kThreads / 32;
+constexpr int kConvGroups = 4;         // pairs of warps that convert a row each
+constexpr int kConvThreads = 64;       // of one such pair
+constexpr int kBlock = kThreads + kConvGroups * kConvThreads;
+constexpr int kRows = 2 * kTile;       // rows of one tile of the first product on the fused path
+constexpr int kCols = 64;              // columns of one ring slot: 128-byte rows
+constexpr int kSlots = 3;              // ring slots per warp
 constexpr int kMaxSplit = 8;           // CTAs of a cluster that share a tile's K range
+constexpr uint32_t kXSlot = kRows * kCols * 2;
+
+// A ring slot: the tile's rows of x and 8 NT ranks of A, 64 columns each.
+__host__ __device__ constexpr uint32_t slot_bytes(int nt) { return kXSlot + static_cast<uint32_t>(nt) * 8 * kCols * 2; }
+__host__ __device__ constexpr uint32_t shrink_smem(int nt) { return kWarps * kSlots * slot_bytes(nt) + 1024; }
 
 struct ShrinkParams {
     const __nv_bfloat16* x;      // [M][K]
-    const __nv_bfloat16* a[2];   // [L][r][K]; the second one of a gate/up pair
     const float* scale;          // [L] or null (1)
     const int* ids;              // [M]
     int M, K, r, L;
-    int tiles;                   // ceil(M / 32)
     int passes;                  // CTAs that share a tile's distinct adapters
     int chunks;                  // CTAs along the rank: ceil(r / (8 NT))
+    int plan_x;                  // grid columns of the plan
     __nv_bfloat16* tw;           // [M][pairs][r / 8][hi 8 | lo 8]: t 2^-e_m in two bf16 parts
     __half* xh;                  // [M][K]: x 2^-e_m in the dequantizer's k order
     float* rowscale;             // [M]: 2^e_m
@@ -44,39 +54,63 @@ struct ShrinkParams {
     int num_t;
 };
 
+// Barrier of the first product's warps.
+__device__ __forceinline__ void product_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
+
 // One token tile of the fused kernel: its distinct adapters in order of first use, and each row's place among them.
+// A thread takes the rows tid and tid + 128; every row is compared with all of the tile's (no early exit: the loads of
+// the loop are then independent), and a place is a count of set bits.
 __device__ __forceinline__ void plan_tile(const ShrinkParams& p, int t_blk) {
     constexpr int BT = fused::BT;
-    static_assert(BT <= kThreads, "one thread per token of a tile");
-    __shared__ int id[BT];
-    __shared__ int warp_first[kWarps];
-    const int i = threadIdx.x;
-    const int m = t_blk * BT + i;
+    static_assert(BT % 32 == 0 && BT > kThreads && BT <= 2 * kThreads, "one or two rows per thread, whole warps");
+    __shared__ __align__(16) int id[BT];
+    __shared__ uint32_t leads[BT / 32];            // bit i % 32 of word i / 32: row i is its adapter's first
     const int rows = min(BT, p.M - t_blk * BT);
-    const int mine = i < rows ? adapter_of(p.ids, m, p.L) : -1;
-    if (i < BT) id[i] = mine;
-    __syncthreads();
-    int first = i;                                 // the tile's first row with this adapter
-    if (mine >= 0)
-        for (int j = 0; j < i; ++j)
-            if (id[j] == mine) { first = j; break; }
-    const bool leads = mine >= 0 && first == i;
-    const uint32_t bal = __ballot_sync(0xFFFFFFFFu, leads);
-    if ((i & 31) == 0) warp_first[i >> 5] = __popc(bal);
-    __syncthreads();
-    int place = __popc(bal & ((1u << (i & 31)) - 1u)), total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < (i >> 5)) place += warp_first[w];
-        total += warp_first[w];
+    for (int i = threadIdx.x; i < BT; i += kThreads) id[i] = i < rows ? adapter_of(p.ids, t_blk * BT + i, p.L) : -1;
+    product_sync();
+    int first[2];
+    const int4* quads = reinterpret_cast<const int4*>(id);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = static_cast<int>(threadIdx.x) + h * kThreads;
+        first[h] = i;
+        if (i >= BT) continue;                     // whole warps
+        const int a = id[i];
+#pragma unroll 8
+        for (int q = BT / 4 - 1; q >= 0; --q) {
+            const int4 v = quads[q];
+            first[h] = v.w == a ? 4 * q + 3 : first[h];
+            first[h] = v.z == a ? 4 * q + 2 : first[h];
+            first[h] = v.y == a ? 4 * q + 1 : first[h];
+            first[h] = v.x == a ? 4 * q : first[h];
+        }
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, a >= 0 && first[h] == i);
+        if ((i & 31) == 0) leads[i >> 5] = bits;
     }
-    __syncthreads();
-    if (leads) {
-        p.tile_list[t_blk * BT + place] = mine;
-        id[i] = place;                             // only this row's entry: others read id[first] below
+    product_sync();
+    const auto place = [&](int i) {                // adapters first met before row i
+        int n = 0;
+        for (int w = 0; w < BT / 32; ++w) {
+            const uint32_t below = w < (i >> 5) ? 0xFFFFFFFFu : w == (i >> 5) ? (1u << (i & 31)) - 1u : 0u;
+            n += __popc(leads[w] & below);
+        }
+        return n;
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = static_cast<int>(threadIdx.x) + h * kThreads;
+        if (i >= rows) continue;
+        const int n = place(first[h]);
+        p.row_slot[t_blk * BT + i] = id[i] >= 0 ? n : -1;
+        if (id[i] >= 0 && first[h] == i) p.tile_list[t_blk * BT + n] = id[i];
     }
-    __syncthreads();
-    if (i < rows) p.row_slot[m] = mine >= 0 ? id[first] : -1;
-    if (i == 0) p.tile_count[t_blk] = total;
+    if (threadIdx.x == 0) {
+        int n = 0;
+        for (int w = 0; w < BT / 32; ++w) n += __popc(leads[w]);
+        p.tile_count[t_blk] = n;
+    }
 }
 
 // The conversion's row scale (convert_x_kernel): 2^e with the row's largest magnitude in [2^15, 2^16) after division,
@@ -88,195 +122,279 @@ __device__ __forceinline__ float row_scale(uint32_t amax) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// The first product and the conversion for tiles of 32 rows.  grid: (tiles * passes + num_t, S, chunks * pairs),
-// cluster (1, S, 1).
+// The larger of m and |a|, |b|, per bf16 half; a NaN is passed over, as by the conversion's fmaxf.
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t m, uint32_t a, uint32_t b) {
+    uint32_t o;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(o) : "r"(m));
+    return o;
+}
+
+// One CTA's part of the first product: the K range of cluster rank `rank` of S, for the tile's n-th distinct adapters
+// with n % passes == pass, 8 NT ranks from j0 on, of the pair's member.
 //
-// Each warp multiplies its share of the K range, 32 columns at a time (dot_block).  The warps' sums meet in shared
-// memory, the cluster's CTAs' in distributed shared memory, each added in a fixed order.
-//
-// Rows of a tile with other adapters are multiplied too and not written: a tile makes one pass per distinct adapter,
-// and its passes are spread over `passes` CTAs.
-//
-// The same kernel converts the activations (as convert_x_kernel), whose row scale the extra K-steps share, so x comes
-// from DRAM once: the maxima are taken from the registers that feed the MMAs, and the first pass's CTAs then read their
-// rows again, from L2, to convert them.
+// Each warp runs a pipeline of its own: its lane 0 keeps kSlots boxes of 32 rows x 64 columns of x, and the same columns
+// of the adapter, on their way by TMA while the warp multiplies the oldest (mma.sync, fragments by ldmatrix).  No warp
+// waits for another until the sums meet in shared memory, and the cluster's CTAs' in distributed shared memory, each
+// added in a fixed order.  t must share the row scale of the converted activations: the rows' maxima are taken from the
+// fragments.  Rows of the tile with other adapters are multiplied too and not written.  (The cluster's barriers count
+// every live thread: they complete once the converting warps have left.)
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const ShrinkParams p) {
-    ptx::launch_dependents();
-    constexpr int MT = 2, kRows = kTile * MT;
+__device__ __forceinline__ void shrink_tile(const CUtensorMap& map_x, const CUtensorMap& map_a, const ShrinkParams& p,
+                                            uint8_t* smem, int tile, int pass, int pair, int j0, int rank, int S) {
     constexpr int kSums = kRows * NT * 8;
-    __shared__ float part[kWarps][kSums];          // [row][rank] per warp
+    constexpr uint32_t kSlot = slot_bytes(NT);
+    static_assert(kSums * 4 <= kSlots * kSlot && kSlot % 1024 == 0, "a warp's sums reuse its ring; swizzled boxes");
+    __shared__ __align__(8) uint64_t full[kWarps][kSlots];
     __shared__ uint32_t amax[kWarps][kRows];
     __shared__ float scale_s[kRows];
-    const int S = static_cast<int>(gridDim.y);
-    const int rank = static_cast<int>(blockIdx.y);             // rank in the cluster (1, S, 1)
-    const int shrink_ctas = p.tiles * p.passes;
-    if (static_cast<int>(blockIdx.x) >= shrink_ctas) {
-        if (blockIdx.y == 0 && blockIdx.z == 0) plan_tile(p, static_cast<int>(blockIdx.x) - shrink_ctas);
-    } else {
-        const int tile = static_cast<int>(blockIdx.x) / p.passes, pass = static_cast<int>(blockIdx.x) % p.passes;
-        const int pair = static_cast<int>(blockIdx.z) / p.chunks, chunk = static_cast<int>(blockIdx.z) % p.chunks;
-        const bool converts = pass == 0 && blockIdx.z == 0;
-        const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
-        const int m0 = tile * kRows;
-        const int j0 = chunk * NT * 8;
-        const int mine = lane < kRows && m0 + lane < p.M ? adapter_of(p.ids, m0 + lane, p.L) : -1;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, mine);
-        uint32_t leaders = __ballot_sync(0xFFFFFFFFu, mine >= 0 && (__ffs(same) - 1) == lane);
-        const int kb_all = p.K / 32;
-        const int kb0 = static_cast<int>(static_cast<int64_t>(kb_all) * rank / S);
-        const int kb1 = static_cast<int>(static_cast<int64_t>(kb_all) * (rank + 1) / S);
-        const int g = lane >> 2, c = lane & 3;
-        const uint4* xr[2 * MT];
-#pragma unroll
-        for (int q = 0; q < 2 * MT; ++q) {         // rows past M repeat the last one; their results are not written
-            const int64_t row = min(m0 + g + 8 * q, p.M - 1);
-            xr[q] = reinterpret_cast<const uint4*>(p.x + row * p.K) + c;
+    __shared__ int id_s[kRows];
+    __shared__ int abort_flag;
+    const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+    const int g = lane >> 2, c = lane & 3;
+    const int m0 = tile * kRows;
+    const int mine = m0 + lane < p.M ? adapter_of(p.ids, m0 + lane, p.L) : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, mine);
+    uint32_t leaders = __ballot_sync(0xFFFFFFFFu, mine >= 0 && (__ffs(same) - 1) == lane);
+    for (int n = 0; n < pass; ++n) leaders &= leaders - 1;     // the first adapter of this CTA's
+    if (warp == 0 && pass == 0 && pair == 0 && j0 == 0 && rank == 0) {
+        // rows without an adapter: zeros in tw, so that a tile's boxes of it need no mask
+        const int pieces = p.pairs * p.r / 4;
+        for (int row = 0; row < kRows && m0 + row < p.M; ++row) {
+            if (__shfl_sync(0xFFFFFFFFu, mine, row) >= 0) continue;
+            uint4* o = reinterpret_cast<uint4*>(p.tw) + static_cast<int64_t>(m0 + row) * pieces;
+            for (int i = lane; i < pieces; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
         }
-        bool first = true;                         // the pass that also takes the rows' maxima
-        for (int n = 0; leaders != 0 || (converts && first); ++n, leaders &= leaders - 1) {
-            if (leaders != 0 && n % p.passes != pass) continue;
-            const bool with = leaders != 0;        // false: a converting CTA without an adapter in its rows
-            const int adapter = with ? __shfl_sync(0xFFFFFFFFu, mine, __ffs(leaders) - 1) : -1;
-            const __nv_bfloat16* a = (pair == 0 ? p.a[0] : p.a[1]) + (static_cast<int64_t>(with ? adapter : 0) * p.r + j0) * p.K;
-            const int nt_live = with ? min(NT, p.r / 8 - chunk * NT) : 0;
-            float acc[MT][NT][4];
+    }
+    if (leaders == 0) return;                                  // the same in every CTA of the cluster
+    const int kc_all = p.K / kCols;
+    const int kc0 = static_cast<int>(static_cast<int64_t>(kc_all) * rank / S) + warp;          // this warp's first chunk
+    const int kc1 = static_cast<int>(static_cast<int64_t>(kc_all) * (rank + 1) / S);
+    const int nk = kc0 < kc1 ? (kc1 - kc0 + kWarps - 1) / kWarps : 0;                          // and their number
+    uint8_t* ring = smem + warp * kSlots * kSlot;
+    const uint32_t ring_addr = ptx::smem_addr(ring);
+    float* part = reinterpret_cast<float*>(smem);              // warp w's sums at w * kPartStride
+    constexpr int kPartStride = kSlots * kSlot / 4;
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kWarps; ++w)
+            for (int i = 0; i < kSlots; ++i) ptx::mbar_init(&full[w][i], 1);
+        abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0) id_s[lane] = mine;
+    product_sync();
+    bool ok = true, first = true;
+    uint32_t used = 0, issued = 0;                             // chunks multiplied, copies started (lane 0)
+    while (leaders != 0) {
+        const int adapter = __shfl_sync(0xFFFFFFFFu, mine, __ffs(leaders) - 1);
+        const float factor = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
+        const auto issue = [&](int i) {
+            const uint32_t s = issued % kSlots;
+            ++issued;
+            ptx::mbar_arrive_expect_tx(&full[warp][s], kSlot);
+            ptx::tma_load_2d(ring + s * kSlot, &map_x, &full[warp][s], (kc0 + i * kWarps) * kCols, m0);
+            ptx::tma_load_3d(ring + s * kSlot + kXSlot, &map_a, &full[warp][s], (kc0 + i * kWarps) * kCols, j0, adapter);
+        };
+        float acc[2][NT][4];
 #pragma unroll
-            for (int q = 0; q < MT; ++q)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[q][i][e] = 0.0f;
-            uint32_t mx[2 * MT];
+                for (int e = 0; e < 4; ++e) acc[q][i][e] = 0.0f;
+        uint32_t mx[4] = {0u, 0u, 0u, 0u};                     // rows g, g + 8, g + 16, g + 24
+        if (lane == 0)
+            for (int i = 0; i < min(kSlots, nk); ++i) issue(i);
+        for (int i = 0; i < nk; ++i, ++used) {
+            const uint32_t s = used % kSlots;
+            ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&full[warp][s], (used / kSlots) & 1u, &abort_flag)) && ok;
+            const uint32_t x_slot = ring_addr + s * kSlot, a_slot = x_slot + kXSlot;
 #pragma unroll
-            for (int q = 0; q < 2 * MT; ++q) mx[q] = 0u;
-            constexpr int U = NT == 1 ? 4 : 2;                 // column blocks in flight per warp
-            for (int kb = kb0 + warp; kb < kb1; kb += kWarps * U) {
-                uint4 vx[U][2 * MT], va[U][NT];
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            for (int ks = 0; ks < kCols / 16; ++ks) {
+                uint32_t xa[2][4], b[(NT + 1) / 2][4];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int b = kb + u * kWarps;
-                    const bool in = b < kb1;
-#pragma unroll
-                    for (int q = 0; q < 2 * MT; ++q) vx[u][q] = in ? __ldg(xr[q] + 4 * b) : zero;
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        va[u][i] = in && i < nt_live
-                                       ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<int64_t>(8 * i + g) * p.K) + c + 4 * b)
-                                       : zero;
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t row = static_cast<uint32_t>(16 * q + (lane & 15));
+                    const uint32_t piece = static_cast<uint32_t>(2 * ks + (lane >> 4));
+                    ptx::ldmatrix_x4(x_slot + row * 128 + ((piece ^ (row & 7)) << 4), xa[q]);
                 }
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (first) {
+                for (int j = 0; j < (NT + 1) / 2; ++j) {
+                    // two rank blocks: lanes 0-7 and 8-15 address the first one's halves of k, 16-31 the second's
+                    const uint32_t row = static_cast<uint32_t>(16 * j + (NT > 1 ? (lane >> 4) * 8 : 0) + (lane & 7));
+                    const uint32_t piece = static_cast<uint32_t>(2 * ks + ((lane >> 3) & 1));
+                    ptx::ldmatrix_x4(a_slot + row * 128 + ((piece ^ (row & 7)) << 4), b[j]);
+                }
+                if (first) {
 #pragma unroll
-                        for (int q = 0; q < 2 * MT; ++q) {
-                            const uint4 v = vx[u][q];
-                            mx[q] = __vmaxu2(mx[q], __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                                             __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-                        }
+                    for (int q = 0; q < 2; ++q) {
+                        mx[2 * q] = absmax_bf16x2(mx[2 * q], xa[q][0], xa[q][2]);
+                        mx[2 * q + 1] = absmax_bf16x2(mx[2 * q + 1], xa[q][1], xa[q][3]);
                     }
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int q = 0; q < MT; ++q) dot_block(acc[q][i], vx[u][2 * q], vx[u][2 * q + 1], va[u][i]);
                 }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        mma_bf16_16816(acc[q][j], xa[q][0], xa[q][1], xa[q][2], xa[q][3], b[j / 2][2 * (j & 1)],
+                                       b[j / 2][2 * (j & 1) + 1]);
             }
+            __syncwarp();
+            if (lane == 0 && ok && i + kSlots < nk) issue(i + kSlots);
+        }
+        // the warp's ring is empty: its sums go there
+        float* sums = part + warp * kPartStride;
 #pragma unroll
-            for (int q = 0; q < MT; ++q)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const int at = (16 * q + g) * NT * 8 + 8 * i + 2 * c;
-                    *reinterpret_cast<float2*>(&part[warp][at]) = make_float2(acc[q][i][0], acc[q][i][1]);
-                    *reinterpret_cast<float2*>(&part[warp][at + 8 * NT * 8]) = make_float2(acc[q][i][2], acc[q][i][3]);
-                }
-            if (first) {
-#pragma unroll
-                for (int q = 0; q < 2 * MT; ++q) {
-                    uint32_t v = max(mx[q] & 0xFFFFu, mx[q] >> 16);
-                    v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-                    v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-                    if (c == 0) amax[warp][g + 8 * q] = v;
-                }
+            for (int i = 0; i < NT; ++i) {
+                const int at = (16 * q + g) * NT * 8 + 8 * i + 2 * c;
+                *reinterpret_cast<float2*>(&sums[at]) = make_float2(acc[q][i][0], acc[q][i][1]);
+                *reinterpret_cast<float2*>(&sums[at + 8 * NT * 8]) = make_float2(acc[q][i][2], acc[q][i][3]);
             }
-            __syncthreads();
-            for (int e = threadIdx.x; e < kSums; e += kThreads) {
-                float s = part[0][e];
+        if (first) {
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) s += part[w][e];
-                part[0][e] = s;                                // this CTA's slice of the sum
+            for (int q = 0; q < 4; ++q) {
+                uint32_t v = max(mx[q] & 0xFFFFu, mx[q] >> 16);
+                v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+                v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+                if (c == 0) amax[warp][g + 8 * q] = v;
             }
-            if (first && threadIdx.x < kRows) {
+        }
+        product_sync();
+        for (int e = threadIdx.x; e < kSums; e += kThreads) {
+            float s = part[e];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) s += part[w * kPartStride + e];
+            part[e] = s;                                       // this CTA's slice of the sum
+        }
+        if (first && threadIdx.x < kRows) {
+            uint32_t v = amax[0][threadIdx.x];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) v = max(v, amax[w][threadIdx.x]);
+            amax[0][threadIdx.x] = v;
+        }
+        if (S > 1) ptx::cluster_sync(); else product_sync();
+        if (first) {
+            if (threadIdx.x < kRows) {
                 uint32_t v = amax[0][threadIdx.x];
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) v = max(v, amax[w][threadIdx.x]);
-                amax[0][threadIdx.x] = v;
-            }
-            if (S > 1) ptx::cluster_sync(); else __syncthreads();
-            if (first) {
-                if (threadIdx.x < kRows) {
-                    uint32_t v = amax[0][threadIdx.x];
-                    for (int q = 0; S > 1 && q < S; ++q)
+                for (int q = 0; q < kMaxSplit; ++q)
+                    if (S > 1 && q < S)
                         v = max(v, __float_as_uint(ptx::ld_shared_cluster_f32(&amax[0][threadIdx.x], static_cast<uint32_t>(q))));
-                    const float sc = row_scale(v);
-                    scale_s[threadIdx.x] = sc;
-                    if (converts && rank == 0 && m0 + static_cast<int>(threadIdx.x) < p.M) p.rowscale[m0 + threadIdx.x] = sc;
-                }
-                __syncthreads();
+                scale_s[threadIdx.x] = row_scale(v);
             }
-            // every CTA of the cluster finishes its share of the tile's sums, two ranks at a time
-            for (int e = 2 * (static_cast<int>(threadIdx.x) + rank * kThreads); with && e < kSums; e += 2 * S * kThreads) {
-                float s0 = part[0][e], s1 = part[0][e + 1];
-                if (S > 1) {
-                    s0 = s1 = 0.0f;
-                    for (int q = 0; q < S; ++q) {
-                        s0 += ptx::ld_shared_cluster_f32(&part[0][e], static_cast<uint32_t>(q));
-                        s1 += ptx::ld_shared_cluster_f32(&part[0][e + 1], static_cast<uint32_t>(q));
-                    }
-                }
-                const int row = e / (NT * 8), j = j0 + e % (NT * 8);
-                const int m = m0 + row;
-                if (m < p.M && j < p.r && p.ids[m] == adapter) {
-                    const float sc = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
-                    s0 *= sc;
-                    s1 *= sc;
-                    const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));       // 2^-e_m
-                    __nv_bfloat16* o = p.tw + (static_cast<int64_t>(m) * p.pairs + pair) * 2 * p.r + 16 * (j / 8) + j % 8;
-                    *reinterpret_cast<uint32_t*>(o) = fused::bf16_part(s0 * inv, s1 * inv, false);
-                    *reinterpret_cast<uint32_t*>(o + 8) = fused::bf16_part(s0 * inv, s1 * inv, true);
-                }
-            }
-            if (S > 1) ptx::cluster_sync(); else __syncthreads();      // the sums are read before the next pass
-            first = false;
-            if (!with) break;
+            product_sync();
         }
-        if (converts) {
-            if (rank == 0) {
-                // rows without an adapter: zeros in tw, so that a tile's box of it needs no mask
-                const int pieces = p.pairs * p.r / 4;
-                for (int row = warp; row < kRows && m0 + row < p.M; row += kWarps) {
-                    if (__shfl_sync(0xFFFFFFFFu, mine, row) >= 0) continue;
-                    uint4* o = reinterpret_cast<uint4*>(p.tw) + static_cast<int64_t>(m0 + row) * pieces;
-                    for (int i = lane; i < pieces; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        // every CTA of the cluster finishes its share of the tile's sums, two ranks at a time
+        for (int e = 2 * (static_cast<int>(threadIdx.x) + rank * kThreads); e < kSums; e += 2 * S * kThreads) {
+            const int row = e / (NT * 8), j = j0 + e % (NT * 8);
+            if (j >= p.r || id_s[row] != adapter) continue;
+            float s0 = part[e], s1 = part[e + 1];
+            if (S > 1) {
+                float v0[kMaxSplit], v1[kMaxSplit];            // every CTA's loads before the first sum
+#pragma unroll
+                for (int q = 0; q < kMaxSplit; ++q) {
+                    v0[q] = q < S ? ptx::ld_shared_cluster_f32(&part[e], static_cast<uint32_t>(q)) : 0.0f;
+                    v1[q] = q < S ? ptx::ld_shared_cluster_f32(&part[e + 1], static_cast<uint32_t>(q)) : 0.0f;
+                }
+                s0 = v0[0];
+                s1 = v1[0];
+#pragma unroll
+                for (int q = 1; q < kMaxSplit; ++q) {
+                    s0 += v0[q];
+                    s1 += v1[q];
                 }
             }
-            // the CTA's columns of its rows, a row per warp at a time
-            const int c0 = 4 * kb0, c1 = 4 * kb1;
-            for (int row = warp; row < kRows && m0 + row < p.M; row += kWarps) {
-                const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));
-                const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(m0 + row) * p.K);
-                uint4* dst = reinterpret_cast<uint4*>(p.xh + static_cast<int64_t>(m0 + row) * p.K);
-                for (int i = c0 + lane; i < c1; i += 32 * 4) {
-                    uint4 v[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (i + 32 * u < c1) v[u] = __ldg(src + i + 32 * u);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (i + 32 * u < c1) dst[i + 32 * u] = p.bits == 4 ? convert8<4>(v[u], inv) : convert8<8>(v[u], inv);
-                }
-            }
+            const float f = factor * __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));     // s 2^-e_m
+            __nv_bfloat16* o = p.tw + (static_cast<int64_t>(m0 + row) * p.pairs + pair) * 2 * p.r + 16 * (j / 8) + j % 8;
+            *reinterpret_cast<uint32_t*>(o) = fused::bf16_part(s0 * f, s1 * f, false);
+            *reinterpret_cast<uint32_t*>(o + 8) = fused::bf16_part(s0 * f, s1 * f, true);
         }
+        first = false;
+        for (int n = 0; n < p.passes; ++n) leaders &= leaders - 1;
+        // the sums are read, by this CTA and its peers, before the rings are filled again or the CTA ends
+        ptx::fence_proxy_async_smem();
+        if (S > 1) ptx::cluster_sync(); else product_sync();
+    }
+    if (!ok && lane == 0)                                      // an expired wait: leave no copy in flight
+        for (uint32_t at = issued > kSlots ? issued - kSlots : 0; at < issued; ++at)
+            ptx::mbar_wait(&full[warp][at % kSlots], (at / kSlots) & 1u, nullptr);
+}
+
+// The activations' conversion (as convert_x_kernel) of rows first, first + step, ... of the tile, a row by a pair of
+// warps: its loads go out together and stay in registers (up to 4608 columns; more are read again from L2).
+template <int kBits>
+__device__ __forceinline__ void convert_rows(const ShrinkParams& p, int m0, int first, int step, int group) {
+    __shared__ float red[2][kConvGroups][2];
+    constexpr int kCache = 9;
+    const int tid = static_cast<int>(threadIdx.x - kThreads) & (kConvThreads - 1);
+    const int n8 = p.K / 8;
+    int parity = 0;
+    for (int row = first; row < kRows && m0 + row < p.M; row += step, parity ^= 1) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(m0 + row) * p.K);
+        uint4* dst = reinterpret_cast<uint4*>(p.xh + static_cast<int64_t>(m0 + row) * p.K);
+        uint4 v[kCache];
+#pragma unroll
+        for (int j = 0; j < kCache; ++j) {
+            const int i = tid + j * kConvThreads;
+            v[j] = i < n8 ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kCache; ++j) top = absmax_bf16x8(v[j], top);
+#pragma unroll 2
+        for (int i = tid + kCache * kConvThreads; i < n8; i += kConvThreads) top = absmax_bf16x8(__ldg(src + i), top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if ((tid & 31) == 0) red[parity][group][tid >> 5] = top;
+        asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "n"(kConvThreads) : "memory");
+        top = fmaxf(red[parity][group][0], red[parity][group][1]);
+        const float sc = row_scale(__float_as_uint(top) >> 16);
+        if (tid == 0) p.rowscale[m0 + row] = sc;
+        const float inv = __uint_as_float(0x7F000000u - __float_as_uint(sc));
+#pragma unroll
+        for (int j = 0; j < kCache; ++j) {
+            const int i = tid + j * kConvThreads;
+            if (i < n8) dst[i] = convert8<kBits>(v[j], inv);
+        }
+#pragma unroll 2
+        for (int i = tid + kCache * kConvThreads; i < n8; i += kConvThreads) dst[i] = convert8<kBits>(__ldg(src + i), inv);
+    }
+}
+
+// Everything the adapters of a fused call need before the GEMM, in one launch: the token tiles' adapter lists, the
+// activations' conversion and the adapters' first product.  grid (plan_x + tiles * passes * chunks * pairs, S), cluster
+// (1, S, 1): first the lists, then the CTAs of every tile of 32 rows.  A tile's first column of CTAs also converts its
+// rows, in warps of their own beside the product's, so that the two readers of a row meet in L2 (33792 x 4608, rank 32:
+// 408 MB read from DRAM for 311 MB of x).  What bounds it there is the way from L2 to the SMs, 1.5 GB in 162 us: x twice,
+// its converted copy, and A once per tile.  (One kernel after the other read x from DRAM twice, 182 us; both by the same
+// warps, the tile held in shared memory between product and conversion, spent its time in one tile's barriers, 265 us.)
+template <int NT>
+__global__ void __launch_bounds__(kBlock, 2) lora_prepare_kernel(const __grid_constant__ CUtensorMap map_x,
+                                                                 const __grid_constant__ CUtensorMap map_a0,
+                                                                 const __grid_constant__ CUtensorMap map_a1,
+                                                                 const ShrinkParams p) {
+    ptx::launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    const int S = static_cast<int>(gridDim.y), rank = static_cast<int>(blockIdx.y);            // rank in the cluster
+    const int bx = static_cast<int>(blockIdx.x) - p.plan_x;
+    const int products = p.passes * p.chunks * p.pairs;
+    const int tile = bx / products, i = bx - tile * products;
+    if (threadIdx.x >= kThreads) {
+        if (bx < 0 || i != 0) return;
+        const int group = static_cast<int>(threadIdx.x - kThreads) / kConvThreads;
+        if (p.bits == 4) convert_rows<4>(p, tile * kRows, rank + S * group, S * kConvGroups, group);
+        else convert_rows<8>(p, tile * kRows, rank + S * group, S * kConvGroups, group);
+        return;
+    }
+    if (bx < 0) {
+        const int t_blk = static_cast<int>(blockIdx.x) * S + rank;
+        if (t_blk < p.num_t) plan_tile(p, t_blk);
+    } else {
+        const int pass = i % p.passes, chunk = i / p.passes % p.chunks, pair = i / p.passes / p.chunks;
+        uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+        shrink_tile<NT>(map_x, pair == 0 ? map_a0 : map_a1, p, smem, tile, pass, pair, chunk * NT * 8, rank, S);
     }
     // Launched behind the parameter transpose under programmatic dependent launch; as with the conversion of the
     // plain layer, the last CTA waits for it, so that this kernel's completion implies both.

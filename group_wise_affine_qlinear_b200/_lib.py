@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -43,10 +44,11 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libqlinear.so (built in-tree by group_wise_affine_qlinear_b200.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
-        if _lib is not None:
-            return _lib
-        _lib = load_library(library_path())
+        if _lib is None:
+            _lib = load_library(library_path())
         return _lib
 
 
@@ -355,20 +357,20 @@ def _on_stream(dev: int, stream, call):
             return call(stream.cuda_stream)
 
 
-def _need_workspace(workspace: torch.Tensor | None, dev: torch.device) -> None:
+def _need_workspace(workspace: torch.Tensor | None, dev: int) -> None:
     if workspace is None:
         return
-    if not isinstance(workspace, torch.Tensor) or workspace.device != dev:
-        raise ValueError(f"workspace must be a tensor on {dev}")
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be a tensor on cuda:{dev}")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
 
 
 def _adapter_shape(a: torch.Tensor, b: torch.Tensor, what: str) -> tuple[int, int]:
     """(adapters, rank) of lora_a [L][r][K] and lora_b [L][N][r]."""
-    for name, t in ((what + "_a", a), (what + "_b", b)):
+    for name, t in (("_a", a), ("_b", b)):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise ValueError(f"{name} must be a tensor of three dimensions")
+            raise ValueError(f"{what}{name} must be a tensor of three dimensions")
     n, r, _ = a.shape
     if n < 1 or r < 8 or r % 8 or r > LORA_MAX_RANK:
         raise ValueError(f"{what}_a: at least one adapter, of a rank that is a multiple of 8 up to {LORA_MAX_RANK}")
@@ -379,6 +381,18 @@ def _need_rows(ids: torch.Tensor, scale: torch.Tensor | None, M: int, n: int) ->
     _need_cuda(ids, "adapter_ids", torch.int32, (M,))
     if scale is not None:
         _need_cuda(scale, "lora_scale", torch.float32, (n,))
+
+
+@functools.lru_cache(maxsize=1024)
+def _lora_workspace(dev: int, M: int, K: int, N: int, adapters: int, rank: int, bits: int) -> int:
+    """lora_workspace_size() on device `dev` (which is current); it is a function of the shape and the SM count."""
+    return lora_workspace_size(M, K, N, adapters, rank, bits)
+
+
+@functools.lru_cache(maxsize=1024)
+def _swiglu_lora_workspace(dev: int, M: int, K: int, I: int, adapters: int, rank: int) -> int:
+    """swiglu_lora_workspace_size() on device `dev` (which is current)."""
+    return swiglu_lora_workspace_size(M, K, I, adapters, rank)
 
 
 def lora_workspace_size(M: int, K: int, N: int, adapters: int, rank: int, bits: int = 4) -> int:
@@ -438,12 +452,12 @@ def _forward_lora(x, codes, scales, biases, lora_a, lora_b, ids, lora_scale, out
             _need_cuda(out, "out", out_dtype, (M, N))
         _same_device(x.device, (("codes", codes), ("scales", scales), ("biases", biases), ("lora_a", lora_a),
                                 ("lora_b", lora_b), ("adapter_ids", ids), ("lora_scale", lora_scale), ("out", out)))
-    _need_workspace(workspace, x.device)
+    _need_workspace(workspace, dev)
     name = "qlinear_lora_forward" if bits == 4 else "qlinear8_lora_forward"
 
     def call(st):
         y = x.new_empty((M, N), dtype=out_dtype) if out is None else out
-        ws = (x.new_empty(lora_workspace_size(M, K, N, n, r, bits), dtype=torch.uint8) if workspace is None
+        ws = (x.new_empty(_lora_workspace(dev, M, K, N, n, r, bits), dtype=torch.uint8) if workspace is None
               else workspace)
         _check(getattr(L, name)(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(),
                                 lora_a.data_ptr(), lora_b.data_ptr(), _ptr(lora_scale), ids.data_ptr(), y.data_ptr(),
@@ -503,11 +517,11 @@ def swiglu_lora(x: torch.Tensor, gate, up, gate_lora, up_lora, adapter_ids: torc
                                 ("up scales", us), ("up biases", ub), ("gate_lora_a", ga), ("gate_lora_b", gbb),
                                 ("up_lora_a", ua), ("up_lora_b", ubb), ("adapter_ids", adapter_ids),
                                 ("lora_scale", lora_scale), ("out", out)))
-    _need_workspace(workspace, x.device)
+    _need_workspace(workspace, dev)
 
     def call(st):
         h = x.new_empty((M, I), dtype=out_dtype) if out is None else out
-        ws = (x.new_empty(swiglu_lora_workspace_size(M, K, I, n, r), dtype=torch.uint8) if workspace is None
+        ws = (x.new_empty(_swiglu_lora_workspace(dev, M, K, I, n, r), dtype=torch.uint8) if workspace is None
               else workspace)
         _check(L.qlinear_swiglu_lora_forward(x.data_ptr(), gc.data_ptr(), gs.data_ptr(), gb.data_ptr(), uc.data_ptr(),
                                              us.data_ptr(), ub.data_ptr(), ga.data_ptr(), gbb.data_ptr(), ua.data_ptr(),
@@ -547,7 +561,7 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: 
     M, D = x.shape
     xd = x.dtype
     xt = _dtype_code(x, "x")
-    S, yt = 1, _BF16
+    S, yt = 0, _BF16                       # S 0: y is [M][D]
     if y is not None:
         if not isinstance(y, torch.Tensor) or y.dim() not in (2, 3):
             raise ValueError("y must be a tensor [M][D] or [S][M][D]")
@@ -556,6 +570,8 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: 
             if yt == _BF16:
                 raise ValueError("partials y [S][M][D] must be float32")
             S = y.shape[0]
+            if S == 0:
+                raise ValueError("y holds no partials")
     elif post_weight is not None or gate is not None or out is not None:
         raise ValueError("post_weight, gate and out need y")
     if not post_norm and post_weight is not None:
@@ -565,45 +581,41 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: 
             raise ValueError("pre_weight, scale, shift and h need pre_norm")
         if y is None:
             raise ValueError("nothing to compute: no y and no pre_norm")
-    # (name, tensor, dtype, shape) of everything given; T is the number of segments, P the vectors' type
+    # T: segments of gate, scale and shift; P: the vectors' type
     T = P = None
-    given = [("x", x, xd, (M, D))]
-    if y is not None:
-        given.append(("y", y, y.dtype, (M, D) if y.dim() == 2 else (S, M, D)))
-    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight), ("gate", gate), ("scale", scale),
-                    ("shift", shift)):
-        if t is None:
-            continue
-        if P is None:
-            P = t.dtype
-            pt = _dtype_code(t, name)
-        if name[-6:] == "weight":
-            given.append((name, t, P, (D,)))
-        else:
-            if T is None:
-                T = t.shape[0]
-            given.append((name, t, P, (T, D)))
-    if segment_ids is not None:
-        given.append(("segment_ids", segment_ids, torch.int32, (M,)))
-    elif T is not None and T != 1:
+    for t in (gate, scale, shift):
+        if t is not None:
+            T, P = t.shape[0], t.dtype
+            break
+    else:
+        if post_weight is not None:
+            P = post_weight.dtype
+        elif pre_weight is not None:
+            P = pre_weight.dtype
+    if segment_ids is None and T is not None and T != 1:
         raise ValueError("gate, scale and shift of several segments need segment_ids")
-    if out is not None:
-        given.append(("out", out, xd, (M, D)))
-    if h is not None:
-        given.append(("h", h, torch.bfloat16, (M, D)))
     dev = x.get_device()
-    for name, t, dtype, shape in given:
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+    rows, vec, mod = (M, D), (D,), (T, D)
+    for t, dtype, shape, name in ((x, xd, rows, "x"), (y, None if y is None else y.dtype, rows if S == 0 else (S, M, D), "y"),
+                                  (post_weight, P, vec, "post_weight"), (gate, P, mod, "gate"),
+                                  (pre_weight, P, vec, "pre_weight"), (scale, P, mod, "scale"),
+                                  (shift, P, mod, "shift"), (segment_ids, torch.int32, rows[:1], "segment_ids"),
+                                  (out, xd, rows, "out"), (h, torch.bfloat16, rows, "h")):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 or
+                              not t.is_contiguous()):
             _need_cuda(t, name, dtype, shape)
             _same_device(x.device, ((name, t),))
+    pt = _BF16 if P is None or P is torch.bfloat16 else _F32
+    if pt == _F32 and P is not torch.float32:
+        raise ValueError(f"the weights, gate, scale and shift must be bfloat16 or float32, got {P}")
 
     def call(st):
         r = x.new_empty((M, D)) if y is not None and out is None else out
         n = x.new_empty((M, D), dtype=torch.bfloat16) if pre_norm and h is None else h
         # without per-segment vectors every segment is as good as any other
-        _check(L.qlinear_norm_residual(x.data_ptr(), xt, _ptr(y), yt, S, 1 if post_norm else 0, _ptr(post_weight),
+        _check(L.qlinear_norm_residual(x.data_ptr(), xt, _ptr(y), yt, S or 1, 1 if post_norm else 0, _ptr(post_weight),
                                        _ptr(gate), residual_scale, branch_scale, _ptr(pre_weight), _ptr(scale),
-                                       _ptr(shift), _BF16 if P is None else pt, _ptr(segment_ids),
+                                       _ptr(shift), pt, _ptr(segment_ids),
                                        2 ** 31 - 1 if T is None else T, eps, _ptr(r), _ptr(n), M, D, st),
                "qlinear_norm_residual")
         return (x if y is None else r), n

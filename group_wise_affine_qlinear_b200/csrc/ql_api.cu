@@ -77,6 +77,12 @@ cudaError_t skinny_smem_attr() {
     const cudaError_t e = cudaFuncSetAttribute(skinny::skinny_kernel<NT, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                skinny::Layout<NT, B>::kSmemBytes);
     if (e != cudaSuccess) return e;
+    if constexpr (B == 4) {
+        const cudaError_t p = cudaFuncSetAttribute(skinny::skinny_kernel<NT, B, true, true>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   skinny::Layout<NT, B>::kSmemBytes);
+        if (p != cudaSuccess) return p;
+    }
     return cudaFuncSetAttribute(skinny::skinny_kernel<NT, B, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 skinny::Layout<NT, B>::kSmemBytes);
 }
@@ -435,21 +441,23 @@ struct LoraPlan {
 };
 
 // Weight-streaming path: about as many one-warp tasks as the main kernel has drain warps (4 per SM), by cutting K into
-// up to 32 slices of at least four 32-column blocks.
-LoraPlan lora_plan_streaming(int64_t M, int64_t K, int r, int L, size_t base, int sm_count) {
+// up to 64 slices of at least four 32-column blocks.
+LoraPlan lora_plan_streaming(int64_t M, int64_t K, int r, int L, int pairs, size_t base, int sm_count) {
     LoraPlan lp;
     const int64_t tiles = (M + lora::kTile - 1) / lora::kTile;
     lp.per_tile = static_cast<int>(std::min<int64_t>(std::min<int64_t>(L, M), lora::kTile));
     lp.chunks = (r + 15) / 16;
-    const int64_t tasks = tiles * lp.per_tile * lp.chunks;
-    lp.slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({32, 4 * sm_count / tasks, K / 128})));
+    const int64_t tasks = pairs * tiles * lp.per_tile * lp.chunks;
+    lp.slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({64, 4 * sm_count / tasks, K / 128})));
     lp.off_t = round_up(base, 256);
-    lp.workspace = lp.off_t + round_up(static_cast<size_t>(lp.slices) * M * r * 4, 256);
+    lp.workspace = lp.off_t + round_up(static_cast<size_t>(lp.slices) * pairs * M * r * 4, 256);
     return lp;
 }
 
-// Fused path: tiles of 32 rows.  Where they are few, a cluster of up to 8 CTAs shares a tile's K range, each warp with
-// two 64-column chunks at least, and a tile's distinct adapters go to up to 16 CTAs.
+// Fused path: tiles of 32 rows, a cluster of S CTAs sharing a tile's K range.  A CTA's time is about 6 us of barriers
+// and first loads and 1 us for each of its warps' 64-column chunks (measured on a B200 from 333 to 33792 rows), and
+// two CTAs fit an SM; the S with the least time is taken, of two chunks per warp at least.  CTAs left over share the
+// tiles' distinct adapters.
 LoraPlan lora_plan_fused(int64_t M, int64_t K, int r, int L, int pairs, size_t base, int sm_count) {
     LoraPlan lp;
     const int64_t tiles = (M + lora::kRows - 1) / lora::kRows;
@@ -457,10 +465,17 @@ LoraPlan lora_plan_fused(int64_t M, int64_t K, int r, int L, int pairs, size_t b
     lp.nt = r8 >= 3 ? 4 : r8;
     lp.chunks = (r8 + lp.nt - 1) / lp.nt;
     const int64_t ctas = tiles * pairs * lp.chunks;
-    const int64_t want = 2 * sm_count;                         // the first product's CTAs that fit the GPU at once
-    while (2 * lp.S <= lora::kMaxSplit && 2 * ctas * lp.S <= want && K / lora::kCols >= 2 * lora::kWarps * 2 * lp.S) lp.S *= 2;
-    while (lp.passes < std::min(L, lora::kRows) && ctas * lp.S * lp.passes < want) ++lp.passes;
-    if (M <= 512) lp.passes = std::min(L, lora::kTile);
+    const int64_t room = 2 * sm_count;
+    double best = 0.0;
+    for (int S = 1; S <= lora::kMaxSplit && (S == 1 || K / lora::kCols >= 2 * lora::kWarps * S); S *= 2) {
+        const double waves = static_cast<double>((ctas * S + room - 1) / room);
+        const double t = waves * (6.0 + static_cast<double>(K) / (lora::kCols * lora::kWarps * S));
+        if (S == 1 || t < best) {
+            best = t;
+            lp.S = S;
+        }
+    }
+    lp.passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(room / (ctas * lp.S), std::min(L, lora::kRows))));
     lp.off_t = round_up(base, 256);
     const size_t num_t = static_cast<size_t>((M + fused::BT - 1) / fused::BT);
     lp.off_slot = lp.off_t + round_up(static_cast<size_t>(pairs) * M * r * 4, 256);     // two bf16 parts of t
@@ -472,7 +487,7 @@ LoraPlan lora_plan_fused(int64_t M, int64_t K, int r, int L, int pairs, size_t b
 
 LoraPlan lora_plan(const Plan& pl, int64_t M, int64_t K, int r, int L, int sm_count) {
     return pl.path == QL_PATH_TC_FUSED ? lora_plan_fused(M, K, r, L, 1, pl.workspace, sm_count)
-                                       : lora_plan_streaming(M, K, r, L, pl.workspace, sm_count);
+                                       : lora_plan_streaming(M, K, r, L, 1, pl.workspace, sm_count);
 }
 
 // Fused path: t of every row's adapter, the converted activations and the token tiles' adapter lists, launched behind
@@ -672,6 +687,36 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
     return launch_status();
 }
 
+// Weight-streaming path: the first product's tasks, and what the reduce kernel needs for the second.
+lora::DotTasks dot_tasks(const LoraArgs& la, const LoraPlan& lp, const void* x, int64_t M, int64_t K, uint8_t* ws) {
+    lora::DotTasks d = {};
+    d.x = static_cast<const __nv_bfloat16*>(x);
+    for (int i = 0; i < 2; ++i) d.a[i] = static_cast<const __nv_bfloat16*>(la.a[i]);
+    d.ids = la.ids;
+    d.tp = reinterpret_cast<float*>(ws + lp.off_t);
+    d.M = static_cast<int>(M);
+    d.K = static_cast<int>(K);
+    d.r = la.r;
+    d.L = la.L;
+    d.pairs = la.pairs;
+    d.per_tile = lp.per_tile;
+    d.chunks = lp.chunks;
+    d.slices = lp.slices;
+    return d;
+}
+
+lora::ExpandParams expand_params(const LoraArgs& la, const LoraPlan& lp, uint8_t* ws) {
+    lora::ExpandParams e = {};
+    for (int i = 0; i < 2; ++i) e.b[i] = static_cast<const __nv_bfloat16*>(la.b[i]);
+    e.scale = la.scale;
+    e.tp = reinterpret_cast<const float*>(ws + lp.off_t);
+    e.ids = la.ids;
+    e.r = la.r;
+    e.L = la.L;
+    e.slices = lp.slices;
+    return e;
+}
+
 // Launches the weight-streaming kernel, with or without adapters.
 template <int NT, int B>
 ql_status launch_skinny(dim3 grid, cudaStream_t st, const CUtensorMap& mc, const CUtensorMap& mx, const CUtensorMap& ms,
@@ -681,6 +726,25 @@ ql_status launch_skinny(dim3 grid, cudaStream_t st, const CUtensorMap& mc, const
                                 skinny::Layout<NT, B>::kSmemBytes, st, mc, mx, ms, mb, p);
     return launch_dependent(skinny::skinny_kernel<NT, B>, grid, skinny::kThreads, skinny::Layout<NT, B>::kSmemBytes, st,
                             mc, mx, ms, mb, static_cast<const skinny::Params&>(p));
+}
+
+// Code, scale and bias maps of one weight for the weight-streaming kernel: boxes of 128 bytes (32 words) of codes of
+// each of 128 rows, 128-byte swizzle, for either code width; scale and bias boxes of 8 groups where the row pitch allows
+// (G % 8 == 0: a multiple of 16 bytes; every chunk then lies inside one box).
+ql_status skinny_weight_maps(const uint32_t* codes, const void* scales, const void* biases, int64_t K, int64_t N, int bits,
+                             bool param_tma, CUtensorMap* mc, CUtensorMap* ms, CUtensorMap* mb) {
+    const int64_t G = K / kGroup;
+    ql_status s;
+    if ((s = encode_2d(mc, CU_TENSOR_MAP_DATA_TYPE_UINT32, codes, K * bits / 32, N, K * bits / 8,
+                       skinny::kBoxBytes / skinny::BW / 4, skinny::BW, CU_TENSOR_MAP_SWIZZLE_128B)) != QL_OK)
+        return s;
+    *ms = *mb = *mc;
+    if (!param_tma) return QL_OK;
+    if ((s = encode_2d(ms, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, scales, G, N, G * 2, skinny::kParGroups, skinny::BW,
+                       CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK)
+        return s;
+    return encode_2d(mb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, biases, G, N, G * 2, skinny::kParGroups, skinny::BW,
+                     CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
@@ -693,30 +757,15 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
     CUtensorMap mc, mx;
     ql_status s;
     const int bits = pl.bits;
-    // code boxes: 128 bytes (32 words) of each of 128 rows, 128-byte swizzle, for either code width
-    if ((s = encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT32, codes, K * bits / 32, N, K * bits / 8,
-                       skinny::kBoxBytes / skinny::BW / 4, skinny::BW, CU_TENSOR_MAP_SWIZZLE_128B)) != QL_OK)
-        return s;
+    const bool param_tma = (G % skinny::kParGroups) == 0;
+    CUtensorMap ms, mb;
+    if ((s = skinny_weight_maps(codes, scales, biases, K, N, bits, param_tma, &mc, &ms, &mb)) != QL_OK) return s;
     if ((s = encode_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, K, M, K * 2, skinny::BK, pl.nt,
                        CU_TENSOR_MAP_SWIZZLE_128B)) != QL_OK)
         return s;
-    // scale/bias boxes of 8 groups by TMA need a 16-byte row pitch (G % 8 == 0); every chunk then
-    // lies inside one box
-    const bool param_tma = (G % skinny::kParGroups) == 0;
-    CUtensorMap ms = mc, mb = mc;
-    if (param_tma) {
-        if ((s = encode_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, scales, G, N, G * 2, skinny::kParGroups, skinny::BW,
-                           CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK)
-            return s;
-        if ((s = encode_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, biases, G, N, G * 2, skinny::kParGroups, skinny::BW,
-                           CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK)
-            return s;
-    }
     skinny::LoraParams p = {};
     if (la)
-        p.dot = {static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(la->a[0]), la->ids,
-                 reinterpret_cast<float*>(wsb + lp->off_t), static_cast<int>(M), static_cast<int>(K), la->r, la->L,
-                 lp->per_tile, lp->chunks, lp->slices};
+        p.dot = dot_tasks(*la, *lp, x, M, K, wsb);
     p.param_tma = param_tma ? 1 : 0;
     p.partial = reinterpret_cast<float*>(wsb);
     p.scales = static_cast<const __half*>(scales);
@@ -757,17 +806,9 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
     const int* rexp = rowexp;
     const dim3 red_grid(static_cast<unsigned>(p.num_w), static_cast<unsigned>((M + 1) / 2));
     if (la) {
-        lora::ExpandParams ep;
-        ep.b = static_cast<const __nv_bfloat16*>(la->b[0]);
-        ep.scale = la->scale;
-        ep.tp = reinterpret_cast<const float*>(wsb + lp->off_t);
-        ep.slices = lp->slices;
-        ep.ids = la->ids;
-        ep.r = la->r;
-        ep.L = la->L;
-        auto red = bf16_out ? lora::lora_reduce_kernel<true> : lora::lora_reduce_kernel<false>;
+        auto red = bf16_out ? lora::lora_reduce_kernel<true, false> : lora::lora_reduce_kernel<false, false>;
         s = launch_dependent(red, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt, p.units, pl.ctas, pl.segmax,
-                             p.partial_elems, ep);
+                             p.partial_elems, expand_params(*la, *lp, wsb));
     } else if (bf16_out)
         s = launch_dependent(skinny::skinny_reduce_kernel<true>, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt,
                              p.units, pl.ctas, pl.segmax, p.partial_elems);
@@ -864,6 +905,82 @@ ql_status run_swiglu(const SwigluPlan& pl, const void* x, const uint32_t* gc, co
     return launch_status();
 }
 
+// The pair with adapters for up to 64 tokens: both weights streamed in one launch (as run_skinny, the up weight's tiles
+// after the gate weight's), g and u brought together by the reduce kernel.  24 tokens of 12288 columns, K = 4608, rank
+// 16: 36 us a call against 62 on the fused path, whose tiles cost the same for 192 tokens.
+ql_status run_swiglu_streaming(const Plan& pl, const LoraPlan& lp, const LoraArgs& la, const void* x, const uint32_t* gc,
+                               const void* gs, const void* gb, const uint32_t* uc, const void* us, const void* ub, void* h,
+                               bool bf16_out, int64_t M, int64_t K, int64_t I, void* ws, cudaStream_t st) {
+    const int64_t G = K / kGroup;
+    uint8_t* wsb = static_cast<uint8_t*>(ws);
+    void* xp = wsb + pl.off_xp;
+    int* rowexp = reinterpret_cast<int*>(wsb + pl.off_re);
+    const bool param_tma = (G % skinny::kParGroups) == 0;
+    CUtensorMap mc, ms, mb, mx;
+    skinny::PairParams p = {};
+    ql_status s;
+    if ((s = skinny_weight_maps(gc, gs, gb, K, I, 4, param_tma, &mc, &ms, &mb)) != QL_OK) return s;
+    if ((s = skinny_weight_maps(uc, us, ub, K, I, 4, param_tma, &p.map_codes2, &p.map_scales2, &p.map_biases2)) != QL_OK)
+        return s;
+    if ((s = encode_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, K, M, K * 2, skinny::BK, pl.nt,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) != QL_OK)
+        return s;
+    p.param_tma = param_tma ? 1 : 0;
+    p.partial = reinterpret_cast<float*>(wsb);
+    p.scales = static_cast<const __half*>(gs);
+    p.biases = static_cast<const __half*>(gb);
+    p.scales2 = static_cast<const __half*>(us);
+    p.biases2 = static_cast<const __half*>(ub);
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(I);
+    p.G = static_cast<int>(G);
+    const int tiles = static_cast<int>((I + skinny::BW - 1) / skinny::BW);
+    p.num_w = 2 * tiles;
+    p.cpt = static_cast<int>((G + skinny::Layout<16, 4>::CG - 1) / skinny::Layout<16, 4>::CG);
+    p.units = pl.units;
+    p.segmax = pl.segmax;
+    p.partial_elems = static_cast<int64_t>(pl.ctas) * pl.segmax * M * skinny::BW;
+    p.dot = dot_tasks(la, lp, x, M, K, wsb);
+    const dim3 pre_grid(static_cast<unsigned>(skinny::kPrepCluster), static_cast<unsigned>(M));
+    skinny::skinny_prepass_kernel<4><<<pre_grid, skinny::kPrepThreads, 0, st>>>(
+        static_cast<const uint4*>(x), static_cast<uint4*>(xp), rowexp, static_cast<int>(K));
+    if ((s = launch_status()) != QL_OK) return s;
+    prof_begin(st);
+    const dim3 grid(static_cast<unsigned>(pl.ctas));
+    s = pl.nt == 16   ? launch_dependent(skinny::skinny_kernel<16, 4, true, true>, grid, skinny::kThreads,
+                                         skinny::Layout<16, 4>::kSmemBytes, st, mc, mx, ms, mb, p)
+        : pl.nt == 32 ? launch_dependent(skinny::skinny_kernel<32, 4, true, true>, grid, skinny::kThreads,
+                                         skinny::Layout<32, 4>::kSmemBytes, st, mc, mx, ms, mb, p)
+                      : launch_dependent(skinny::skinny_kernel<64, 4, true, true>, grid, skinny::kThreads,
+                                         skinny::Layout<64, 4>::kSmemBytes, st, mc, mx, ms, mb, p);
+    if (s != QL_OK) return s;
+    prof_end(st);
+    const float* part = p.partial;
+    const int* rexp = rowexp;
+    const dim3 red_grid(static_cast<unsigned>(tiles), static_cast<unsigned>((M + 1) / 2));
+    auto red = bf16_out ? lora::lora_reduce_kernel<true, true> : lora::lora_reduce_kernel<false, true>;
+    s = launch_dependent(red, red_grid, 256, 0, st, part, rexp, h, p.M, p.N, p.cpt, p.units, pl.ctas, pl.segmax,
+                         p.partial_elems, expand_params(la, lp, wsb));
+    if (s != QL_OK) return s;
+    set_dispatch("path=tc_skinny_swiglu_lora bits=4 nt=%d ctas=%d segmax=%d units=%lld launches=3", pl.nt, pl.ctas,
+                 pl.segmax, static_cast<long long>(pl.units));
+    return launch_status();
+}
+
+// Plans of the pair with adapters: streaming up to 64 tokens (sp.path QL_PATH_TC_SKINNY, a weight of both's tiles), else
+// the fused kernel.
+ql_status swiglu_lora_plan(int64_t M, int64_t K, int64_t I, int r, int L, int sm_count, Plan* sp, LoraPlan* lp) {
+    if (M > 64) {
+        sp->path = QL_PATH_TC_FUSED;
+        *lp = lora_plan_fused(M, K, r, L, 2, swiglu_plan(M, K, I).workspace, sm_count);
+        return QL_OK;
+    }
+    const int64_t rows = (I + skinny::BW - 1) / skinny::BW * skinny::BW;
+    const ql_status s = make_plan(M, K, 2 * rows, QL_PATH_TC_SKINNY, 0, sm_count, 4, sp);
+    if (s == QL_OK) *lp = lora_plan_streaming(M, K, r, L, 2, sp->workspace, sm_count);
+    return s;
+}
+
 // Adapter arguments: ranks in steps of 8 (a 16-byte row of B), up to the shrink kernel's widest.
 ql_status check_lora(const LoraArgs& la) {
     if (la.L < 1 || la.r < 1 || !la.ids) return QL_ERR_INVALID_ARG;
@@ -909,11 +1026,12 @@ ql_status swiglu_impl(const void* x, const uint32_t* gc, const void* gs, const v
     if (la && lora_overlaps(*la, M, K, I, h, hb)) return QL_ERR_INVALID_ARG;
     const SwigluPlan pl = swiglu_plan(M, K, I);
     DeviceInfo* dev = nullptr;
+    Plan sp;
     LoraPlan lp;
     size_t need = pl.workspace;
     if (la) {
         if ((s = device_info(&dev)) != QL_OK) return s;
-        lp = lora_plan_fused(M, K, la->r, la->L, 2, pl.workspace, dev->sm_count);
+        if ((s = swiglu_lora_plan(M, K, I, la->r, la->L, dev->sm_count, &sp, &lp)) != QL_OK) return s;
         need = lp.workspace;
     }
     if (!workspace || workspace_bytes < need) return QL_ERR_WORKSPACE;
@@ -923,6 +1041,9 @@ ql_status swiglu_impl(const void* x, const uint32_t* gc, const void* gs, const v
         if (overlap(workspace, need, in[i], in_bytes[i])) return QL_ERR_INVALID_ARG;
     if (la && lora_overlaps(*la, M, K, I, workspace, need)) return QL_ERR_INVALID_ARG;
     if ((s = device_info(&dev)) != QL_OK) return s;
+    if (la && sp.path == QL_PATH_TC_SKINNY)
+        return run_swiglu_streaming(sp, lp, *la, x, gc, gs, gb, uc, us, ub, h, out_dtype == QL_BF16, M, K, I, workspace,
+                                    stream);
     return run_swiglu(pl, x, gc, gs, gb, uc, us, ub, h, out_dtype == QL_BF16, M, K, I, workspace, stream,
                       dev->sm_count, la, &lp);
 }
@@ -1367,7 +1488,10 @@ size_t qlinear_swiglu_lora_workspace_size(int64_t M, int64_t K, int64_t I, int32
     DeviceInfo* dev = nullptr;
     int sms = 148;
     if (device_info(&dev) == QL_OK) sms = dev->sm_count;
-    return lora_plan_fused(M, K, r, L, 2, swiglu_plan(M, K, I).workspace, sms).workspace;
+    Plan sp;
+    LoraPlan lp;
+    if (swiglu_lora_plan(M, K, I, r, L, sms, &sp, &lp) != QL_OK) return static_cast<size_t>(-1);
+    return lp.workspace;
 }
 
 ql_status qlinear_swiglu_lora_forward(const void* x, const uint32_t* gate_codes, const void* gate_scales,

@@ -401,86 +401,108 @@ __global__ void __launch_bounds__(kBlock, 2) lora_prepare_kernel(const __grid_co
     if (blockIdx.x == gridDim.x - 1) ptx::grid_dependency_wait();
 }
 
-// y[t][n] = 2^rowexp[t] * (sum of the stream-K partials, as skinny_reduce_kernel) + sum_j t[t][j] B[a][n][j] with
-// t = s sum_z tp[z], all in fp32 from the bf16 adapter, rounded once.  One CTA per (128-column tile, 2 tokens); a
-// thread's first kEager chunks of B are loaded before the wait for the partials.
+// The weight-streaming path's last kernel: y[t][n] = 2^rowexp[t] * (sum of the stream-K partials, as
+// skinny_reduce_kernel) + sum_j t[t][j] B[a][n][j] with t = s sum_z tp[z], all in fp32 from the bf16 adapter, rounded
+// once.  kPair: g and u of a gate/up pair that way, from the two tiles of the column, and h = silu(g) u.  One CTA per
+// (128-column tile, 2 tokens); a thread's first kEager chunks of B are loaded before the wait for the partials.
 struct ExpandParams {
-    const __nv_bfloat16* b;      // [L][N][r]
+    const __nv_bfloat16* b[2];   // [L][N][r] of each member
     const float* scale;          // [L] or null (1)
-    const float* tp;             // [slices][M][r]
+    const float* tp;             // [slices][pairs][M][r]
     const int* ids;              // [M]
     int r, L, slices;
 };
 
-template <bool kBf16Out>
+template <bool kBf16Out, bool kPair>
 __global__ void __launch_bounds__(256) lora_reduce_kernel(const float* __restrict__ partial,
                                                           const int* __restrict__ rowexp, void* __restrict__ y, int M,
                                                           int N, int cpt, int64_t units, int P, int segmax,
                                                           int64_t partial_elems, const ExpandParams ep) {
-    __shared__ int64_t seg_base[skinny::kMaxCtas];
-    __shared__ int count;
-    __shared__ float ps[2][128];
-    __shared__ __align__(16) float tl[2][kMaxRank];
-    constexpr int kEager = 4;
-    const int w = blockIdx.x;
-    const int t = blockIdx.y * 2 + (threadIdx.x >> 7), n = w * skinny::BW + (threadIdx.x & 127);
+    constexpr int kPairs = kPair ? 2 : 1;
+    constexpr int kEager = kPair ? 2 : 4;
+    __shared__ int64_t seg_base[kPairs][skinny::kMaxCtas];
+    __shared__ int count[kPairs];
+    __shared__ float ps[2][kPairs][128];
+    __shared__ __align__(16) float tl[2][kPairs][kMaxRank];
+    const int w = blockIdx.x;                                     // tile of the gate weight; the up's is w + gridDim.x
+    const int half = threadIdx.x >> 7, i128 = threadIdx.x & 127;
+    const int t = blockIdx.y * 2 + half, n = w * skinny::BW + i128;
     const bool live = t < M && n < N;
-    if (threadIdx.x == 0) count = skinny::list_segments(w, cpt, units, P, segmax, seg_base);
+    if (i128 == 0 && half < kPairs)
+        count[half] = skinny::list_segments(w + half * static_cast<int>(gridDim.x), cpt, units, P, segmax, seg_base[half]);
     const int a = t < M ? ep.ids[t] : -1;
     const bool with = a >= 0 && a < ep.L;                         // the first product records an id out of range
     const int chunks = with && live ? ep.r / 8 : 0;
-    const uint4* b = reinterpret_cast<const uint4*>(ep.b + (static_cast<int64_t>(with ? a : 0) * N + (live ? n : 0)) * ep.r);
-    uint4 eager[kEager];
+    const int64_t row = (static_cast<int64_t>(with ? a : 0) * N + (live ? n : 0)) * ep.r;
+    uint4 eager[kPairs][kEager];
 #pragma unroll
-    for (int i = 0; i < kEager; ++i) eager[i] = i < chunks ? __ldg(b + i) : make_uint4(0u, 0u, 0u, 0u);
+    for (int q = 0; q < kPairs; ++q)
+#pragma unroll
+        for (int i = 0; i < kEager; ++i)
+            eager[q][i] = i < chunks ? __ldg(reinterpret_cast<const uint4*>(ep.b[q] + row) + i) : make_uint4(0u, 0u, 0u, 0u);
     const float sc = with && ep.scale != nullptr ? __ldg(ep.scale + a) : 1.0f;
     __syncthreads();
     ptx::grid_dependency_wait();                                  // partials and tp come from the kernel before
     // t of the CTA's two tokens: a token's 128 threads share out the slices, then add their sums in order
-    const int half = threadIdx.x >> 7, i128 = threadIdx.x & 127;
     const int groups = 128 / ep.r, j = i128 % ep.r, group = i128 / ep.r;
     if (with && group < groups) {
-        const float* tp = ep.tp + static_cast<int64_t>(t) * ep.r + j;
-        const int64_t step = static_cast<int64_t>(M) * ep.r;
-        float sum = 0.0f;
+        const int64_t step = static_cast<int64_t>(kPairs) * M * ep.r;
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) {
+            const float* tp = ep.tp + (static_cast<int64_t>(q) * M + t) * ep.r + j;
+            float sum = 0.0f;
 #pragma unroll 8
-        for (int z = group; z < ep.slices; z += groups) sum += tp[z * step];
-        ps[half][i128] = sum;
+            for (int z = group; z < ep.slices; z += groups) sum += tp[z * step];
+            ps[half][q][i128] = sum;
+        }
     }
-    float acc = live ? skinny::sum_segments(partial, partial_elems, seg_base, count, M, t, i128) : 0.0f;
+    float acc[kPairs];
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q)
+        acc[q] = live ? skinny::sum_segments(partial, partial_elems, seg_base[q], count[q], M, t, i128) : 0.0f;
     __syncthreads();
     if (with && i128 < ep.r) {
-        float sum = ps[half][i128];
-        for (int q = 1; q < groups; ++q) sum += ps[half][i128 + q * ep.r];
-        tl[half][i128] = sc * sum;
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) {
+            float sum = ps[half][q][i128];
+            for (int z = 1; z < groups; ++z) sum += ps[half][q][i128 + z * ep.r];
+            tl[half][q][i128] = sc * sum;
+        }
     }
     __syncthreads();
     if (!live) return;
-    acc = ldexpf(acc, rowexp[t]);
-    const float4* tt = reinterpret_cast<const float4*>(tl[half]);
-    float delta = 0.0f;
-    auto add = [&](const uint4 v, int i) {
-        const float4 t0 = tt[2 * i], t1 = tt[2 * i + 1];
-        const uint32_t q[4] = {finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w)};
-        delta = fmaf(t0.x, bf16_lo(q[0]), delta);
-        delta = fmaf(t0.y, bf16_hi(q[0]), delta);
-        delta = fmaf(t0.z, bf16_lo(q[1]), delta);
-        delta = fmaf(t0.w, bf16_hi(q[1]), delta);
-        delta = fmaf(t1.x, bf16_lo(q[2]), delta);
-        delta = fmaf(t1.y, bf16_hi(q[2]), delta);
-        delta = fmaf(t1.z, bf16_lo(q[3]), delta);
-        delta = fmaf(t1.w, bf16_hi(q[3]), delta);
-    };
+    const int ex = rowexp[t];
 #pragma unroll
-    for (int i = 0; i < kEager; ++i)
-        if (i < chunks) add(eager[i], i);
-    for (int i = kEager; i < chunks; ++i) add(__ldg(b + i), i);
-    acc += delta;
+    for (int q = 0; q < kPairs; ++q) {
+        const float4* tt = reinterpret_cast<const float4*>(tl[half][q]);
+        const uint4* b = reinterpret_cast<const uint4*>(ep.b[q] + row);
+        float delta = 0.0f;
+        auto add = [&](const uint4 v, int i) {
+            const float4 t0 = tt[2 * i], t1 = tt[2 * i + 1];
+            const uint32_t e[4] = {finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w)};
+            delta = fmaf(t0.x, bf16_lo(e[0]), delta);
+            delta = fmaf(t0.y, bf16_hi(e[0]), delta);
+            delta = fmaf(t0.z, bf16_lo(e[1]), delta);
+            delta = fmaf(t0.w, bf16_hi(e[1]), delta);
+            delta = fmaf(t1.x, bf16_lo(e[2]), delta);
+            delta = fmaf(t1.y, bf16_hi(e[2]), delta);
+            delta = fmaf(t1.z, bf16_lo(e[3]), delta);
+            delta = fmaf(t1.w, bf16_hi(e[3]), delta);
+        };
+#pragma unroll
+        for (int i = 0; i < kEager; ++i)
+            if (i < chunks) add(eager[q][i], i);
+        for (int i = kEager; i < chunks; ++i) add(__ldg(b + i), i);
+        acc[q] = ldexpf(acc[q], ex) + delta;
+    }
+    float out = acc[0];
+    // as the fused kernel's SwiGLU epilogue
+    if constexpr (kPair) out = __fdividef(acc[0], 1.0f + __expf(-acc[0])) * acc[1];
     const int64_t e = static_cast<int64_t>(t) * N + n;
     if constexpr (kBf16Out) {
-        reinterpret_cast<__nv_bfloat16*>(y)[e] = __float2bfloat16_rn(acc);
+        reinterpret_cast<__nv_bfloat16*>(y)[e] = __float2bfloat16_rn(out);
     } else {
-        reinterpret_cast<float*>(y)[e] = acc;
+        reinterpret_cast<float*>(y)[e] = out;
     }
 }
 

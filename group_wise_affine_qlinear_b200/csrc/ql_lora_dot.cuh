@@ -35,14 +35,15 @@ __device__ __forceinline__ int adapter_of(const int* ids, int m, int L) {
     return -1;
 }
 
-// The weight-streaming path's first product (M <= 64), as tasks of one warp each: (row tile, n-th distinct adapter of
-// the tile, 16 ranks, K slice).  The slices' partial sums are added in order by the kernel that uses them.
+// The weight-streaming path's first product (M <= 64), as tasks of one warp each: (member of a gate/up pair, row tile,
+// n-th distinct adapter of the tile, 16 ranks, K slice).  The slices' partial sums are added in order by the kernel that
+// uses them.
 struct DotTasks {
     const __nv_bfloat16* x;      // [M][K]
-    const __nv_bfloat16* a;      // [L][r][K]
+    const __nv_bfloat16* a[2];   // [L][r][K] of each member
     const int* ids;              // [M]
-    float* tp;                   // [slices][M][r]
-    int M, K, r, L;
+    float* tp;                   // [slices][pairs][M][r]
+    int M, K, r, L, pairs;
     int per_tile;                // tasks are laid out for this many distinct adapters in a tile
     int chunks;                  // ceil(r / 16)
     int slices;
@@ -52,12 +53,14 @@ __device__ __forceinline__ void run_dot_tasks(const DotTasks& p, int worker, int
     const int lane = static_cast<int>(threadIdx.x & 31), g = lane >> 2, c = lane & 3;
     const int tiles = (p.M + kTile - 1) / kTile;
     const int kb_all = p.K / 32;
-    for (int task = worker; task < tiles * p.per_tile * p.chunks * p.slices; task += workers) {
+    for (int task = worker; task < p.pairs * tiles * p.per_tile * p.chunks * p.slices; task += workers) {
         const int z = task % p.slices;
         int rest = task / p.slices;
         const int j0 = (rest % p.chunks) * 16;
         rest /= p.chunks;
-        const int nth = rest % p.per_tile, m0 = (rest / p.per_tile) * kTile;
+        const int nth = rest % p.per_tile;
+        rest /= p.per_tile;
+        const int m0 = (rest % tiles) * kTile, pair = rest / tiles;
         const int mine = lane < kTile && m0 + lane < p.M ? adapter_of(p.ids, m0 + lane, p.L) : -1;
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, mine);
         uint32_t leaders = __ballot_sync(0xFFFFFFFFu, mine >= 0 && (__ffs(same) - 1) == lane);
@@ -71,7 +74,7 @@ __device__ __forceinline__ void run_dot_tasks(const DotTasks& p, int worker, int
         const uint4* x0 = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(min(m0 + g, p.M - 1)) * p.K) + c;
         const uint4* x1 = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(min(m0 + g + 8, p.M - 1)) * p.K) + c;
         const bool second = j0 + 8 < p.r;
-        const uint4* a0 = reinterpret_cast<const uint4*>(p.a + (static_cast<int64_t>(adapter) * p.r + j0 + g) * p.K) + c;
+        const uint4* a0 = reinterpret_cast<const uint4*>((pair == 0 ? p.a[0] : p.a[1]) + (static_cast<int64_t>(adapter) * p.r + j0 + g) * p.K) + c;
         const uint4* a1 = second ? a0 + static_cast<int64_t>(p.K) : a0;          // 8 rows of K bf16 further
         float d0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         constexpr int U = 3;                       // column blocks in flight
@@ -95,7 +98,7 @@ __device__ __forceinline__ void run_dot_tasks(const DotTasks& p, int worker, int
             dot_block(d0, vx0, vx1, __ldg(a0 + 4 * kb));
             dot_block(d1, vx0, vx1, __ldg(a1 + 4 * kb));
         }
-        float* out = p.tp + (static_cast<int64_t>(z) * p.M + m0) * p.r + j0 + 2 * c;
+        float* out = p.tp + ((static_cast<int64_t>(z) * p.pairs + pair) * p.M + m0) * p.r + j0 + 2 * c;
         if (id0 == adapter) {
             *reinterpret_cast<float2*>(out + g * p.r) = make_float2(d0[0], d0[1]);
             if (second) *reinterpret_cast<float2*>(out + g * p.r + 8) = make_float2(d1[0], d1[1]);

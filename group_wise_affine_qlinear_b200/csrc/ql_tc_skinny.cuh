@@ -51,6 +51,8 @@
 // the adapters' first product meanwhile (run_dot_tasks), beside the stream of codes and off its critical path; the
 // adapters' reduce kernel adds the second product.  As a kernel of its own in front of the prepass the first product
 // cost 8 us at M = 1 and 24 us with 8 rows of 53248 columns.
+// Pair mode (kPair, a SwiGLU pair with adapters): the up weight's tiles follow the gate weight's in one run of chunks, so
+// both stream in one launch; the pair's reduce kernel brings a tile's two halves together.
 #pragma once
 
 #include "ql_ptx.cuh"
@@ -122,8 +124,15 @@ struct Params {
 struct LoraParams : Params {
     lora::DotTasks dot;
 };
-template <bool kLora> struct PickParams { using type = Params; };
-template <> struct PickParams<true> { using type = LoraParams; };
+// Pair mode: the up weight; num_w counts the tiles of both, N the rows of one.
+struct PairParams : LoraParams {
+    CUtensorMap map_codes2, map_scales2, map_biases2;
+    const __half* scales2;   // [N][G]
+    const __half* biases2;   // [N][G]
+};
+template <bool kLora, bool kPair> struct PickParams { using type = Params; };
+template <> struct PickParams<true, false> { using type = LoraParams; };
+template <> struct PickParams<true, true> { using type = PairParams; };
 
 // First unit of CTA c's run (runs are [first(c), first(c+1))).
 __host__ __device__ __forceinline__ int64_t run_first(int64_t units, int P, int c) {
@@ -212,12 +221,12 @@ __global__ void __cluster_dims__(kPrepCluster, 1, 1) __launch_bounds__(kPrepThre
         xo[c] = prescale8<kBits>(xr[c], ex);
 }
 
-template <int NT, int B, bool kLora = false>
+template <int NT, int B, bool kLora = false, bool kPair = false>
 __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_constant__ CUtensorMap map_codes,
                                                             const __grid_constant__ CUtensorMap map_x,
                                                             const __grid_constant__ CUtensorMap map_scales,
                                                             const __grid_constant__ CUtensorMap map_biases,
-                                                            const typename PickParams<kLora>::type p) {
+                                                            const __grid_constant__ typename PickParams<kLora, kPair>::type p) {
     using L = Layout<NT, B>;
     constexpr int NC = L::NC;
     constexpr int NXC = L::NXC;
@@ -314,15 +323,23 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
                 if (!ptx::mbar_wait(&c_empty[s], ((ci / NC) & 1u) ^ 1u, abort_flag)) break;
                 uint8_t* st = smem + L::kOffC + s * kStageBytes;
                 ptx::mbar_arrive_expect_tx(&c_full[s], kCBytes + (p.param_tma ? 2 * kParHalf : 0u));
+                const CUtensorMap *mc = &map_codes, *ms = &map_scales, *mb = &map_biases;
+                if constexpr (kPair) {
+                    if (w >= p.num_w / 2) {
+                        w -= p.num_w / 2;
+                        mc = &p.map_codes2;
+                        ms = &p.map_scales2;
+                        mb = &p.map_biases2;
+                    }
+                }
 #pragma unroll
                 for (int bx = 0; bx < CG / kBoxGroups; ++bx)   // consecutive boxes: long contiguous row segments
-                    ptx::tma_load_2d(st + bx * kBoxBytes, &map_codes, &c_full[s], (g0 + bx * kBoxGroups) * L::kGroupWords,
-                                     w * BW);
+                    ptx::tma_load_2d(st + bx * kBoxBytes, mc, &c_full[s], (g0 + bx * kBoxGroups) * L::kGroupWords, w * BW);
                 if (p.param_tma) {
                     // the 8-group box holding the chunk (a chunk of 4 groups uses half of it)
                     const int gp = g0 - g0 % kParGroups;
-                    ptx::tma_load_2d(st + kCBytes, &map_scales, &c_full[s], gp, w * BW);
-                    ptx::tma_load_2d(st + kCBytes + kParHalf, &map_biases, &c_full[s], gp, w * BW);
+                    ptx::tma_load_2d(st + kCBytes, ms, &c_full[s], gp, w * BW);
+                    ptx::tma_load_2d(st + kCBytes + kParHalf, mb, &c_full[s], gp, w * BW);
                 }
             }
             // never leave the CTA with bulk copies still landing in its shared memory
@@ -450,19 +467,27 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
                             cw[kPieces * h + e] = *reinterpret_cast<const uint4*>(crow + (((c + e) ^ (r & 7)) << 4));
                     }
                 }
-                const int n = w * BW + r;
                 if (p.param_tma) {
                     const int pc0 = g0 % kParGroups + 2 * j;        // the pair's first column in the parameter box
                     sp = *reinterpret_cast<const uint32_t*>(st + kCBytes + r * kParGroups * 2 + 2 * pc0);
                     bp = *reinterpret_cast<const uint32_t*>(st + kCBytes + kParHalf + r * kParGroups * 2 + 2 * pc0);
                 } else {
+                    const __half *scales = p.scales, *biases = p.biases;
+                    int n = w * BW + r;
+                    if constexpr (kPair) {
+                        if (w >= p.num_w / 2) {
+                            n -= p.num_w / 2 * BW;
+                            scales = p.scales2;
+                            biases = p.biases2;
+                        }
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int q = 2 * j + h;
                         const int64_t at = static_cast<int64_t>(n) * p.G + g0 + q;
                         if (n < p.N && q < ng && in_bounds(at, static_cast<int64_t>(p.N) * p.G)) {
-                            sp |= static_cast<uint32_t>(__half_as_ushort(__ldg(p.scales + at))) << (16 * h);
-                            bp |= static_cast<uint32_t>(__half_as_ushort(__ldg(p.biases + at))) << (16 * h);
+                            sp |= static_cast<uint32_t>(__half_as_ushort(__ldg(scales + at))) << (16 * h);
+                            bp |= static_cast<uint32_t>(__half_as_ushort(__ldg(biases + at))) << (16 * h);
                         }
                     }
                 }

@@ -321,7 +321,8 @@ def _pair_call(x, gate, up, ad, ids, scale, **kw):
 @pytest.mark.parametrize("M,K,I,n,r,how", [
     (1, 64, 8, 1, 8, "one"), (24, 1024, 264, 6, 16, "mixed"), (191, 320, 136, 3, 24, "runs"),
     (193, 512, 264, 40, 8, "distinct"), (400, 1024, 520, 5, 64, "mixed"), (300, 256, 136, 2, 128, "runs"),
-    (33, 4608, 264, 12, 32, "distinct"),
+    (33, 4608, 264, 12, 32, "distinct"), (20, 320, 136, 3, 24, "mixed"), (64, 2048, 520, 9, 40, "runs"),
+    (64, 576, 8, 64, 128, "distinct"),
 ])
 def test_swiglu_lora(M, K, I, n, r, how):
     rng = np.random.default_rng(M + K + I + r)
@@ -352,6 +353,38 @@ def test_swiglu_lora_without_adapters_is_the_plain_pair():
         mixed = _pair_call(x, gate, up, ad, ids, scale, out_dtype=torch.float32)
         bare = torch.from_numpy(ids < 0).cuda()
         assert torch.equal(mixed[bare], none[bare])
+
+
+@pytest.mark.parametrize("M,K,I", [(3, 4608, 264), (48, 320, 136), (260, 1024, 264)])
+def test_swiglu_lora_repeats_and_replays(M, K, I):
+    rng = np.random.default_rng(M + K)
+    x, gate, up, ad, scale = _pair(rng, M, K, I, 4, 16)
+    ids = _ids(rng, M, 4, "mixed")
+    d = [to_dev_bf16(v) for v in ad]
+    args = (to_dev_bf16(x), _dev_w(gate), _dev_w(up), (d[0], d[1]), (d[2], d[3]), _dev_ids(ids),
+            torch.from_numpy(scale).cuda())
+    ref = ql.swiglu_lora(*args)
+    ws = torch.empty(ql.swiglu_lora_workspace_size(M, K, I, 4, 16), dtype=torch.uint8, device="cuda")
+    for fill in (0xFF, 0x00):
+        ws.fill_(fill)
+        assert torch.equal(ql.swiglu_lora(*args, workspace=ws), ref)
+    out = torch.empty_like(ref)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ql.swiglu_lora(*args, out=out, workspace=ws)
+    for _ in range(2):
+        out.fill_(float("nan"))
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    # a non-finite entry of either up projection counts as zero and is recorded
+    bad = d[3].clone()
+    bad[1, 5, 3] = float("inf")
+    ql.swiglu_lora(*args[:4], (d[2], bad), *args[5:])
+    assert ql.device_status() == (1 if (ids == 1).any() else 0)
+    del g
 
 
 def test_swiglu_lora_keeps_gate_and_up_apart():

@@ -104,7 +104,7 @@ __device__ __forceinline__ void plan_tile(const ShrinkParams& p, int t_blk) {
         if (i >= rows) continue;
         const int n = place(first[h]);
         p.row_slot[t_blk * BT + i] = id[i] >= 0 ? n : -1;
-        if (id[i] >= 0 && first[h] == i) p.tile_list[t_blk * BT + n] = id[i];
+        if (id[i] >= 0 && first[h] == i && in_bounds(n, BT)) p.tile_list[t_blk * BT + n] = id[i];
     }
     if (threadIdx.x == 0) {
         int n = 0;
@@ -307,9 +307,10 @@ __device__ __forceinline__ void shrink_tile(const CUtensorMap& map_x, const CUte
                 }
             }
             const float f = factor * __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));     // s 2^-e_m
-            __nv_bfloat16* o = p.tw + (static_cast<int64_t>(m0 + row) * p.pairs + pair) * 2 * p.r + 16 * (j / 8) + j % 8;
-            *reinterpret_cast<uint32_t*>(o) = fused::bf16_part(s0 * f, s1 * f, false);
-            *reinterpret_cast<uint32_t*>(o + 8) = fused::bf16_part(s0 * f, s1 * f, true);
+            const int64_t at = (static_cast<int64_t>(m0 + row) * p.pairs + pair) * 2 * p.r + 16 * (j / 8) + j % 8;
+            if (!in_bounds(at, static_cast<int64_t>(p.M) * p.pairs * 2 * p.r - 9)) continue;
+            *reinterpret_cast<uint32_t*>(p.tw + at) = fused::bf16_part(s0 * f, s1 * f, false);
+            *reinterpret_cast<uint32_t*>(p.tw + at + 8) = fused::bf16_part(s0 * f, s1 * f, true);
         }
         first = false;
         for (int n = 0; n < p.passes; ++n) leaders &= leaders - 1;

@@ -98,7 +98,9 @@ __device__ __forceinline__ void run_dot_tasks(const DotTasks& p, int worker, int
             dot_block(d0, vx0, vx1, __ldg(a0 + 4 * kb));
             dot_block(d1, vx0, vx1, __ldg(a1 + 4 * kb));
         }
-        float* out = p.tp + ((static_cast<int64_t>(z) * p.pairs + pair) * p.M + m0) * p.r + j0 + 2 * c;
+        const int64_t at = ((static_cast<int64_t>(z) * p.pairs + pair) * p.M + m0) * p.r + j0 + 2 * c;
+        if (!in_bounds(at, static_cast<int64_t>(p.slices) * p.pairs * p.M * p.r)) continue;
+        float* out = p.tp + at;
         if (id0 == adapter) {
             *reinterpret_cast<float2*>(out + g * p.r) = make_float2(d0[0], d0[1]);
             if (second) *reinterpret_cast<float2*>(out + g * p.r + 8) = make_float2(d1[0], d1[1]);

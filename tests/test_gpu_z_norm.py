@@ -222,16 +222,18 @@ def test_streams_repeats_and_graphs():
             assert torch.equal(out, r) and torch.equal(ho, h)
 
 
-def test_row_offsets_beyond_32_bits():
-    """More than 2^31 elements: the last rows' offsets do not fit 32 bits."""
-    D = 32768
+@pytest.mark.parametrize("D", [64, 8192, 32768])
+def test_row_offsets_beyond_32_bits(D):
+    """More than 2^31 elements: the last rows' offsets do not fit 32 bits (short rows, the ring, a CTA per row)."""
     M = 2 ** 31 // D + 3
     x = torch.zeros((M, D), dtype=torch.bfloat16, device="cuda")
     rng = np.random.default_rng(9)
     tail = torch.from_numpy(rng.standard_normal((3, D)).astype(np.float32)).cuda().bfloat16()
     x[-3:] = tail
     h = ql.norm_residual(x)[1]
-    assert torch.equal(h[-3:], ql.norm_residual(tail)[1])
+    alone = ql.norm_residual(tail)[1]
+    # the tail alone may take another form, whose sums run in another order
+    assert torch.allclose(h[-3:].float(), alone.float(), rtol=2 * B, atol=0)
     assert (h[:8] == 0).all()
 
 

@@ -717,6 +717,13 @@ lora::ExpandParams expand_params(const LoraArgs& la, const LoraPlan& lp, uint8_t
     return e;
 }
 
+// Grid of the adapters' reduce kernel: a pair of tokens per CTA while four CTAs per SM hold them all, then several.
+dim3 reduce_grid(int tiles, int64_t M, int sm_count) {
+    const int64_t pairs = (M + 1) / 2;
+    const int64_t rounds = std::max<int64_t>(1, (tiles * pairs + 4 * sm_count - 1) / (4 * sm_count));
+    return dim3(static_cast<unsigned>(tiles), static_cast<unsigned>((pairs + rounds - 1) / rounds));
+}
+
 // Launches the weight-streaming kernel, with or without adapters.
 template <int NT, int B>
 ql_status launch_skinny(dim3 grid, cudaStream_t st, const CUtensorMap& mc, const CUtensorMap& mx, const CUtensorMap& ms,
@@ -807,8 +814,8 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
     const dim3 red_grid(static_cast<unsigned>(p.num_w), static_cast<unsigned>((M + 1) / 2));
     if (la) {
         auto red = bf16_out ? lora::lora_reduce_kernel<true, false> : lora::lora_reduce_kernel<false, false>;
-        s = launch_dependent(red, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt, p.units, pl.ctas, pl.segmax,
-                             p.partial_elems, expand_params(*la, *lp, wsb));
+        s = launch_dependent(red, reduce_grid(p.num_w, M, sm_count), 256, 0, st, part, rexp, y, p.M, p.N, p.cpt, p.units,
+                             pl.ctas, pl.segmax, p.partial_elems, expand_params(*la, *lp, wsb));
     } else if (bf16_out)
         s = launch_dependent(skinny::skinny_reduce_kernel<true>, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt,
                              p.units, pl.ctas, pl.segmax, p.partial_elems);
@@ -816,7 +823,6 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
         s = launch_dependent(skinny::skinny_reduce_kernel<false>, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt,
                              p.units, pl.ctas, pl.segmax, p.partial_elems);
     if (s != QL_OK) return s;
-    (void)sm_count;
     set_dispatch("path=tc_skinny%s bits=%d nt=%d ctas=%d segmax=%d units=%lld launches=3 why=%s", la ? "_lora" : "", bits,
                  pl.nt, pl.ctas, pl.segmax, static_cast<long long>(pl.units), pl.why);
     return launch_status();
@@ -910,7 +916,7 @@ ql_status run_swiglu(const SwigluPlan& pl, const void* x, const uint32_t* gc, co
 // 16: 36 us a call against 62 on the fused path, whose tiles cost the same for 192 tokens.
 ql_status run_swiglu_streaming(const Plan& pl, const LoraPlan& lp, const LoraArgs& la, const void* x, const uint32_t* gc,
                                const void* gs, const void* gb, const uint32_t* uc, const void* us, const void* ub, void* h,
-                               bool bf16_out, int64_t M, int64_t K, int64_t I, void* ws, cudaStream_t st) {
+                               bool bf16_out, int64_t M, int64_t K, int64_t I, void* ws, cudaStream_t st, int sm_count) {
     const int64_t G = K / kGroup;
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     void* xp = wsb + pl.off_xp;
@@ -957,7 +963,7 @@ ql_status run_swiglu_streaming(const Plan& pl, const LoraPlan& lp, const LoraArg
     prof_end(st);
     const float* part = p.partial;
     const int* rexp = rowexp;
-    const dim3 red_grid(static_cast<unsigned>(tiles), static_cast<unsigned>((M + 1) / 2));
+    const dim3 red_grid = reduce_grid(tiles, M, sm_count);
     auto red = bf16_out ? lora::lora_reduce_kernel<true, true> : lora::lora_reduce_kernel<false, true>;
     s = launch_dependent(red, red_grid, 256, 0, st, part, rexp, h, p.M, p.N, p.cpt, p.units, pl.ctas, pl.segmax,
                          p.partial_elems, expand_params(la, lp, wsb));
@@ -1043,7 +1049,7 @@ ql_status swiglu_impl(const void* x, const uint32_t* gc, const void* gs, const v
     if ((s = device_info(&dev)) != QL_OK) return s;
     if (la && sp.path == QL_PATH_TC_SKINNY)
         return run_swiglu_streaming(sp, lp, *la, x, gc, gs, gb, uc, us, ub, h, out_dtype == QL_BF16, M, K, I, workspace,
-                                    stream);
+                                    stream, dev->sm_count);
     return run_swiglu(pl, x, gc, gs, gb, uc, us, ub, h, out_dtype == QL_BF16, M, K, I, workspace, stream,
                       dev->sm_count, la, &lp);
 }

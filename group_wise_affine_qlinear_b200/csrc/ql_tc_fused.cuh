@@ -463,6 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                     __syncwarp();
                 }
                 if (!ok) break;
+                int copied = -1;                               // the stage whose copies are not announced yet
+                const auto announce = [&] {
+                    ptx::fence_proxy_async_smem();             // visible to the MMAs' reads of shared memory
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&x_full[copied]);
+                };
                 for (; p0 < p1; p0 += 4, ++i) {
                     int s;
                     uint32_t ph;
@@ -485,16 +491,26 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                             const int q = 8 * e + 4 * h + (lane >> 3);
                             const int slot = __shfl_sync(0xFFFFFFFFu, o, q & 31);
                             const int rel = 2 * p0 + c - slot * width;
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (slot >= 0 && static_cast<uint32_t>(rel) < static_cast<uint32_t>(width))
-                                v = __ldg(reinterpret_cast<const uint4*>(p.tw) +
-                                          (static_cast<int64_t>(t_blk) * BT + q) * width + rel);
-                            *reinterpret_cast<uint4*>(stage + q * 128 + ((c ^ (q & 7)) << 4)) = v;
+                            const bool in = slot >= 0 && static_cast<uint32_t>(rel) < static_cast<uint32_t>(width);
+                            ptx::copy16_async(stage + q * 128 + ((c ^ (q & 7)) << 4),
+                                              reinterpret_cast<const uint4*>(p.tw) +
+                                                  (in ? (static_cast<int64_t>(t_blk) * BT + q) * width + rel : 0), in);
                         }
                     }
-                    ptx::fence_proxy_async_smem();             // visible to the MMAs' reads of shared memory
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&x_full[s]);
+                    if (mixed == 0) {
+                        if (lane == 0) ptx::mbar_arrive(&x_full[s]);
+                        continue;
+                    }
+                    ptx::copy_async_commit();
+                    if (copied >= 0) {
+                        ptx::copy_async_wait<1>();
+                        announce();
+                    }
+                    copied = s;
+                }
+                if (copied >= 0) {
+                    ptx::copy_async_wait<0>();
+                    announce();
                 }
             }
             if (lane == 0) {

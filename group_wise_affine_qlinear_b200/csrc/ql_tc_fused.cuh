@@ -423,7 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
         // whose tw is zero) are a box of tw shifted by that place, and the TMA's fill past either end of tw's row gives
         // the zeros; 24 lanes issue a box each.  Eights with several adapters (where two requests meet, or tokens in
         // no order) are copied by the warp, in the layout the TMA writes: 128-byte rows, 16-byte pieces permuted by
-        // the row's number mod 8.
+        // the row's number mod 8.  All of a step's copies are on their way at once, and a step is announced when the
+        // next one's are (290 rows of 38 requests, rank 64, a 128 -> 224 pair: 43 us, by loads and stores 102; by the
+        // epilogue warps while they wait for the tile 32, but a layer with long prompts took 3 % longer).
         if constexpr (kLora) {
             constexpr int kEights = BT / 8;
             uint32_t i = 0;
@@ -463,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                     __syncwarp();
                 }
                 if (!ok) break;
+                const uint4* tw = reinterpret_cast<const uint4*>(p.tw) + static_cast<int64_t>(t_blk) * BT * width;
                 int copied = -1;                               // the stage whose copies are not announced yet
                 const auto announce = [&] {
                     ptx::fence_proxy_async_smem();             // visible to the MMAs' reads of shared memory
@@ -481,20 +484,19 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                         ptx::tma_load_2d(stage + 1024 * lane, &p.map_tw, &x_full[s], 16 * p0 - 8 * width * max(eight, 0),
                                          t_blk * BT + 8 * lane);
                     const int c = lane & 7;
-                    for (uint32_t left = mixed; left != 0; left &= left - 1) {
-                        const int e = __ffs(left) - 1;
-                        int o = own[0];
 #pragma unroll
-                        for (int j = 1; j < BT / 32; ++j) o = (e >> 2) == j ? own[j] : o;
+                    for (int j = 0; j < BT / 32; ++j) {
+                        for (uint32_t left = (mixed >> (4 * j)) & 15u; left != 0; left &= left - 1) {
+                            const int e = __ffs(left) - 1;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {          // four rows at a time, eight lanes each
-                            const int q = 8 * e + 4 * h + (lane >> 3);
-                            const int slot = __shfl_sync(0xFFFFFFFFu, o, q & 31);
-                            const int rel = 2 * p0 + c - slot * width;
-                            const bool in = slot >= 0 && static_cast<uint32_t>(rel) < static_cast<uint32_t>(width);
-                            ptx::copy16_async(stage + q * 128 + ((c ^ (q & 7)) << 4),
-                                              reinterpret_cast<const uint4*>(p.tw) +
-                                                  (in ? (static_cast<int64_t>(t_blk) * BT + q) * width + rel : 0), in);
+                            for (int h = 0; h < 2; ++h) {      // four rows at a time, eight lanes each
+                                const int q = 8 * e + 4 * h + (lane >> 3);
+                                const int slot = __shfl_sync(0xFFFFFFFFu, own[j], q);
+                                const int rel = 2 * p0 + c - slot * width;
+                                const bool in = slot >= 0 && static_cast<uint32_t>(rel) < static_cast<uint32_t>(width);
+                                ptx::copy16_async(stage + (32 * j + q) * 128 + ((c ^ (q & 7)) << 4),
+                                                  tw + (in ? (32 * j + q) * width + rel : 0), in);
+                            }
                         }
                     }
                     if (mixed == 0) {

@@ -306,11 +306,13 @@ __device__ __forceinline__ void shrink_tile(const CUtensorMap& map_x, const CUte
                     s1 += v1[q];
                 }
             }
-            const float f = factor * __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));     // s 2^-e_m
+            // the factor first: s 2^-e_m alone can leave fp32's range where t and t 2^-e_m do not
+            const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale_s[row]));
+            const float t0 = s0 * factor * inv, t1 = s1 * factor * inv;
             const int64_t at = (static_cast<int64_t>(m0 + row) * p.pairs + pair) * 2 * p.r + 16 * (j / 8) + j % 8;
             if (!in_bounds(at, static_cast<int64_t>(p.M) * p.pairs * 2 * p.r - 9)) continue;
-            *reinterpret_cast<uint32_t*>(p.tw + at) = fused::bf16_part(s0 * f, s1 * f, false);
-            *reinterpret_cast<uint32_t*>(p.tw + at + 8) = fused::bf16_part(s0 * f, s1 * f, true);
+            *reinterpret_cast<uint32_t*>(p.tw + at) = fused::bf16_part(t0, t1, false);
+            *reinterpret_cast<uint32_t*>(p.tw + at + 8) = fused::bf16_part(t0, t1, true);
         }
         first = false;
         for (int n = 0; n < p.passes; ++n) leaders &= leaders - 1;
@@ -407,8 +409,7 @@ __global__ void __launch_bounds__(kBlock, 2) lora_prepare_kernel(const __grid_co
 // once.  kPair: g and u of a gate/up pair that way, from the two tiles of the column, and h = silu(g) u.  A CTA takes a
 // 128-column tile and two tokens at a time, the tokens y, y + gridDim.y, ... of the pairs of tokens: listing the tile's
 // partials once for many tokens, in one wave of CTAs (24 tokens x 12288 pairs: 10 us behind the stream, of which the CTAs'
-// start takes 4; one token's 13824 columns 2.7 us).  The first tokens' B is loaded
-// before the wait for the partials.
+// start takes 4; one token's 13824 columns 2.7 us).  The first tokens' B is loaded before the wait for the partials.
 struct ExpandParams {
     const __nv_bfloat16* b[2];   // [L][N][r] of each member
     const float* scale;          // [L] or null (1)

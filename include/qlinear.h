@@ -348,6 +348,8 @@ QL_API ql_status qlinear_reduce_partials(const float* partials, int32_t S, int64
  * Non-finite activations and entries of lora_a reach the outputs of their own rows only.  A non-finite entry of
  * lora_b counts as zero and is recorded as QL_ERR_INVALID_ARG in the device status word: rows of several adapters
  * share a tensor-core tile, where it would reach the others' outputs.
+ * Above 64 rows t is held as two bf16 terms (2^-16 relative) of t over the row's power of two; an adapter that makes t
+ * more than 2^110 times its row's largest activation gives infinities there.
  *
  * Up to 64 rows the weights are streamed as in qlinear_forward and the adapters are added where the partial sums
  * meet; above, they are extra K-steps of the fused kernel, one 64-column step per 32 / r distinct adapters of each

@@ -168,6 +168,31 @@ def test_large_and_small_adapters(M):
     assert np.all(np.abs(y - ref) <= bound)
 
 
+@pytest.mark.parametrize("M", [20, 400])
+def test_factors_far_from_one_on_rows_far_from_one(M):
+    """A row near the bottom of bf16's range with a large factor, and one near its top with a small one: the product of
+    the factor and the row's own power of two would leave fp32's range, t itself and t over that power do not.  Bound as
+    in test_large_and_small_adapters."""
+    rng = np.random.default_rng(16)
+    K, N, n, r = 512, 136, 3, 16
+    codes = np.zeros((N, K // 8), np.uint32)
+    zero = np.zeros((N, K // 64), np.float16)
+    x = rng.standard_normal((M, K))
+    x[1::3] *= 2.0 ** -101
+    x[2::3] *= 2.0 ** 112
+    scale = np.array([1.0, 2.0 ** 20, 2.0 ** -50], np.float32)
+    ids = (np.arange(M) % n).astype(np.int32)
+    xb, ab, bb = _bits(x), _bits(rng.standard_normal((n, r, K))), _bits(rng.standard_normal((n, N, r)))
+    y = ql.forward_lora(to_dev_bf16(xb), to_dev_codes(codes), to_dev_f16(zero), to_dev_f16(zero), to_dev_bf16(ab),
+                        to_dev_bf16(bb), _dev_ids(ids), torch.from_numpy(scale).cuda(),
+                        out_dtype=torch.float32).double().cpu().numpy()
+    xv, av, bv = O.decode_bf16(xb), O.decode_bf16(ab), O.decode_bf16(bb)
+    ref = O.lora_delta(xb, ab, bb, scale, ids)
+    u = np.einsum("mk,mjk->mj", np.abs(xv), np.abs(av[ids])) * scale[ids].astype(np.float64)[:, None]
+    bound = np.einsum("mj,mnj->mn", u, np.abs(bv[ids])) * (2.0 ** -16 + (K + 2 * r) * 2.0 ** -23)
+    assert np.all(np.abs(y - ref) <= bound)
+
+
 @pytest.mark.parametrize("M", [24, 300])
 def test_non_finite_rows_and_adapters_stay_in_their_rows(M):
     rng = np.random.default_rng(7)

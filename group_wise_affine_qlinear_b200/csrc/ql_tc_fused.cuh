@@ -67,8 +67,8 @@
 // operand is t, scaled like the row's activations and cut into two bf16, t = hi + lo to 2^-16 relative (the MMA's
 // type is per instruction: these steps run in bf16, whose exponents cannot overflow where f16's could).  A "part" is 8
 // columns of B under 16 of t's, [hi 8 | lo 8]; a tile's distinct adapters lie side by side, r / 8 parts each (in
-// SwiGLU mode the gate's r / 8, then the up's, each zero under the other row group), four parts to a step; a token's
-// row is zero outside its own adapter's parts.  So a tile pays for the adapters in it (one step per 32 / r of them),
+// SwiGLU mode the gate's r / 8, then the up's, each multiplied for its own row group alone), four parts to a step; a
+// token's row is zero outside its own adapter's parts.  So a tile pays for the adapters in it (one step per 32 / r of them),
 // nothing travels through memory a second time, and y is rounded once.  B comes by TMA through the code ring (a code
 // stage per extra step), t by TMA too, eight rows at a time, but for the eights that meet several adapters.
 #pragma once
@@ -693,9 +693,18 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                         const uint32_t d = tmem_base + kAccCol + static_cast<uint32_t>(gsel * BT);
                         const uint32_t a_tm = tmem_base + kAStageCol + 64u * static_cast<uint32_t>(i % NA) + 32u * gsel;
                         const int nu = min(BK / UK, p1 - p0);               // one 16-column MMA per part
-                        for (int u = 0; u < nu; ++u)
-                            ptx::mma_f16_ts(d, a_tm + u * (UK / 2), ptx::sdesc_sw128(x_addr + u * UK * 2), idesc_lora, 1u);
-                        ptx::mma_commit(&x_empty[xs]);
+                        int seg = p0 / p.r8, part = p0 - seg * p.r8;
+                        for (int u = 0; u < nu; ++u) {
+                            // the gate's and the up's parts each for their own row group: a zero operand under
+                            // the other would turn an infinite t of one projection into a NaN of both
+                            if (!kSwiGLU || (seg & 1) == gsel)
+                                ptx::mma_f16_ts(d, a_tm + u * (UK / 2), ptx::sdesc_sw128(x_addr + u * UK * 2), idesc_lora, 1u);
+                            if (kSwiGLU && ++part == p.r8) {
+                                part = 0;
+                                ++seg;
+                            }
+                        }
+                        ptx::mma_commit(&x_empty[xs]);                      // (with no MMA of its own: of those before)
                     }
                 }
                 if (ok) ptx::mma_commit(&acc_full[0]);

@@ -45,12 +45,12 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // records QL_ERR_DEVICE_TIMEOUT and lets the kernel unwind.
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;   // 1 s
 
-// Kernels whose code producer the checked build can hold back (qlinear_test_stall).
-constexpr int kStallFused = 1, kStallSkinny = 2;
+// Kernels whose code producer (the norms' ring: whose row copies) the checked build can hold back (qlinear_test_stall).
+constexpr int kStallFused = 1, kStallSkinny = 2, kStallNorm = 4;
 
 #ifdef QL_BOUNDS_CHECK
 // Test hooks of the checked build (the index-checked variant): the host can shorten the wait limit and
-// hold back the code producer of the kernels in a mask, so that a real pipeline's waits expire with no
+// hold back the producer of the kernels in a mask, so that a real pipeline's waits expire with no
 // copy or MMA in flight and its unwinding can be tested.  The shipped build has neither: its limit is
 // the constant above and nothing is held back.
 static __device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;

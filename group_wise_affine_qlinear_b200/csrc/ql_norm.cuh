@@ -236,10 +236,11 @@ __device__ __forceinline__ void modulate(const Params& p, const F8& r, float inv
 
 // A row by a CTA, from the loaded x (in r) and v to its stores.  w: the vectors of the thread's pieces, or null to
 // fetch them piece by piece.  row_done() runs once every thread has its inputs in registers: after the first
-// reduction's barrier (a row without a reduction is the caller's to synchronize).
-template <bool kXF32, bool kHasY, int VPT, class RowDone>
+// reduction's barrier (a row without a reduction is the caller's to synchronize).  store(): whether to store, asked
+// where the values are ready.
+template <bool kXF32, bool kHasY, int VPT, class Store, class RowDone>
 __device__ __forceinline__ void finish_row(const Params& p, F8 (&r)[VPT], const F8 (&v)[VPT], int64_t row,
-                                           int seg, const Vectors* w, float (*red)[32], bool store, RowDone&& row_done) {
+                                           int seg, const Vectors* w, float (*red)[32], Store&& store, RowDone&& row_done) {
     const int nv = p.D / 8, tid = static_cast<int>(threadIdx.x), nthreads = static_cast<int>(blockDim.x);
     bool told = false;
     if constexpr (kHasY) {
@@ -249,26 +250,28 @@ __device__ __forceinline__ void finish_row(const Params& p, F8 (&r)[VPT], const 
             row_done();
             told = true;
         }
+        const bool keep = store();
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = tid + j * nthreads;
             if (c >= nv) continue;
             Vectors t;
             if (w == nullptr) load_vectors<true>(p, seg, c, t);
-            update<kXF32>(p, r[j], v[j], inv, w == nullptr ? t : w[j], row + 8 * c, store);
+            update<kXF32>(p, r[j], v[j], inv, w == nullptr ? t : w[j], row + 8 * c, keep);
         }
     }
     if (p.h != nullptr) {
         const float inv = inv_rms(p, row_sum(sum_squares<VPT>(r), red[1]));
         if (!told) row_done();
         told = true;
+        const bool keep = store();
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = tid + j * nthreads;
             if (c >= nv) continue;
             Vectors t;
             if (w == nullptr) load_vectors<false>(p, seg, c, t);
-            modulate(p, r[j], inv, w == nullptr ? t : w[j], row + 8 * c, store);
+            modulate(p, r[j], inv, w == nullptr ? t : w[j], row + 8 * c, keep);
         }
     }
     if (!told) row_done();
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(1024) norm_row_kernel(const Params p) {
         if constexpr (kY != kYNone) v[j] = unpack<kYF>(yr[j]);
         if constexpr (kYF) v[j] = add_partials(p, row + 8 * c, v[j]);
     }
-    finish_row<kXF32, kY != kYNone, VPT>(p, r, v, row, seg, VPT == 1 ? w : nullptr, red, true, [] {});
+    finish_row<kXF32, kY != kYNone, VPT>(p, r, v, row, seg, VPT == 1 ? w : nullptr, red, [] { return true; }, [] {});
 }
 
 // Persistent CTAs: CTA b takes the rows [b M / B, (b + 1) M / B) of a grid of B; row i of its list lies in ring stage
@@ -465,6 +468,7 @@ __global__ void __launch_bounds__(RingCfg<kCfg>::kThreads, RingCfg<kCfg>::kCtas)
     const auto issue = [&](int64_t m, int s, int seg) {
         if (m >= m_end) return;
         seg_s[s] = seg;
+        if (stalled(kStallNorm)) return;                   // the checked build can hold every copy back
         if (seg < 0 || seg >= p.T) {
             ptx::mbar_arrive(&full[s]);
             return;
@@ -476,17 +480,15 @@ __global__ void __launch_bounds__(RingCfg<kCfg>::kThreads, RingCfg<kCfg>::kCtas)
             ptx::bulk_load(dst + x_pad + z * y_pad, static_cast<const uint8_t*>(p.y) + (z * p.M + m) * yb, yb, &full[s]);
     };
     int64_t m = p.M * blockIdx.x / gridDim.x;
-    int64_t ahead = m;                                     // the next row to copy
-    int next_seg = 0;
+    int next_seg = 0;                                      // of row m + stages, the next to copy
     if (tid == 0) {
         int segs[kMaxStages];                              // all of them at once: their loads are the start's latency
 #pragma unroll
-        for (int i = 0; i < kMaxStages; ++i) segs[i] = segment(ahead + i);
+        for (int i = 0; i < kMaxStages; ++i) segs[i] = segment(m + i);
 #pragma unroll
         for (int i = 0; i < kMaxStages; ++i)
-            if (i < stages) issue(ahead + i, i, segs[i]);
-        ahead += stages;
-        next_seg = segment(ahead);
+            if (i < stages) issue(m + i, i, segs[i]);
+        next_seg = segment(m + stages);
     }
     Vectors w[kHold ? VPT : 1];
     int held = -1;
@@ -501,17 +503,17 @@ __global__ void __launch_bounds__(RingCfg<kCfg>::kThreads, RingCfg<kCfg>::kCtas)
         const int seg = segment(m);
         if (seg >= 0 && seg < p.T) hold(seg);
     }
-    bool ok = true;
+    // a wait of some thread has expired: no more stores or copies, the same barriers
+    const auto aborted = [&] { return *const_cast<volatile int*>(&abort_flag) != 0; };
     int s = 0;
     uint32_t phase = 0;
     for (; m < m_end; ++m) {
-        ok = ptx::mbar_wait(&full[s], phase, &abort_flag) && ok;       // on expiry: no more stores, same barriers
+        ptx::mbar_wait(&full[s], phase, &abort_flag);
         const int seg = seg_s[s];
         const auto refill = [&] {
-            if (tid == 0) {
-                issue(ahead, s, next_seg);
-                ++ahead;
-                next_seg = segment(ahead);
+            if (tid == 0 && !aborted()) {
+                issue(m + stages, s, next_seg);
+                next_seg = segment(m + stages + 1);
             }
         };
         if (seg < 0 || seg >= p.T) {                                   // the same in every thread
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(RingCfg<kCfg>::kThreads, RingCfg<kCfg>::kCtas)
             }
             const int reductions = (kY != kYNone && p.post_norm ? 1 : 0) + (p.h != nullptr ? 1 : 0);
             if (reductions == 0) __syncthreads();                      // no barrier would tell that the stage is read
-            finish_row<kXF32, kY != kYNone, VPT>(p, r, v, m * D, seg, kHold ? w : nullptr, red, ok, refill);
+            finish_row<kXF32, kY != kYNone, VPT>(p, r, v, m * D, seg, kHold ? w : nullptr, red, [&] { return !aborted(); }, refill);
             // with two reductions a row each one's buffer is read before the other's barrier; with one, the next row
             // must not overtake its readers
             if (reductions == 1) __syncthreads();
@@ -550,6 +552,12 @@ __global__ void __launch_bounds__(RingCfg<kCfg>::kThreads, RingCfg<kCfg>::kCtas)
             s = 0;
             phase ^= 1u;
         }
+    }
+    if (tid == 0 && aborted()) {
+        // no copy may land after the CTA: wait for the phase that each barrier is in (the limit also bounds the wait for
+        // one with no copy under way)
+        for (int i = 0; i < stages; ++i)
+            ptx::mbar_wait(&full[i], ptx::mbar_test(ptx::smem_addr(&full[i]), 0) ? 1u : 0u, nullptr);
     }
 }
 

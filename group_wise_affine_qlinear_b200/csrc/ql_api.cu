@@ -1398,7 +1398,7 @@ ql_status qlinear_selftest_bounded_wait(cudaStream_t stream) {
 
 ql_status qlinear_test_stall(int32_t kernel_mask, uint64_t wait_limit_ns) {
 #ifdef QL_BOUNDS_CHECK
-    if (kernel_mask < 0 || kernel_mask > (kStallFused | kStallSkinny | kStallNorm) || wait_limit_ns == 0) return QL_ERR_INVALID_ARG;
+    if (kernel_mask < 0 || kernel_mask > (kStallFused | kStallSkinny | kStallNorm | kStallPrepare) || wait_limit_ns == 0) return QL_ERR_INVALID_ARG;
     const unsigned long long limit = wait_limit_ns;
     if (cudaMemcpyToSymbol(g_stall_mask, &kernel_mask, sizeof(kernel_mask)) != cudaSuccess ||
         cudaMemcpyToSymbol(g_wait_limit_ns, &limit, sizeof(limit)) != cudaSuccess)

@@ -45,8 +45,9 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // records QL_ERR_DEVICE_TIMEOUT and lets the kernel unwind.
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;   // 1 s
 
-// Kernels whose code producer (the norms' ring: whose row copies) the checked build can hold back (qlinear_test_stall).
-constexpr int kStallFused = 1, kStallSkinny = 2, kStallNorm = 4;
+// Kernels whose code producer (the norms' ring, the adapters' first product: whose copies) the checked build can hold
+// back (qlinear_test_stall).
+constexpr int kStallFused = 1, kStallSkinny = 2, kStallNorm = 4, kStallPrepare = 8;
 
 #ifdef QL_BOUNDS_CHECK
 // Test hooks of the checked build (the index-checked variant): the host can shorten the wait limit and

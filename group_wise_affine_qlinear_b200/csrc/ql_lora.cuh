@@ -203,7 +203,7 @@ __device__ __forceinline__ void shrink_tile(const CUtensorMap& map_x, const CUte
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[q][i][e] = 0.0f;
         uint32_t mx[4] = {0u, 0u, 0u, 0u};                     // rows g, g + 8, g + 16, g + 24
-        if (lane == 0)
+        if (lane == 0 && ok && !stalled(kStallPrepare))        // (the checked build can hold every copy back)
             for (int i = 0; i < min(kSlots, nk); ++i) issue(i);
         for (int i = 0; i < nk; ++i, ++used) {
             const uint32_t s = used % kSlots;
@@ -242,7 +242,14 @@ __device__ __forceinline__ void shrink_tile(const CUtensorMap& map_x, const CUte
             __syncwarp();
             if (lane == 0 && ok && i + kSlots < nk) issue(i + kSlots);
         }
-        // the warp's ring is empty: its sums go there
+        // the warp's ring is empty: its sums go there (after an expired wait: once the copies under way have landed; none
+        // is started any more)
+        if (!ok && lane == 0) {
+            for (uint32_t at = issued > kSlots ? issued - kSlots : 0; at < issued; ++at)
+                ptx::mbar_wait(&full[warp][at % kSlots], (at / kSlots) & 1u, nullptr);
+            issued = 0;
+        }
+        __syncwarp();
         float* sums = part + warp * kPartStride;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -320,9 +327,6 @@ __device__ __forceinline__ void shrink_tile(const CUtensorMap& map_x, const CUte
         ptx::fence_proxy_async_smem();
         if (S > 1) ptx::cluster_sync(); else product_sync();
     }
-    if (!ok && lane == 0)                                      // an expired wait: leave no copy in flight
-        for (uint32_t at = issued > kSlots ? issued - kSlots : 0; at < issued; ++at)
-            ptx::mbar_wait(&full[warp][at % kSlots], (at / kSlots) & 1u, nullptr);
 }
 
 // The activations' conversion (as convert_x_kernel) of rows first, first + step, ... of the tile, a row by a pair of

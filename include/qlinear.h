@@ -176,7 +176,8 @@ QL_API ql_status qlinear_last_dispatch(char* buf, size_t len);
  * counterpart.  kernel_mask bit 0 holds back the code producer of the fused tensor-core kernel
  * (QL_PATH_TC_FUSED), bit 1 that of the weight-streaming kernel (QL_PATH_TC_SKINNY): they issue no code
  * or parameter load; bit 2 the row copies of qlinear_norm_residual's ring (D > 512 and more than two rows per
- * SM).  The kernel's other roles then wait until the limit, record QL_ERR_DEVICE_TIMEOUT and
+ * SM); bit 3 the copies of the kernel in front of QL_PATH_TC_FUSED that does the adapters' first product.  The
+ * kernel's other roles then wait until the limit, record QL_ERR_DEVICE_TIMEOUT and
  * unwind (nothing of theirs in flight, tensor memory freed).  wait_limit_ns replaces the one-second
  * limit of every bounded wait in the library's kernels (> 0); call with kernel_mask 0 and 1000000000
  * to restore the defaults.  Synchronous (two small host-to-device copies on the legacy stream).

@@ -65,7 +65,8 @@ __device__ __forceinline__ constexpr bool stalled(int) { return false; }
 
 // Roles of the tensor-core kernels that the checked build can hold back at their start (qlinear_test_delay):
 // the activation producer, the code producer, the dequantizers (builders), the MMA issuers and the
-// epilogue (drain) warps.
+// epilogue (drain) warps.  In the adapters' first product: the converting warps (activations), the tiles' lists (codes)
+// and the product's warps (MMA); in the norms' ring: the row copies (activations) and the warps (epilogue).
 constexpr int kDelayActivations = 1, kDelayCodes = 2, kDelayDequant = 4, kDelayMma = 8, kDelayEpilogue = 16;
 
 #ifdef QL_BOUNDS_CHECK
@@ -76,7 +77,7 @@ static __device__ int g_delay_mask;
 static __device__ unsigned long long g_delay_ns;
 __device__ __forceinline__ void test_delay(int role_bit) {
     if ((g_delay_mask & role_bit) == 0) return;
-    const uint64_t d = g_delay_ns * ((blockIdx.x * 7u + (threadIdx.x >> 5) * 3u) % 8u) / 7u;
+    const uint64_t d = g_delay_ns * ((blockIdx.x * 7u + blockIdx.y * 5u + (threadIdx.x >> 5) * 3u) % 8u) / 7u;
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < d) {
     }

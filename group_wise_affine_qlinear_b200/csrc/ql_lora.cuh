@@ -390,11 +390,13 @@ __global__ void __launch_bounds__(kBlock, 2) lora_prepare_kernel(const __grid_co
     const int tile = bx / products, i = bx - tile * products;
     if (threadIdx.x >= kThreads) {
         if (bx < 0 || i != 0) return;
+        test_delay(kDelayActivations);   // the checked build can hold these warps back (qlinear_test_delay)
         const int group = static_cast<int>(threadIdx.x - kThreads) / kConvThreads;
         if (p.bits == 4) convert_rows<4>(p, tile * kRows, rank + S * group, S * kConvGroups, group);
         else convert_rows<8>(p, tile * kRows, rank + S * group, S * kConvGroups, group);
         return;
     }
+    test_delay(bx < 0 ? kDelayCodes : kDelayMma);   // (and the lists', the product's)
     if (bx < 0) {
         const int t_blk = static_cast<int>(blockIdx.x) * S + rank;
         if (t_blk < p.num_t) plan_tile(p, t_blk);

@@ -482,6 +482,7 @@ __global__ void __launch_bounds__(RingCfg<kCfg>::kThreads, RingCfg<kCfg>::kCtas)
     int64_t m = p.M * blockIdx.x / gridDim.x;
     int next_seg = 0;                                      // of row m + stages, the next to copy
     if (tid == 0) {
+        test_delay(kDelayActivations);                     // the checked build can hold the copies back (qlinear_test_delay)
         int segs[kMaxStages];                              // all of them at once: their loads are the start's latency
 #pragma unroll
         for (int i = 0; i < kMaxStages; ++i) segs[i] = segment(m + i);
@@ -505,6 +506,7 @@ __global__ void __launch_bounds__(RingCfg<kCfg>::kThreads, RingCfg<kCfg>::kCtas)
     }
     // a wait of some thread has expired: no more stores or copies, the same barriers
     const auto aborted = [&] { return *const_cast<volatile int*>(&abort_flag) != 0; };
+    test_delay(kDelayEpilogue);                            // (and the warps)
     int s = 0;
     uint32_t phase = 0;
     for (; m < m_end; ++m) {

@@ -205,9 +205,10 @@ QL_API ql_status qlinear_test_ring_depth(int32_t variant);
  * (0/7 .. 7/7) of max_ns, so that every hand-off between roles (TMA rings, tensor-memory stages,
  * accumulators, partials) meets other orders of arrival; the output must not change.  Bits: 1 the
  * activation producer, 2 the code producer, 4 the dequantizers, 8 the MMA issuers, 16 the epilogue or
- * drain warps.  role_mask 0 turns it off.  Synchronous (two small host-to-device copies on the legacy
- * stream).  The shipped library returns QL_ERR_UNSUPPORTED; QL_ERR_INVALID_ARG for an unknown bit or
- * max_ns above 1 ms.
+ * drain warps; in the adapters' first product above 64 rows 1 the conversion, 2 the tiles' adapter lists, 8 the
+ * product; in the norms' ring 1 the row copies, 16 the warps.  role_mask 0 turns it off.  Synchronous (two
+ * small host-to-device copies on the legacy stream).  The shipped library returns QL_ERR_UNSUPPORTED;
+ * QL_ERR_INVALID_ARG for an unknown bit or max_ns above 1 ms.
  */
 QL_API ql_status qlinear_test_delay(int32_t role_mask, uint64_t max_ns);
 

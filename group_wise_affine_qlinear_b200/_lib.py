@@ -333,10 +333,18 @@ def swiglu(x: torch.Tensor, gate, up, out: torch.Tensor | None = None, workspace
 def _fit(dev: int, *specs) -> bool:
     """Whether every tensor of the (tensor, dtype, shape) specs is contiguous, of that type and shape, on CUDA device
     `dev`: the one pass of a call whose arguments are right.  Where it fails, the checks by name say what is wrong."""
-    for t, dtype, shape in specs:
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-            return False
+    try:
+        for t, dtype, shape in specs:
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+                return False
+    except AttributeError:                 # not a tensor
+        return False
     return True
+
+
+def _need_dims(t, dims: int, name: str) -> None:
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a tensor of {dims} dimensions")
 
 
 def _same_device(dev: torch.device, tensors) -> None:
@@ -374,9 +382,8 @@ def _need_workspace(workspace: torch.Tensor | None, dev: int) -> None:
 
 def _adapter_shape(a: torch.Tensor, b: torch.Tensor, what: str) -> tuple[int, int]:
     """(adapters, rank) of lora_a [L][r][K] and lora_b [L][N][r]."""
-    for name, t in (("_a", a), ("_b", b)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise ValueError(f"{what}{name} must be a tensor of three dimensions")
+    _need_dims(a, 3, what + "_a")
+    _need_dims(b, 3, what + "_b")
     n, r, _ = a.shape
     if n < 1 or r < 8 or r % 8 or r > LORA_MAX_RANK:
         raise ValueError(f"{what}_a: at least one adapter, of a rank that is a multiple of 8 up to {LORA_MAX_RANK}")
@@ -436,6 +443,8 @@ def forward8_lora(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bi
 
 def _forward_lora(x, codes, scales, biases, lora_a, lora_b, ids, lora_scale, out, workspace, out_dtype, stream, bits):
     L = lib()
+    _need_dims(x, 2, "x")
+    _need_dims(codes, 2, "codes")
     N, K = _weights_shape(codes, scales, bits)
     M = x.shape[0]
     n, r = _adapter_shape(lora_a, lora_b, "lora")
@@ -494,6 +503,8 @@ def swiglu_lora(x: torch.Tensor, gate, up, gate_lora, up_lora, adapter_ids: torc
     uc, us, ub = up
     ga, gbb = gate_lora
     ua, ubb = up_lora
+    _need_dims(x, 2, "x")
+    _need_dims(gc, 2, "gate codes")
     I, K = _weights_shape(gc, gs)
     M = x.shape[0]
     n, r = _adapter_shape(ga, gbb, "gate_lora")
@@ -588,28 +599,33 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: 
             raise ValueError("nothing to compute: no y and no pre_norm")
     # T: segments of gate, scale and shift; P: the vectors' type
     T = P = None
-    for t in (gate, scale, shift):
+    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
         if t is not None:
+            _need_dims(t, 2, name)
             T, P = t.shape[0], t.dtype
             break
     else:
-        if post_weight is not None:
-            P = post_weight.dtype
-        elif pre_weight is not None:
-            P = pre_weight.dtype
+        for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+            if t is not None:
+                _need_dims(t, 1, name)
+                P = t.dtype
+                break
     if segment_ids is None and T is not None and T != 1:
         raise ValueError("gate, scale and shift of several segments need segment_ids")
     dev = x.get_device()
     rows, vec, mod = (M, D), (D,), (T, D)
-    for t, dtype, shape, name in ((x, xd, rows, "x"), (y, None if y is None else y.dtype, rows if S == 0 else (S, M, D), "y"),
-                                  (post_weight, P, vec, "post_weight"), (gate, P, mod, "gate"),
-                                  (pre_weight, P, vec, "pre_weight"), (scale, P, mod, "scale"),
-                                  (shift, P, mod, "shift"), (segment_ids, torch.int32, rows[:1], "segment_ids"),
-                                  (out, xd, rows, "out"), (h, torch.bfloat16, rows, "h")):
-        if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 or
-                              not t.is_contiguous()):
-            _need_cuda(t, name, dtype, shape)
-            _same_device(x.device, ((name, t),))
+    try:
+        for t, dtype, shape, name in ((x, xd, rows, "x"), (y, None if y is None else y.dtype, rows if S == 0 else (S, M, D), "y"),
+                                      (post_weight, P, vec, "post_weight"), (gate, P, mod, "gate"),
+                                      (pre_weight, P, vec, "pre_weight"), (scale, P, mod, "scale"),
+                                      (shift, P, mod, "shift"), (segment_ids, torch.int32, rows[:1], "segment_ids"),
+                                      (out, xd, rows, "out"), (h, torch.bfloat16, rows, "h")):
+            if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 or
+                                  not t.is_contiguous()):
+                _need_cuda(t, name, dtype, shape)
+                _same_device(x.device, ((name, t),))
+    except AttributeError:
+        raise ValueError(f"{name} must be a CUDA tensor") from None
     pt = _BF16 if P is None or P is torch.bfloat16 else _F32
     if pt == _F32 and P is not torch.float32:
         raise ValueError(f"the weights, gate, scale and shift must be bfloat16 or float32, got {P}")

@@ -364,6 +364,8 @@ def _on_stream(dev: int, stream, call):
     inside belongs to it."""
     if stream is None and torch._C._cuda_getDevice() == dev:        # (a tensor on it: CUDA is initialized)
         return call(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is not None and stream.device.index != dev:           # its device would become the current one
+        raise ValueError(f"stream must be on cuda:{dev}, got one on {stream.device}")
     with torch.cuda.device(dev):
         if stream is None:
             return call(torch._C._cuda_getCurrentRawStream(dev))

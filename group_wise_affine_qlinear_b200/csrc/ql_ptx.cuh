@@ -100,15 +100,6 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
-// ------------------------------------------------------------------ programmatic dependent launch
-
 // ------------------------------------------------------------------ thread-block clusters
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -131,6 +122,8 @@ __device__ __forceinline__ float ld_shared_cluster_f32(const void* p, uint32_t r
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
     return v;
 }
+
+// ------------------------------------------------------------------ programmatic dependent launch
 
 // Lets the next kernel on the stream (launched with programmatic stream
 // serialization) be scheduled before this grid finishes; it must still call
@@ -162,8 +155,7 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
-// 2-D tiled bulk copy shared -> global (out-of-bounds elements are not written),
-// tracked by this thread's bulk async-group.
+// 3-D tiled bulk copy global -> shared, as tma_load_2d.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
                                             int32_t z) {
     asm volatile(
@@ -178,6 +170,8 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
 
+// 2-D tiled bulk copy shared -> global (out-of-bounds elements are not written),
+// tracked by this thread's bulk async-group.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
                  ::"l"(map), "r"(smem_addr(src)), "r"(x), "r"(y) : "memory");

@@ -587,14 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                     int s;
                     uint32_t ph;
                     ring_pos<NC>(ci, s, ph);
-                    if (ci >= static_cast<uint32_t>(NC) && !waited) {
-                        ptx::grid_dependency_wait();
-#pragma unroll
-                        for (int e = 0; e < NC; ++e)
-                            ptx::tma_load_2d(smem + C::kOffP + e * C::kPBytes, &map_params, &c_full[e],
-                                             first_w[e] * BW, first_kc[e]);
-                        waited = true;
-                    }
+                    if (ci >= static_cast<uint32_t>(NC) && !waited) late_params();
                     if (!ptx::mbar_wait(&c_empty[s], ph ^ 1, abort_flag)) { ok = false; break; }
                     ptx::mbar_arrive_expect_tx(&c_full[s], C::kCBytes + C::kPBytes);
                     load_codes(smem + C::kOffC + s * C::kCBytes, &c_full[s], kc, w_blk);

@@ -441,7 +441,9 @@ struct LoraPlan {
 };
 
 // Weight-streaming path: about as many one-warp tasks as the main kernel has drain warps (4 per SM), by cutting K into
-// up to 64 slices of at least four 32-column blocks.
+// up to 64 slices of at least four 32-column blocks.  (64 rows of 64 adapters leave one slice
+// from rank 72 on, a pair from 40 on: a warp then walks all of K, and the stream waits for it.  4608 -> 4608, 64 rows of
+// 64 adapters: rank 16 25 us, rank 128 114 us, without adapters 19 us, the bytes of rank 128 alone 25 us.)
 LoraPlan lora_plan_streaming(int64_t M, int64_t K, int r, int L, int pairs, size_t base, int sm_count) {
     LoraPlan lp;
     const int64_t tiles = (M + lora::kTile - 1) / lora::kTile;
@@ -974,7 +976,9 @@ ql_status run_swiglu_streaming(const Plan& pl, const LoraPlan& lp, const LoraArg
 }
 
 // Plans of the pair with adapters: streaming up to 64 tokens (sp.path QL_PATH_TC_SKINNY, a weight of both's tiles), else
-// the fused kernel.
+// the fused kernel.  Measured against the fused kernel at K = 4608, rank 16, four adapters, 1024 / 4608 / 12288 columns:
+// 1 token 18 / 25 / 35 us to 51 / 53 / 64; 24 tokens 26 / 29 / 43 to 57 / 58 / 61; 64 tokens 29 / 37 / 63 to 58 / 59 / 63; with
+// an adapter per token the fused kernel falls further behind (64 tokens of 4608 columns, rank 64: 133 us to 570).
 ql_status swiglu_lora_plan(int64_t M, int64_t K, int64_t I, int r, int L, int sm_count, Plan* sp, LoraPlan* lp) {
     if (M > 64) {
         sp->path = QL_PATH_TC_FUSED;
@@ -1258,7 +1262,7 @@ ql_status launch_norm(const norm::Params& p, int sm_count, cudaStream_t st) {
             norm::norm_group_kernel<kXF32, kY, 2><<<grid, 32 * norm::kGroupWarps, 0, st>>>(p, G, per_warp);
         return launch_status();
     }
-    if (p.M > 2 * sm_count) {
+    if (p.M > 2 * sm_count) {           // about where the ring's start is paid back (figures in ql_norm.cuh)
         constexpr int kYB = kY == norm::kYNone ? 0 : kY == norm::kYF32 ? 4 : 2;
         const uint32_t stage = norm::stage_bytes(p.D, kXF32 ? 4 : 2, kYB, kYB ? p.S : 0);
         RingShape rs;

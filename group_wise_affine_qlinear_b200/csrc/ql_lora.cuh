@@ -5,9 +5,10 @@
 //
 // A is bf16 [L][r][K], B bf16 [L][N][r], s fp32 [L]; a row with a negative id has no adapter.
 //
-// The first product ("shrink") reads every activation once more and the adapters in use; it is bound by that
-// traffic, so it runs on mma.sync straight from global memory (ql_lora_dot.cuh): on the fused path in the kernel below,
-// which converts the activations on the way, on the weight-streaming path in that kernel's idle warps.  The second
+// The first product ("shrink") reads every activation once more and the adapters in use: a flop per byte and rank, too
+// few for the tensor core's large tiles, so it runs on mma.sync: on the fused path in the kernel below, fed by TMA, which
+// converts the activations beside it, on the weight-streaming path straight from global memory in that kernel's drain
+// warps (ql_lora_dot.cuh).  The second
 // ("expand") never makes a pass over y of its own: the weight-streaming path adds it in fp32 where it sums its partials
 // (lora_reduce_kernel), the fused path appends it to the tile's K loop (ql_tc_fused.cuh), so y is rounded once.
 #pragma once
@@ -330,7 +331,8 @@ __device__ __forceinline__ void shrink_tile(const CUtensorMap& map_x, const CUte
 }
 
 // The activations' conversion (as convert_x_kernel) of rows first, first + step, ... of the tile, a row by a pair of
-// warps: its loads go out together and stay in registers (up to 4608 columns; more are read again from L2).
+// warps: its loads go out together and stay in registers, nine pieces of 8 a thread (4608 columns of a row; the product's
+// registers leave no more), and what is beyond is read again from L2.
 template <int kBits>
 __device__ __forceinline__ void convert_rows(const ShrinkParams& p, int m0, int first, int step, int group) {
     __shared__ float red[2][kConvGroups][2];
@@ -374,9 +376,11 @@ __device__ __forceinline__ void convert_rows(const ShrinkParams& p, int m0, int 
 // activations' conversion and the adapters' first product.  grid (plan_x + tiles * passes * chunks * pairs, S), cluster
 // (1, S, 1): first the lists, then the CTAs of every tile of 32 rows.  A tile's first column of CTAs also converts its
 // rows, in warps of their own beside the product's, so that the two readers of a row meet in L2 (33792 x 4608, rank 32:
-// 408 MB read from DRAM for 311 MB of x).  What bounds it there is the way from L2 to the SMs, 1.5 GB in 162 us: x twice,
-// its converted copy, and A once per tile.  (One kernel after the other read x from DRAM twice, 182 us; both by the same
-// warps, the tile held in shared memory between product and conversion, spent its time in one tile's barriers, 265 us.)
+// 408 MB read from DRAM for 311 MB of x).  What passes between L2 and the SMs there is x twice, its converted copy and A
+// once per tile, 1.24 GB in 162 us; neither DRAM nor L2 is near its rate (a fifth and a third of it), each warp waits for
+// its own three boxes.  With few tiles it is latency: 18 us for 333 rows.  (One kernel after the other read x from DRAM
+// twice, 182 us; both by the same warps, the tile held in shared memory between product and conversion, spent its time in
+// one tile's barriers, 265 us.)  Two CTAs per SM leave 80 registers a thread, of which 31 to 40 are spilled.
 template <int NT>
 __global__ void __launch_bounds__(kBlock, 2) lora_prepare_kernel(const __grid_constant__ CUtensorMap map_x,
                                                                  const __grid_constant__ CUtensorMap map_a0,

@@ -12,13 +12,21 @@
 // The operation moves each row once and does a dozen flops per element, so DRAM bounds it; a row therefore stays in
 // registers from its load to its stores.  What it must not do is fetch and combine the five vectors (weights, gate,
 // scale, shift) again for every row: that alone is 2.5 times the row's bytes from L1 and half of the instructions
-// (4608 x 4608, bf16: 59 us with the vectors read per row, 46% of all issue slots busy; 45 us, 3.8 TB/s, with them held in
-// registers, premultiplied, for as long as the segment stays the same; 33792 rows 238 us, 5.2 TB/s; with an fp32 residual
-// and two fp32 partials 451 us, 6.2 TB/s).  Forms:
-//   D <= kGroupMax          8, 16 or 32 lanes per row, no block barrier, the next row loaded ahead into registers
-//   longer rows, a few      a CTA per row, straight from global memory (latency: everything is loaded at once)
+// (4608 x 4608, bf16: 59 us with the vectors read per row, 46% of all issue slots busy; 43 us, 3.9 TB/s, with them held in
+// registers, premultiplied, for as long as the segment stays the same; 33792 rows 223 us, 5.6 TB/s; with an fp32 residual
+// and two fp32 partials 467 us, 6.0 TB/s).  Forms, with what each measured against the other (bf16, one call on cold
+// caches, some 7 us of each being the call's start and end):
+//   D <= kGroupMax          8, 16 or 32 lanes per row, no block barrier, the next row loaded ahead into registers.  33792
+//                           rows against the other forms: 72 columns 16 us to 22, 128 18 to 23, 256 26 to 25, 384 46 to
+//                           35, 512 47 to 37: it pays up to 256 columns.
+//   longer rows, a few      a CTA per row, straight from global memory (latency: everything is loaded at once).  148 rows
+//                           of 4608 against the ring: 10 us to 12; 296 rows 14 to 14; 592 rows 18 to 16; 1184 rows 29 to
+//                           20; but of 16384 columns 1184 rows 61 to 78 (the ring has one CTA per SM there).
 //   longer rows, many       persistent CTAs over consecutive rows with a ring of rows in shared memory, filled by bulk
 //                           copies while earlier rows are reduced and written
+// Rows too wide for two of them in an SM's shared memory take a CTA per row at any number; with four pieces per thread that
+// form has 1024 threads of 64 registers, spills (up to 532 bytes, fp32 with partials) and loads a piece's partials one
+// after the other: 4096 x 8192, fp32 with three partials 194 us, 3.8 TB/s; 2048 x 18432 with two 271 us, 2.5 TB/s.
 #pragma once
 
 #include "ql_ptx.cuh"
@@ -27,7 +35,7 @@ namespace ql {
 namespace norm {
 
 constexpr int kMaxD = 32768;          // 1024 threads x 4 vectors of 8
-constexpr int kGroupMax = 512;        // 32 lanes x 2 vectors of 8
+constexpr int kGroupMax = 512;        // 32 lanes x 2 vectors of 8 (see above: the second pays no longer)
 constexpr int kGroupWarps = 4;        // warps per CTA of the group form
 
 enum { kYNone = 0, kYBf16 = 1, kYF32 = 2 };

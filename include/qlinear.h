@@ -356,7 +356,8 @@ QL_API ql_status qlinear_reduce_partials(const float* partials, int32_t S, int64
  *
  * Up to 64 rows the weights are streamed as in qlinear_forward and the adapters are added where the partial sums
  * meet; above, they are extra K-steps of the fused kernel, one 64-column step per 32 / r distinct adapters of each
- * 192-row tile, so rows of one adapter are best kept together.
+ * 192-row tile, so rows of one adapter are best kept together (tokens in no order also have their t copied in
+ * smaller pieces: 4608 rows of 30 adapters, r = 16, K = N = 4608 take 385 us against 205 in order).
  */
 QL_API size_t qlinear_lora_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group, int32_t L, int32_t r);
 QL_API ql_status qlinear_lora_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
@@ -412,7 +413,8 @@ QL_API ql_status qlinear_swiglu_lora_forward(const void* x, const uint32_t* gate
  * Required (QL_ERR_INVALID_ARG): M >= 1, D >= 8, D % 8 == 0, T >= 1, S >= 1 (S == 1 for bf16 y), eps >= 0 and finite,
  * at least one output.  D <= QL_NORM_MAX_D (QL_ERR_UNSUPPORTED above).  All pointers 16-byte aligned except
  * segment_ids (4).  No workspace.  The mean squares are fp32 sums: a row whose sum of squares leaves fp32's range
- * normalizes by infinity.
+ * normalizes by infinity, and one whose squares fall below it (entries under about 2^-63) by sqrt(eps) alone, so
+ * with eps = 0 its result is infinite or NaN.
  */
 #define QL_NORM_MAX_D 32768
 QL_API ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const void* y, ql_dtype y_dtype, int32_t S,

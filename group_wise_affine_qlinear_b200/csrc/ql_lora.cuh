@@ -380,7 +380,7 @@ __device__ __forceinline__ void convert_rows(const ShrinkParams& p, int m0, int 
 // once per tile, 1.24 GB in 162 us; neither DRAM nor L2 is near its rate (a fifth and a third of it), each warp waits for
 // its own three boxes.  With few tiles it is latency: 18 us for 333 rows.  (One kernel after the other read x from DRAM
 // twice, 182 us; both by the same warps, the tile held in shared memory between product and conversion, spent its time in
-// one tile's barriers, 265 us.)  Two CTAs per SM leave 80 registers a thread, of which 31 to 40 are spilled.
+// one tile's barriers, 265 us.)  Two CTAs per SM leave 80 registers a thread; 31 to 35 are spilled.
 template <int NT>
 __global__ void __launch_bounds__(kBlock, 2) lora_prepare_kernel(const __grid_constant__ CUtensorMap map_x,
                                                                  const __grid_constant__ CUtensorMap map_a0,

@@ -1,5 +1,5 @@
-// The adapters' first product, t[m][j] = sum_k x[m][k] A[a][j][k], a warp's part of it: shared by the kernel in front
-// of the fused path and by the weight-streaming kernel, whose idle warps do it beside the stream.
+// The adapters' first product, t[m][j] = sum_k x[m][k] A[a][j][k]: what the kernel in front of the fused path and the
+// weight-streaming kernel share of it, and the latter's tasks, which its drain warps do beside the stream.
 #pragma once
 
 #include "ql_common.cuh"

@@ -48,9 +48,10 @@
 //   warps 4-19    A builders, copies 0-3 of 4 warps: one weight row per thread
 //   warps 20-23   drain: one weight row per thread, at the end of each tile segment
 // Adapter mode (kLora, low-rank adapters beside the layer): the drain warps, idle until their first segment ends, do
-// the adapters' first product meanwhile (run_dot_tasks), beside the stream of codes and off its critical path; the
-// adapters' reduce kernel adds the second product.  As a kernel of its own in front of the prepass the first product
-// cost 8 us at M = 1 and 24 us with 8 rows of 53248 columns.
+// the adapters' first product meanwhile (run_dot_tasks), beside the stream of codes; the adapters' reduce kernel adds the
+// second product.  As a kernel of its own in front of the prepass the first product cost 8 us at M = 1 and 24 us with 8
+// rows of 53248 columns.  (It outlasts the stream, and finished segments wait for it, where many adapters of a high rank
+// meet: 64 rows of 64 adapters, 4608 -> 4608, rank 128: 114 us for a stream of 19.)
 // Pair mode (kPair, a SwiGLU pair with adapters): the up weight's tiles follow the gate weight's in one run of chunks, so
 // both stream in one launch; the pair's reduce kernel brings a tile's two halves together.
 #pragma once

@@ -90,9 +90,9 @@ def draw(rng):
         N = 8 * _log_int(rng, 8, 2304)
         M = _log_int(rng, 1, max(1, min(8192, 4609 * 12288 * 4608 // (K * N))))
         return {"op": op, "M": M, "K": K, "N": N, "bits": rng.choice([4, 4, 8]),
-                "act": rng.choice([None, None, "silu", "gelu", "gelu_tanh"]), "bias": rng.random() < 0.7, "gate": rng.random() < 0.5,
-                "residual": rng.random() < 0.6, "params": rng.choice(["bf16", "f32"]), "segments": rng.randint(1, min(6, M)),
-                "padding": rng.choice([0, rng.randint(0, M // 16)])}
+                "act": rng.choice([None, None, "silu", "gelu", "gelu_tanh"]), "bias": rng.random() < 0.7,
+                "gate": rng.random() < 0.5, "residual": rng.random() < 0.6, "params": rng.choice(["bf16", "f32"]),
+                "segments": rng.randint(1, min(6, M)), "padding": rng.choice([0, rng.randint(0, M // 16)])}
     D = rng.choice([64, 80, 96, 128, 160, 192, 256])
     pairs = D // 2 if rng.random() < 0.6 else 8 * rng.randint(1, D // 16)
     axes = rng.randint(1, min(4, pairs))
@@ -197,7 +197,8 @@ def prepare(case, seed):
               "x": (torch.randn((M, K), generator=g, device="cuda") * sigma).bfloat16()}
         st["bias"] = torch.randn(N, generator=g, device="cuda").to(pt) if case["bias"] else None
         st["gate"] = (0.5 * torch.randn((T, N), generator=g, device="cuda")).to(pt) if case["gate"] else None
-        st["residual"] = (3.0 * torch.randn((M, N), generator=g, device="cuda")).bfloat16() if case["residual"] else None
+        r = 3.0 * torch.randn((M, N), generator=g, device="cuda") if case["residual"] else None
+        st["residual"] = r.bfloat16() if case["residual"] else None
         st["segment_ids"] = _segments(M, T, case["padding"]) if T > 1 or case["padding"] else None
         st["out"] = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
         return st

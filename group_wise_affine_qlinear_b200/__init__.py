@@ -19,10 +19,25 @@ and biases.  swiglu(x, gate, up) runs a SwiGLU up/gate pair of two packed
 
 Beside the packed projections: forward_lora, forward8_lora and swiglu_lora add the low-rank adapters of many
 requests, each row its own (lora_a bf16 [L][r][K], lora_b bf16 [L][N][r], adapter_ids int32 [M]); norm_residual
-does the norms after and before a block with its gate and residual update.
+does the norms after and before a block with its gate and residual update.  forward_epilogue and forward8_epilogue are
+projections with bias, activation, gate and residual in their epilogue; qk_norm_rotary does the norms of queries and
+keys head by head and their rotation by positions of several axes, rotary_axes that rotation alone (rotary_frequencies
+makes its frequencies).
 """
 from __future__ import annotations
 
+from ._epilogue import (  # noqa: F401
+    ACTIVATIONS,
+    epilogue_workspace_size,
+    forward8_epilogue,
+    forward_epilogue,
+)
+from ._heads import (  # noqa: F401
+    HEAD_MAX_D,
+    qk_norm_rotary,
+    rotary_axes,
+    rotary_frequencies,
+)
 from ._lib import (  # noqa: F401
     GROUP,
     LORA_MAX_RANK,

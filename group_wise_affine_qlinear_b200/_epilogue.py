@@ -1,0 +1,107 @@
+"""Packed projections with bias, activation, gate and residual in their epilogue (see include/qlinear.h)."""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from ._lib import (GROUP, _BF16, _F32, _check, _fit, _need_cuda, _need_dims, _need_workspace, _new, _on_stream, _ptr,
+                   _same_device, _weights_shape, lib)
+
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def epilogue_workspace_size(M: int, K: int, N: int, bits: int = 4) -> int:
+    """Workspace bytes of forward_epilogue() (bits=8: forward8_epilogue())."""
+    fn = lib().qlinear_epilogue_workspace_size if bits == 4 else lib().qlinear8_epilogue_workspace_size
+    v = fn(M, K, N, GROUP)
+    if v == ctypes.c_size_t(-1).value:
+        raise ValueError("shape not supported")
+    return int(v)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace(dev: int, M: int, K: int, N: int, bits: int) -> int:
+    """epilogue_workspace_size() on device `dev` (which is current)."""
+    return epilogue_workspace_size(M, K, N, bits)
+
+
+def forward_epilogue(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, biases: torch.Tensor, *,
+                     bias: torch.Tensor | None = None, activation: str | None = None, gate: torch.Tensor | None = None,
+                     residual: torch.Tensor | None = None, segment_ids: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, out_dtype=None,
+                     stream=None) -> torch.Tensor:
+    """y = residual + gate[seg] * act(x . W^T + bias), rounded once (qlinear_epilogue_forward).
+
+    bias [N] and gate [T][N], both bf16 or both fp32; activation None, "silu", "gelu" or "gelu_tanh"; residual [M][N] of
+    y's type; segment_ids int32 [M] (None: segment 0), a negative one for a padding row, whose row of y is left alone.
+    out may be residual (the update in place).  out_dtype bfloat16 or float32 (None: residual's or out's, else bfloat16).
+    """
+    return _forward_epilogue(x, codes, scales, biases, bias, activation, gate, residual, segment_ids, out, workspace,
+                             out_dtype, stream, 4)
+
+
+def forward8_epilogue(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, biases: torch.Tensor, *,
+                      bias: torch.Tensor | None = None, activation: str | None = None,
+                      gate: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                      segment_ids: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, out_dtype=None, stream=None) -> torch.Tensor:
+    """forward_epilogue() for 8-bit codes, int32 [N][K/4] (qlinear8_epilogue_forward)."""
+    return _forward_epilogue(x, codes, scales, biases, bias, activation, gate, residual, segment_ids, out, workspace,
+                             out_dtype, stream, 8)
+
+
+def _forward_epilogue(x, codes, scales, biases, bias, activation, gate, residual, segment_ids, out, workspace, out_dtype,
+                      stream, bits):
+    L = lib()
+    _need_dims(x, 2, "x")
+    _need_dims(codes, 2, "codes")
+    N, K = _weights_shape(codes, scales, bits)
+    M = x.shape[0]
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    for t, dims, name in ((bias, 1, "bias"), (gate, 2, "gate"), (residual, 2, "residual"), (out, 2, "out")):
+        if t is not None:
+            _need_dims(t, dims, name)
+    if out_dtype is None:
+        out_dtype = residual.dtype if residual is not None else out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("y, its residual and out_dtype must be bfloat16 or float32")
+    P = bias.dtype if bias is not None else gate.dtype if gate is not None else torch.bfloat16
+    if P not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"bias and gate must be bfloat16 or float32, got {P}")
+    T = gate.shape[0] if gate is not None else 1
+    if T < 1:
+        raise ValueError("gate holds no segments")
+    if segment_ids is None and T != 1:
+        raise ValueError("a gate of several segments needs segment_ids")
+    dev = x.get_device()
+    optional = [(t, dtype, shape, name) for t, dtype, shape, name in
+                ((bias, P, (N,), "bias"), (gate, P, (T, N), "gate"), (residual, out_dtype, (M, N), "residual"),
+                 (segment_ids, torch.int32, (M,), "segment_ids"), (out, out_dtype, (M, N), "out")) if t is not None]
+    if not (dev >= 0 and _fit(dev, (x, torch.bfloat16, (M, K)), (codes, torch.int32, (N, K * bits // 32)),
+                              (scales, torch.float16, (N, K // GROUP)), (biases, torch.float16, (N, K // GROUP)),
+                              *[o[:3] for o in optional])):
+        _need_cuda(x, "x", torch.bfloat16, (M, K))
+        _need_cuda(codes, "codes", torch.int32, (N, K * bits // 32))
+        _need_cuda(scales, "scales", torch.float16, (N, K // GROUP))
+        _need_cuda(biases, "biases", torch.float16, (N, K // GROUP))
+        for t, dtype, shape, name in optional:
+            _need_cuda(t, name, dtype, shape)
+        _same_device(x.device, [("codes", codes), ("scales", scales), ("biases", biases)] +
+                     [(name, t) for t, _, _, name in optional])
+    _need_workspace(workspace, dev)
+    name = "qlinear_epilogue_forward" if bits == 4 else "qlinear8_epilogue_forward"
+
+    def call(st):
+        y = _new(x, (M, N), out_dtype) if out is None else out
+        ws = x.new_empty(_workspace(dev, M, K, N, bits) // 2) if workspace is None else workspace
+        # without a gate every segment is as good as any other
+        _check(getattr(L, name)(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(), _ptr(bias),
+                                ACTIVATIONS[activation], _ptr(gate), _BF16 if P == torch.bfloat16 else _F32,
+                                _ptr(residual), _ptr(segment_ids), T if gate is not None else 2 ** 31 - 1, y.data_ptr(),
+                                _BF16 if out_dtype == torch.bfloat16 else _F32, M, K, N, GROUP, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), st), name)
+        return y
+    return _on_stream(dev, stream, call)

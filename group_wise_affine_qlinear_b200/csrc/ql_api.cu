@@ -14,12 +14,14 @@
 
 #include "ql_common.cuh"
 #include "ql_dequant.cuh"
+#include "ql_epilogue.cuh"
 #include "ql_gemv.cuh"
 #include "ql_lora.cuh"
 #include "ql_norm.cuh"
 #include "ql_pack.cuh"
 #include "ql_pack_fit.cuh"
 #include "ql_prepass.cuh"
+#include "ql_rotary.cuh"
 #include "ql_tc_fused.cuh"
 #include "ql_tc_skinny.cuh"
 
@@ -566,6 +568,17 @@ ql_status lora_params(const LoraArgs& la, const LoraPlan& lp, uint8_t* ws, int64
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The epilogue of split K-steps: their ordered sum, four columns per thread and several rows each.
+ql_status launch_epilogue_sum(const float* part, void* y, bool bf16_out, int64_t M, int64_t N, int S,
+                              const epi::Epilogue& e, int sm_count, cudaStream_t st) {
+    const int64_t cols = (N / 4 + 255) / 256;
+    const dim3 grid(static_cast<unsigned>(cols),
+                    static_cast<unsigned>(std::min<int64_t>(M, std::max<int64_t>(1, 8 * sm_count / cols))));
+    const int n = static_cast<int>(N);
+    return bf16_out ? launch_dependent(epi::epilogue_sum_kernel<true>, grid, 256, 0, st, part, y, M, n, S, e)
+                    : launch_dependent(epi::epilogue_sum_kernel<false>, grid, 256, 0, st, part, y, M, n, S, e);
+}
+
 // Launches the fused kernel of a template configuration, with or without adapters.
 template <bool kBf16Out, class FC, bool kSwiGLU, bool kSplitK>
 ql_status launch_fused(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& mc, const CUtensorMap& mc2,
@@ -579,7 +592,8 @@ ql_status launch_fused(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const 
 
 ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
                     void* y, bool bf16_out, int64_t M, int64_t K, int64_t N, void* ws, cudaStream_t st,
-                    int sm_count, const LoraArgs* la = nullptr, const LoraPlan* lp = nullptr) {
+                    int sm_count, const LoraArgs* la = nullptr, const LoraPlan* lp = nullptr,
+                    const epi::Epilogue* ep = nullptr) {
     const int64_t G = K / kGroup;
     auto* base = static_cast<uint8_t*>(ws);
     auto* xh = reinterpret_cast<__half*>(base + pl.off_xh);
@@ -602,7 +616,7 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
                        CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK)
         return s;
     CUtensorMap my;
-    const bool split = pl.split_k > 1;
+    const bool split = pl.split_k > 1 || ep != nullptr;
     float* part = reinterpret_cast<float*>(base + pl.off_part);
     if (split) {
         // fp32 partials [split_k][M][N]: 32 x 32 blocks, clipped at M and N within every slice
@@ -650,14 +664,18 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
         // ordered sum of the slices, rounded once (a plain launch: it reads what the kernel above wrote)
         const int64_t count = M * N;
         const int blocks = static_cast<int>(std::min<int64_t>((count / 4 + 255) / 256, 8 * sm_count));
-        if (bf16_out)
+        if (ep != nullptr)
+            s = launch_epilogue_sum(part, y, bf16_out, M, N, pl.split_k, *ep, sm_count, st);
+        else if (bf16_out)
             ordered_sum_kernel<true><<<blocks, 256, 0, st>>>(part, y, count, pl.split_k);
         else
             ordered_sum_kernel<false><<<blocks, 256, 0, st>>>(part, y, count, pl.split_k);
+        if (s != QL_OK) return s;
         const int nc = bits == 4 ? F4::kNC : F8::kNC;
         const int nx = bits == 4 ? F4::kNX : F8::kNX;
         set_dispatch("path=tc_fused%s bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=%d launches=%d why=%s",
-                     la ? "_lora" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid, pl.split_k, 4, pl.why);
+                     la ? "_lora" : ep ? "_epilogue" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid,
+                     pl.split_k, 4, pl.why);
         return launch_status();
     }
     using B4 = fused::PickCfg<4, true>::type;
@@ -758,7 +776,8 @@ ql_status skinny_weight_maps(const uint32_t* codes, const void* scales, const vo
 
 ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
                      void* y, bool bf16_out, int64_t M, int64_t K, int64_t N, void* ws, cudaStream_t st,
-                     int sm_count, const LoraArgs* la = nullptr, const LoraPlan* lp = nullptr) {
+                     int sm_count, const LoraArgs* la = nullptr, const LoraPlan* lp = nullptr,
+                     const epi::Epilogue* ep = nullptr) {
     const int64_t G = K / kGroup;
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     void* xp = wsb + pl.off_xp;
@@ -818,6 +837,10 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
         auto red = bf16_out ? lora::lora_reduce_kernel<true, false> : lora::lora_reduce_kernel<false, false>;
         s = launch_dependent(red, reduce_grid(p.num_w, M, sm_count), 256, 0, st, part, rexp, y, p.M, p.N, p.cpt, p.units,
                              pl.ctas, pl.segmax, p.partial_elems, expand_params(*la, *lp, wsb));
+    } else if (ep) {
+        auto red = bf16_out ? epi::epilogue_reduce_kernel<true> : epi::epilogue_reduce_kernel<false>;
+        s = launch_dependent(red, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt, p.units, pl.ctas, pl.segmax,
+                             p.partial_elems, *ep);
     } else if (bf16_out)
         s = launch_dependent(skinny::skinny_reduce_kernel<true>, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt,
                              p.units, pl.ctas, pl.segmax, p.partial_elems);
@@ -825,8 +848,8 @@ ql_status run_skinny(const Plan& pl, const void* x, const uint32_t* codes, const
         s = launch_dependent(skinny::skinny_reduce_kernel<false>, red_grid, 256, 0, st, part, rexp, y, p.M, p.N, p.cpt,
                              p.units, pl.ctas, pl.segmax, p.partial_elems);
     if (s != QL_OK) return s;
-    set_dispatch("path=tc_skinny%s bits=%d nt=%d ctas=%d segmax=%d units=%lld launches=3 why=%s", la ? "_lora" : "", bits,
-                 pl.nt, pl.ctas, pl.segmax, static_cast<long long>(pl.units), pl.why);
+    set_dispatch("path=tc_skinny%s bits=%d nt=%d ctas=%d segmax=%d units=%lld launches=3 why=%s",
+                 la ? "_lora" : ep ? "_epilogue" : "", bits, pl.nt, pl.ctas, pl.segmax, static_cast<long long>(pl.units), pl.why);
     return launch_status();
 }
 
@@ -1058,12 +1081,33 @@ ql_status swiglu_impl(const void* x, const uint32_t* gc, const void* gs, const v
                       dev->sm_count, la, &lp);
 }
 
+// What follows the projection in its epilogue.
+struct EpilogueArgs {
+    epi::Epilogue e = {};
+};
+
+ql_status check_epilogue(const EpilogueArgs& a) {
+    const epi::Epilogue& e = a.e;
+    if (e.act < QL_ACT_NONE || e.act > QL_ACT_GELU_TANH || e.T < 1) return QL_ERR_INVALID_ARG;
+    if (!aligned16(e.bias) || !aligned16(e.gate) || !aligned16(e.residual) || (reinterpret_cast<uintptr_t>(e.seg) & 3u) != 0)
+        return QL_ERR_ALIGNMENT;
+    return QL_OK;
+}
+
+// Whether [p, p + n) meets the epilogue's vectors or segments.
+bool epilogue_overlaps(const EpilogueArgs& a, int64_t M, int64_t N, const void* p, size_t n) {
+    const size_t vb = static_cast<size_t>(N) * (a.e.params_f32 ? 4 : 2);
+    return (a.e.bias && overlap(p, n, a.e.bias, vb)) || (a.e.gate && overlap(p, n, a.e.gate, vb * a.e.T)) ||
+           (a.e.seg && overlap(p, n, a.e.seg, static_cast<size_t>(M) * 4));
+}
+
 ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales, const void* biases, void* y,
                        ql_dtype out_dtype, int64_t M, int64_t K, int64_t N, int32_t group, int32_t path,
                        int32_t split_k, void* workspace, size_t workspace_bytes, cudaStream_t stream, int bits,
-                       const LoraArgs* la = nullptr) {
+                       const LoraArgs* la = nullptr, const EpilogueArgs* ep = nullptr) {
     ql_status s = check_shape(M, K, N, group);
     if (s == QL_OK && la) s = check_lora(*la);
+    if (s == QL_OK && ep) s = check_epilogue(*ep);
     if (s != QL_OK) return s;
     if (!x || !codes || !scales || !biases || !y) return QL_ERR_INVALID_ARG;
     if (out_dtype != QL_BF16 && out_dtype != QL_F32) return QL_ERR_INVALID_ARG;
@@ -1077,6 +1121,9 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
     if (overlap(y, yb, x, xb) || overlap(y, yb, codes, cb) || overlap(y, yb, scales, pb) || overlap(y, yb, biases, pb))
         return QL_ERR_INVALID_ARG;
     if (la && lora_overlaps(*la, M, K, N, y, yb)) return QL_ERR_INVALID_ARG;
+    if (ep && (epilogue_overlaps(*ep, M, N, y, yb) ||
+               (ep->e.residual && ep->e.residual != y && overlap(y, yb, ep->e.residual, yb))))
+        return QL_ERR_INVALID_ARG;
     DeviceInfo* dev = nullptr;
     if ((s = device_info(&dev)) != QL_OK) return s;
     Plan pl;
@@ -1087,20 +1134,24 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
         lp = lora_plan(pl, M, K, la->r, la->L, dev->sm_count);
         need = lp.workspace;
     }
+    if (ep && pl.path == QL_PATH_TC_FUSED && pl.split_k == 1) need += static_cast<size_t>(M) * N * 4;
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return QL_ERR_WORKSPACE;
         if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
         if (overlap(workspace, need, x, xb) || overlap(workspace, need, y, yb) ||
             overlap(workspace, need, codes, cb) || overlap(workspace, need, scales, pb) ||
-            overlap(workspace, need, biases, pb) || (la && lora_overlaps(*la, M, K, N, workspace, need)))
+            overlap(workspace, need, biases, pb) || (la && lora_overlaps(*la, M, K, N, workspace, need)) ||
+            (ep && (epilogue_overlaps(*ep, M, N, workspace, need) || overlap(workspace, need, ep->e.residual, yb))))
             return QL_ERR_INVALID_ARG;
     }
     const bool bf16 = out_dtype == QL_BF16;
+    const epi::Epilogue* e = ep ? &ep->e : nullptr;
     if (pl.path == QL_PATH_GEMV)
         return run_gemv(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count);
     if (pl.path == QL_PATH_TC_SKINNY)
-        return run_skinny(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count, la, &lp);
-    return run_fused(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count, la, &lp);
+        return run_skinny(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count, la, &lp,
+                          e);
+    return run_fused(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count, la, &lp, e);
 }
 
 LoraArgs lora_args(const void* a, const void* b, const float* scale, const int32_t* ids, int32_t L, int32_t r) {
@@ -1355,6 +1406,151 @@ ql_status norm_residual_impl(const void* x, ql_dtype x_dtype, const void* y, ql_
                              : launch_norm<false, norm::kYBf16>(p, sm, stream);
 }
 
+// ------------------------------------------------------------------ norms and rotation of heads
+
+// Elements from the first to one past the last of [M][H][D] heads with these strides.
+int64_t heads_span(int64_t token, int64_t head, int64_t M, int64_t H, int64_t D) {
+    return (M - 1) * token + (H - 1) * head + D;
+}
+
+// Whether two sets of heads (element offsets from a common base in units of one byte each) may share memory.  Spans
+// apart share none; so do rows of one period that lie apart in it, as the queries and keys of a packed projection.
+bool heads_overlap(const void* a, int64_t at, int64_t ah, int64_t aheads, const void* b, int64_t bt, int64_t bh,
+                   int64_t bheads, int64_t M, int64_t D, int64_t size) {
+    const auto ax = reinterpret_cast<intptr_t>(a), bx = reinterpret_cast<intptr_t>(b);
+    if (!overlap(a, heads_span(at, ah, M, aheads, D) * size, b, heads_span(bt, bh, M, bheads, D) * size)) return false;
+    if (M == 1 || at != bt || at <= 0) return true;
+    const int64_t period = at * size, na = heads_span(0, ah, 1, aheads, D) * size, nb = heads_span(0, bh, 1, bheads, D) * size;
+    if (na > period || nb > period) return true;
+    const int64_t d = (((bx - ax) % period) + period) % period;        // b's row begins d bytes behind a row of a
+    return d < na || period - d < nb;
+}
+
+ql_status check_heads(const ql_heads& q, int64_t M, int64_t D, int64_t unit, ql_dtype weight_dtype) {
+    if (!q.in || !q.out || q.heads < 1 || !dtype_ok(weight_dtype)) return QL_ERR_INVALID_ARG;
+    // (a stride that only one token or head has is never used)
+    const int64_t st[4] = {M > 1 ? q.in_token : 0, q.heads > 1 ? q.in_head : 0, M > 1 ? q.out_token : 0,
+                           q.heads > 1 ? q.out_head : 0};
+    for (int64_t v : st) {
+        if (v < 0 || v > (1ll << 56) / std::max<int64_t>(M, q.heads)) return QL_ERR_INVALID_ARG;
+        if (v % unit != 0) return QL_ERR_ALIGNMENT;
+    }
+    if (!aligned16(q.in) || !aligned16(q.out) || !aligned16(q.weight)) return QL_ERR_ALIGNMENT;
+    // every output element has a place of its own: tokens of whole heads, or heads of whole tokens
+    const int64_t H = q.heads, t = st[2], h = st[3];
+    const bool by_token = (H == 1 || h >= D) && (M == 1 || t >= (H - 1) * h + D);
+    const bool by_head = (M == 1 || t >= D) && (H == 1 || h >= (M - 1) * t + D);
+    return by_token || by_head ? QL_OK : QL_ERR_INVALID_ARG;
+}
+
+template <bool kF32, bool kAdjacent>
+ql_status launch_heads(const rotary::Params& p, int G, int64_t units, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>((units + rotary::kWarps - 1) / rotary::kWarps));
+    constexpr int kBlock = 32 * rotary::kWarps;
+    if (G == 4) rotary::heads_kernel<kF32, kAdjacent, 4><<<grid, kBlock, 0, st>>>(p);
+    else if (G == 8) rotary::heads_kernel<kF32, kAdjacent, 8><<<grid, kBlock, 0, st>>>(p);
+    else if (G == 16) rotary::heads_kernel<kF32, kAdjacent, 16><<<grid, kBlock, 0, st>>>(p);
+    else rotary::heads_kernel<kF32, kAdjacent, 32><<<grid, kBlock, 0, st>>>(p);
+    return launch_status();
+}
+
+ql_status heads_impl(const ql_heads* q, const ql_heads* k, ql_dtype dtype, int32_t norm_on, ql_dtype weight_dtype, float eps,
+                     const void* positions, int32_t pos_type, int32_t A, const double* turns, const int32_t* axes,
+                     int32_t P, int32_t adjacent, const int32_t* segment_ids, int64_t M, int64_t D, cudaStream_t stream) {
+    if (!q || M < 1 || M > (1ll << 31) - 1 || D < 8 || D % 8 != 0 || P < 0 || 2ll * P > D) return QL_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || (P == 0 && !norm_on)) return QL_ERR_INVALID_ARG;
+    if (norm_on && (!(eps >= 0.0f) || eps > 3.4028235e38f)) return QL_ERR_INVALID_ARG;
+    if (P > 0 && (!positions || !turns || !axes || A < 1 || A > QL_HEAD_MAX_D || pos_type < QL_POS_I32 || pos_type > QL_POS_F32))
+        return QL_ERR_INVALID_ARG;
+    if (P % 8 != 0 || D > QL_HEAD_MAX_D) return QL_ERR_UNSUPPORTED;
+    static_assert(QL_HEAD_MAX_D == rotary::kMaxD, "the documented limit is the kernel's");
+    const int64_t size = dtype == QL_BF16 ? 2 : 4;
+    const ql_heads* set[2] = {q, k};
+    ql_status s;
+    for (const ql_heads* h : set)
+        if (h) {
+            if (!norm_on && h->weight) return QL_ERR_INVALID_ARG;
+            if ((s = check_heads(*h, M, D, 16 / size, weight_dtype)) != QL_OK) return s;
+        }
+    const int64_t pos_size = pos_type == QL_POS_I64 ? 8 : 4;
+    if (P > 0 && (reinterpret_cast<uintptr_t>(positions) % pos_size != 0 || reinterpret_cast<uintptr_t>(turns) % 8 != 0 ||
+                  reinterpret_cast<uintptr_t>(axes) % 4 != 0))
+        return QL_ERR_ALIGNMENT;
+    if (reinterpret_cast<uintptr_t>(segment_ids) % 4 != 0) return QL_ERR_ALIGNMENT;
+    for (const ql_heads* o : set) {
+        if (!o) continue;
+        const size_t n = static_cast<size_t>(heads_span(o->out_token, o->out_head, M, o->heads, D)) * size;
+        if (P > 0 && (overlap(o->out, n, positions, static_cast<size_t>(A) * M * pos_size) ||
+                      overlap(o->out, n, turns, static_cast<size_t>(P) * 8) ||
+                      overlap(o->out, n, axes, static_cast<size_t>(P) * 4)))
+            return QL_ERR_INVALID_ARG;
+        if (segment_ids && overlap(o->out, n, segment_ids, static_cast<size_t>(M) * 4)) return QL_ERR_INVALID_ARG;
+        for (const ql_heads* i : set) {
+            if (!i) continue;
+            if (i->weight && overlap(o->out, n, i->weight, static_cast<size_t>(D) * (weight_dtype == QL_BF16 ? 2 : 4)))
+                return QL_ERR_INVALID_ARG;
+            const bool in_place = i == o && i->in == i->out && (M == 1 || i->in_token == i->out_token) &&
+                                  (i->heads == 1 || i->in_head == i->out_head);
+            if (!in_place && heads_overlap(i->in, i->in_token, i->in_head, i->heads, o->out, o->out_token, o->out_head,
+                                           o->heads, M, D, size))
+                return QL_ERR_INVALID_ARG;
+        }
+    }
+    if (q && k && heads_overlap(q->out, q->out_token, q->out_head, q->heads, k->out, k->out_token, k->out_head, k->heads,
+                                M, D, size))
+        return QL_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    if ((s = device_info(&dev)) != QL_OK) return s;
+    rotary::Params p = {};
+    for (int i = 0; i < 2; ++i)
+        if (set[i])
+            p.set[i] = {set[i]->in, set[i]->out, set[i]->in_token, set[i]->in_head, set[i]->out_token, set[i]->out_head,
+                        set[i]->weight, set[i]->heads};
+    p.pos = positions;
+    p.turns = turns;
+    p.axes = axes;
+    p.seg = segment_ids;
+    p.M = M;
+    p.D = static_cast<int>(D);
+    p.P = P;
+    p.A = A;
+    p.pos_type = pos_type;
+    p.norm = norm_on != 0;
+    p.weight_f32 = weight_dtype == QL_F32;
+    p.eps = eps;
+    p.inv_d = 1.0f / static_cast<float>(D);
+    const int slots = static_cast<int>((D + 15) / 16);
+    const int G = slots <= 4 ? 4 : slots <= 8 ? 8 : slots <= 16 ? 16 : 32;
+    const int per = 32 / G;
+    const int groups = (p.set[0].heads + per - 1) / per + (p.set[1].heads + per - 1) / per;
+    // a warp per token; few tokens share their heads among up to 32 warps per SM
+    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(groups, 32ll * dev->sm_count / M)));
+    const int64_t units = M * p.parts;
+    if ((units + rotary::kWarps - 1) / rotary::kWarps > (1ll << 31) - 1) return QL_ERR_UNSUPPORTED;
+    if (dtype == QL_F32)
+        return adjacent ? launch_heads<true, true>(p, G, units, stream) : launch_heads<true, false>(p, G, units, stream);
+    return adjacent ? launch_heads<false, true>(p, G, units, stream) : launch_heads<false, false>(p, G, units, stream);
+}
+
+EpilogueArgs epilogue_args(const void* bias, int32_t activation, const void* gate, ql_dtype param_dtype,
+                           const void* residual, const int32_t* segment_ids, int32_t T) {
+    EpilogueArgs a;
+    a.e.bias = bias;
+    a.e.gate = gate;
+    a.e.residual = residual;
+    a.e.seg = segment_ids;
+    a.e.T = T;
+    a.e.act = activation;
+    a.e.params_f32 = param_dtype == QL_F32;
+    return a;
+}
+
+size_t epilogue_workspace_impl(int64_t M, int64_t K, int64_t N, int32_t group, int bits) {
+    size_t n = workspace_impl(M, K, N, group, QL_PATH_AUTO, 0, bits);
+    if (n != static_cast<size_t>(-1) && M > 64) n += static_cast<size_t>(M) * N * 4;
+    return n;
+}
+
 }  // namespace
 }  // namespace ql
 
@@ -1526,6 +1722,51 @@ ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const void* y, 
                                 void* h, int64_t M, int64_t D, cudaStream_t stream) {
     return norm_residual_impl(x, x_dtype, y, y_dtype, S, post_norm, post_weight, gate, residual_scale, branch_scale,
                               pre_weight, scale, shift, param_dtype, segment_ids, T, eps, out, h, M, D, stream);
+}
+
+size_t qlinear_epilogue_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group) {
+    return epilogue_workspace_impl(M, K, N, group, 4);
+}
+
+ql_status qlinear_epilogue_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
+                                   const void* bias, int32_t activation, const void* gate, ql_dtype param_dtype,
+                                   const void* residual, const int32_t* segment_ids, int32_t T, void* y,
+                                   ql_dtype out_dtype, int64_t M, int64_t K, int64_t N, int32_t group, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream) {
+    if (!dtype_ok(param_dtype)) return QL_ERR_INVALID_ARG;
+    const EpilogueArgs ep = epilogue_args(bias, activation, gate, param_dtype, residual, segment_ids, T);
+    return forward_impl(x, codes, scales, biases, y, out_dtype, M, K, N, group, QL_PATH_AUTO, 0, workspace,
+                        workspace_bytes, stream, 4, nullptr, &ep);
+}
+
+size_t qlinear8_epilogue_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group) {
+    return epilogue_workspace_impl(M, K, N, group, 8);
+}
+
+ql_status qlinear8_epilogue_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
+                                    const void* bias, int32_t activation, const void* gate, ql_dtype param_dtype,
+                                    const void* residual, const int32_t* segment_ids, int32_t T, void* y,
+                                    ql_dtype out_dtype, int64_t M, int64_t K, int64_t N, int32_t group, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+    if (!dtype_ok(param_dtype)) return QL_ERR_INVALID_ARG;
+    const EpilogueArgs ep = epilogue_args(bias, activation, gate, param_dtype, residual, segment_ids, T);
+    return forward_impl(x, codes, scales, biases, y, out_dtype, M, K, N, group, QL_PATH_AUTO, 0, workspace,
+                        workspace_bytes, stream, 8, nullptr, &ep);
+}
+
+ql_status qlinear_rotary_axes(const ql_heads* x, ql_dtype dtype, const void* positions, ql_pos_type pos_type, int32_t A,
+                              const double* turns, const int32_t* axes, int32_t P, int32_t adjacent,
+                              const int32_t* segment_ids, int64_t M, int64_t D, cudaStream_t stream) {
+    return heads_impl(x, nullptr, dtype, 0, QL_F32, 0.0f, positions, pos_type, A, turns, axes, P, adjacent, segment_ids,
+                      M, D, stream);
+}
+
+ql_status qlinear_qk_norm_rotary(const ql_heads* q, const ql_heads* k, ql_dtype dtype, ql_dtype weight_dtype, float eps,
+                                 const void* positions, ql_pos_type pos_type, int32_t A, const double* turns,
+                                 const int32_t* axes, int32_t P, int32_t adjacent, const int32_t* segment_ids, int64_t M,
+                                 int64_t D, cudaStream_t stream) {
+    return heads_impl(q, k, dtype, 1, weight_dtype, eps, positions, pos_type, A, turns, axes, P, adjacent, segment_ids, M,
+                      D, stream);
 }
 
 size_t qlinear_swiglu_workspace_size(int64_t M, int64_t K, int64_t I, int32_t group) {

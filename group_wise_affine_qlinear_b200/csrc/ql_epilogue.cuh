@@ -1,0 +1,155 @@
+// What follows a packed projection, in its epilogue:
+//
+//   z = x . W^T + bias[n]
+//   a = act(z)                            none, silu, gelu or its tanh form
+//   y = residual + gate[seg[m]][n] * a    fp32 from the accumulator on, rounded once
+//
+// A row whose segment is negative is padding: its row of y is left as it was.
+#pragma once
+
+#include "ql_ptx.cuh"
+#include "ql_tc_skinny.cuh"
+
+namespace ql {
+namespace epi {
+
+struct Epilogue {
+    const void* bias;        // [N] or null (0)
+    const void* gate;        // [T][N] or null (1)
+    const void* residual;    // [M][N] of y's type, may be y, or null (0)
+    const int* seg;          // [M] or null (segment 0)
+    int T;
+    int act;                 // ql_activation
+    int params_f32;          // type of bias and gate: 0 bf16, 1 fp32
+};
+
+// The hardware's exponential and division err by a few fp32 units, the weights' rounding to f16 by 2^-12: of no
+// consequence.  All three give z (or z - 0) for large z, and -0 where e^-z overflows.
+__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+// z Phi(z) with 1 - erf from Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26 (absolute error below
+// 1.5e-7): where the library's erff takes some forty instructions and a branch, this takes a dozen.
+__device__ __forceinline__ float gelu(float z) {
+    const float a = fabsf(z) * 0.70710678f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, a, 1.0f));
+    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                                0.254829592f);
+    const float tail = 0.5f * poly * __expf(-a * a);       // 1 - Phi(|z|)
+    return z >= 0.0f ? z - fminf(z, 1e4f) * tail : z * tail;   // (an infinite z times a zero tail would be NaN)
+}
+
+// 0.5 z (1 + tanh(u)) = z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float gelu_tanh(float z) {
+    const float u2 = 1.59576912f * fmaf(0.044715f * z * z, z, z);
+    return __fdividef(z, 1.0f + __expf(-u2));
+}
+
+__device__ __forceinline__ float activate(int act, float z) {
+    switch (act) {
+        case QL_ACT_SILU: return silu(z);
+        case QL_ACT_GELU: return gelu(z);
+        case QL_ACT_GELU_TANH: return gelu_tanh(z);
+        default: return z;
+    }
+}
+
+// Segment of row m, -1 for a row to leave alone.
+__device__ __forceinline__ int segment_of(const Epilogue& e, int64_t m) {
+    if (e.seg == nullptr) return 0;
+    const int s = __ldg(e.seg + m);
+    if (s >= e.T) {
+        record_status(QL_ERR_INVALID_ARG);
+        return -1;
+    }
+    return s < 0 ? -1 : s;
+}
+
+__device__ __forceinline__ float param(const void* p, int f32, int64_t i) {
+    return f32 ? __ldg(static_cast<const float*>(p) + i)
+               : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + i));
+}
+__device__ __forceinline__ float4 bf16x4(uint2 v) {
+    return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+}
+__device__ __forceinline__ float4 param4(const void* p, int f32, int64_t i) {
+    return f32 ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i))
+               : bf16x4(__ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i)));
+}
+
+// y = epilogue of the fp32 partials [S][M][N], summed in slice order: four columns per thread, whose bias (and gate,
+// while the segment stays the same) it holds over its rows.
+template <bool kBf16Out>
+__global__ void __launch_bounds__(256) epilogue_sum_kernel(const float* __restrict__ partial, void* y, int64_t M, int N,
+                                                           int S, const Epilogue e) {
+    const int n = 4 * static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
+    ptx::grid_dependency_wait();                       // the partials come from the kernel before
+    if (n >= N) return;
+    const float4 bias = e.bias ? param4(e.bias, e.params_f32, n) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 gate = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    int held = -1;
+    for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+        const int seg = segment_of(e, m);
+        if (seg < 0) continue;
+        if (e.gate != nullptr && seg != held) gate = param4(e.gate, e.params_f32, static_cast<int64_t>(seg) * N + n);
+        held = seg;
+        const int64_t at = m * N + n;
+        float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (e.residual != nullptr)
+            r = kBf16Out ? bf16x4(*reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.residual) + at))
+                         : *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + at);
+        float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int s = 0; s < S; ++s) {
+            const float4 v = *reinterpret_cast<const float4*>(partial + s * M * N + at);
+            z = make_float4(z.x + v.x, z.y + v.y, z.z + v.z, z.w + v.w);
+        }
+        const float4 o = make_float4(fmaf(gate.x, activate(e.act, z.x + bias.x), r.x),
+                                     fmaf(gate.y, activate(e.act, z.y + bias.y), r.y),
+                                     fmaf(gate.z, activate(e.act, z.z + bias.z), r.z),
+                                     fmaf(gate.w, activate(e.act, z.w + bias.w), r.w));
+        if constexpr (kBf16Out)
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(y) + at) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        else
+            *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = o;
+    }
+}
+
+// The weight-streaming path's reduce kernel (skinny_reduce_kernel) with the epilogue.  What the caller gave is loaded
+// before the wait for the partials.
+template <bool kBf16Out>
+__global__ void __launch_bounds__(256) epilogue_reduce_kernel(const float* __restrict__ partial,
+                                                              const int* __restrict__ rowexp, void* y, int M, int N,
+                                                              int cpt, int64_t units, int P, int segmax,
+                                                              int64_t partial_elems, const Epilogue e) {
+    __shared__ int64_t seg_base[skinny::kMaxCtas];
+    __shared__ int count;
+    const int w = blockIdx.x;
+    const int t = blockIdx.y * 2 + (threadIdx.x >> 7), r = threadIdx.x & 127;
+    const int n = w * skinny::BW + r;
+    const bool inside = t < M && n < N;
+    const int64_t at = static_cast<int64_t>(t) * N + n;
+    int seg = -1;
+    float bias = 0.0f, gate = 1.0f, res = 0.0f;
+    if (inside) {
+        seg = segment_of(e, t);
+        if (e.bias != nullptr) bias = param(e.bias, e.params_f32, n);
+        if (e.residual != nullptr)
+            res = kBf16Out ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at])
+                           : static_cast<const float*>(e.residual)[at];
+        if (e.gate != nullptr && seg >= 0) gate = param(e.gate, e.params_f32, static_cast<int64_t>(seg) * N + n);
+    }
+    if (threadIdx.x == 0) count = skinny::list_segments(w, cpt, units, P, segmax, seg_base);
+    ptx::grid_dependency_wait();                       // partials come from the kernel before
+    __syncthreads();
+    if (!inside || seg < 0) return;
+    float z = skinny::sum_segments(partial, partial_elems, seg_base, count, M, t, r);
+    z = ldexpf(z, rowexp[t]) + bias;
+    const float o = fmaf(gate, activate(e.act, z), res);
+    if constexpr (kBf16Out)
+        static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(o);
+    else
+        static_cast<float*>(y)[at] = o;
+}
+
+}  // namespace epi
+}  // namespace ql

@@ -425,6 +425,88 @@ QL_API ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const vo
                                        int64_t M, int64_t D, cudaStream_t stream);
 
 /*
+ * A packed projection with bias, activation, gate and residual in its epilogue:
+ *   z[m][n] = sum_k x[m][k] * W[n][k] + bias[n]
+ *   y[m][n] = residual[m][n] + gate[seg][n] * act(z[m][n]),   seg = segment_ids[m]
+ * x, codes, scales, biases and the arithmetic of the packed product as in qlinear_forward; everything behind it in
+ * fp32, y rounded once.
+ *
+ *   bias          [N] of param_dtype (QL_BF16 or QL_F32); NULL: 0
+ *   activation    a ql_activation: z; silu z / (1 + e^-z); gelu z Phi(z); its tanh form
+ *                 z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))
+ *   gate          [T][N] of param_dtype; NULL: 1
+ *   residual      [M][N] of out_dtype; may be y (the update in place; other overlaps are refused); NULL: 0
+ *   segment_ids   int32 [M] on the device; NULL: segment 0 for every row.  A row with a negative segment is padding: its
+ *                 row of y is left as it was.  A row with a segment >= T is left alone too, and the device status word
+ *                 records QL_ERR_INVALID_ARG.
+ *   y             [M][N] of out_dtype (QL_BF16 or QL_F32)
+ *
+ * Preconditions and errors as in qlinear_forward, and T >= 1, a known activation and types (else QL_ERR_INVALID_ARG);
+ * bias, gate and residual 16-byte, segment_ids 4-byte aligned; y and the workspace overlap none of them (but y the
+ * residual, as said).  `workspace` holds qlinear_epilogue_workspace_size(M, K, N, group) bytes.
+ */
+typedef enum { QL_ACT_NONE = 0, QL_ACT_SILU = 1, QL_ACT_GELU = 2, QL_ACT_GELU_TANH = 3 } ql_activation;
+QL_API size_t qlinear_epilogue_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group);
+QL_API ql_status qlinear_epilogue_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
+                                          const void* bias, int32_t activation, const void* gate, ql_dtype param_dtype,
+                                          const void* residual, const int32_t* segment_ids, int32_t T, void* y,
+                                          ql_dtype out_dtype, int64_t M, int64_t K, int64_t N, int32_t group,
+                                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* The same with 8-bit codes (uint32 [N][K/4], as qlinear8_forward). */
+QL_API size_t qlinear8_epilogue_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group);
+QL_API ql_status qlinear8_epilogue_forward(const void* x, const uint32_t* codes, const void* scales, const void* biases,
+                                           const void* bias, int32_t activation, const void* gate, ql_dtype param_dtype,
+                                           const void* residual, const int32_t* segment_ids, int32_t T, void* y,
+                                           ql_dtype out_dtype, int64_t M, int64_t K, int64_t N, int32_t group,
+                                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Rotation of heads by positions of several axes (time, height, width, as in the DiT's rotary embedding: jimmysue
+ * "Ideogram 4" notes, MRoPE), alone or in the same pass as the norms of queries and keys head by head:
+ *   n[m][h][d] = x[m][h][d] / sqrt(mean_d x[m][h][d]^2 + eps) * weight[d]       (qlinear_qk_norm_rotary)
+ *   the first 2 P elements of every head are P pairs (a, b): elements i and i + P, or 2 i and 2 i + 1 (adjacent != 0);
+ *   pair i turns by the angle 2 pi turns[i] positions[axes[i]][m]:  (a, b) <- (a cos - b sin, b cos + a sin)
+ * All of it in fp32 but the angle, whose whole turns are dropped in 64 bits; outputs are rounded once.
+ *
+ * A ql_heads names one tensor of heads, [M][heads][D] with a stride per token and per head (in elements; a head's D
+ * elements lie side by side), e.g. the queries or the keys inside a packed QKV projection's output, or one kept head
+ * by head:
+ *   in, in_token, in_head      what is read
+ *   out, out_token, out_head   what is written: `in` itself with the same strides (in place), or memory that meets no
+ *                              input.  No two elements of it may share a place.
+ *   weight                     [D] of weight_dtype; NULL: 1 (NULL without norms)
+ * The queries and the keys may have different numbers of heads and lie in one buffer.
+ *
+ *   dtype          QL_BF16 or QL_F32, of every tensor of heads
+ *   positions      [A][M] of pos_type on the device: one row per axis.  NULL (with P == 0): norms without rotation
+ *   turns          double [P] on the device: pair i's turns per unit of position, its frequency / 2 pi
+ *   axes           int32 [P] on the device: the axis whose position pair i takes.  A pair with an axis outside [0, A) is
+ *                  not turned, and the device status word records QL_ERR_INVALID_ARG.
+ *   segment_ids    int32 [M] on the device or NULL: a row with a negative one is padding, it is not read and its heads of
+ *                  `out` are left as they were
+ *
+ * Required (QL_ERR_INVALID_ARG): M >= 1, D >= 8, D % 8 == 0, heads >= 1, 0 <= 2 P <= D, eps >= 0 and finite,
+ * A <= QL_HEAD_MAX_D, strides from 0 to 2^56 / max(M, heads).  P % 8 == 0 and D <= QL_HEAD_MAX_D (QL_ERR_UNSUPPORTED otherwise).  Heads, weights and strides 16-byte
+ * aligned, the rest by their element.  k may be NULL (queries alone).  No workspace.
+ */
+#define QL_HEAD_MAX_D 512
+typedef enum { QL_POS_I32 = 0, QL_POS_I64 = 1, QL_POS_F32 = 2 } ql_pos_type;
+typedef struct {
+    const void* in;
+    void* out;
+    int64_t in_token, in_head, out_token, out_head;
+    const void* weight;
+    int32_t heads;
+} ql_heads;
+QL_API ql_status qlinear_rotary_axes(const ql_heads* x, ql_dtype dtype, const void* positions, ql_pos_type pos_type,
+                                     int32_t A, const double* turns, const int32_t* axes, int32_t P, int32_t adjacent,
+                                     const int32_t* segment_ids, int64_t M, int64_t D, cudaStream_t stream);
+QL_API ql_status qlinear_qk_norm_rotary(const ql_heads* q, const ql_heads* k, ql_dtype dtype, ql_dtype weight_dtype,
+                                        float eps, const void* positions, ql_pos_type pos_type, int32_t A,
+                                        const double* turns, const int32_t* axes, int32_t P, int32_t adjacent,
+                                        const int32_t* segment_ids, int64_t M, int64_t D, cudaStream_t stream);
+
+/*
  * Self-test of the bounded waits inside the library's kernels.  Enqueues one small kernel that waits
  * on a barrier nothing ever completes, with the same bounded wait every pipeline role uses: it gives
  * up after the library's wait limit (about one second), records QL_ERR_DEVICE_TIMEOUT in the device

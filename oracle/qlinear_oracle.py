@@ -71,6 +71,8 @@ from __future__ import annotations
 
 import struct
 
+import math
+
 import numpy as np
 
 GROUP = 64
@@ -665,3 +667,52 @@ def norm_residual_ref(x, y=None, post_norm=True, post_weight=None, gate=None, re
     if shift is not None:
         h = h + np.asarray(shift)[seg]
     return r, h
+
+
+# ---------------------------------------------------------------- epilogues, norms and rotation of heads
+
+def erf_cdf(z) -> np.ndarray:
+    """Phi(z), the normal distribution function, through the C library's erfc."""
+    return np.vectorize(lambda v: 0.5 * math.erfc(-v / math.sqrt(2.0)), otypes=[np.float64])(np.asarray(z, np.float64))
+
+
+def activation(z, kind) -> np.ndarray:
+    """act(z) in float64: None, "silu", "gelu" or "gelu_tanh"."""
+    z = np.asarray(z, np.float64)
+    if kind is None:
+        return z
+    if kind == "silu":
+        return silu(z)
+    if kind == "gelu":
+        return z * erf_cdf(z)
+    if kind == "gelu_tanh":
+        return 0.5 * z * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)))
+    raise ValueError(kind)
+
+
+def epilogue_ref(lin, bias=None, act=None, gate=None, residual=None, seg=None) -> np.ndarray:
+    """residual + gate[seg] * act(lin + bias) in float64; rows of a negative segment come out as NaN."""
+    z = np.asarray(lin, np.float64) + (0.0 if bias is None else np.asarray(bias, np.float64)[None, :])
+    seg = np.zeros(z.shape[0], np.int64) if seg is None else np.asarray(seg, np.int64)
+    y = activation(z, act)
+    if gate is not None:
+        y = y * np.asarray(gate, np.float64)[np.maximum(seg, 0)]
+    if residual is not None:
+        y = y + np.asarray(residual, np.float64)
+    y[seg < 0] = np.nan
+    return y
+
+
+def rotary_ref(x, positions, turns, axes, adjacent: bool = False) -> np.ndarray:
+    """Heads x [M][H][D] turned in float64: pair i by 2 pi turns[i] positions[axes[i]][m]."""
+    x = np.asarray(x, np.float64)
+    turns, axes = np.asarray(turns, np.float64), np.asarray(axes, np.int64)
+    P = len(turns)
+    t = np.asarray(positions, np.float64)[axes].T * turns[None, :]
+    angle = 2.0 * math.pi * (t - np.rint(t))
+    c, s = np.cos(angle)[:, None, :], np.sin(angle)[:, None, :]
+    ia, ib = (np.arange(P) * 2, np.arange(P) * 2 + 1) if adjacent else (np.arange(P), np.arange(P) + P)
+    out = x.copy()
+    out[:, :, ia] = x[:, :, ia] * c - x[:, :, ib] * s
+    out[:, :, ib] = x[:, :, ib] * c + x[:, :, ia] * s
+    return out

@@ -106,6 +106,17 @@ cudaError_t fused_smem_attr() {
     return e;
 }
 
+template <int B>
+cudaError_t epilogue_smem_attr() {
+    using EB = typename fused::PickEpiCfg<B, true>::type;
+    using EF = typename fused::PickEpiCfg<B, false>::type;
+    const cudaError_t e = cudaFuncSetAttribute(fused::fused_gemm_kernel<true, EB, false, false, false, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, EB::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(fused::fused_gemm_kernel<false, EF, false, false, false, true>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, EF::kSmemBytes);
+}
+
 template <int NT>
 cudaError_t prepare_smem_attr() {
     return cudaFuncSetAttribute(lora::lora_prepare_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -129,6 +140,7 @@ ql_status device_info(DeviceInfo** out) {
         if (fused_smem_attr<4>() != cudaSuccess || fused_smem_attr<8>() != cudaSuccess ||
             fused_smem_attr<4, true>() != cudaSuccess || fused_smem_attr<4, false, true>() != cudaSuccess ||
             fused_smem_attr<8, false, true>() != cudaSuccess || fused_smem_attr<4, true, true>() != cudaSuccess ||
+            epilogue_smem_attr<4>() != cudaSuccess || epilogue_smem_attr<8>() != cudaSuccess ||
             prepare_smem_attr<1>() != cudaSuccess || prepare_smem_attr<2>() != cudaSuccess ||
             prepare_smem_attr<4>() != cudaSuccess)
             return QL_ERR_CUDA;
@@ -590,6 +602,29 @@ ql_status launch_fused(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const 
                             FC::kSmemBytes, st, mx, mc, mc2, mp, my, static_cast<const fused::Params&>(p));
 }
 
+// The fused kernel in epilogue mode.
+template <int B>
+ql_status launch_epilogue(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& mc, const CUtensorMap& mp,
+                          const CUtensorMap& my, const fused::Params& base, const epi::Epilogue& e, bool bf16_out, int64_t M,
+                          int64_t N) {
+    fused::EpiParams p;
+    static_cast<fused::Params&>(p) = base;
+    p.e = e;
+    p.map_res = my;
+    ql_status s;
+    if (e.residual &&
+        (s = encode_2d(&p.map_res, bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, e.residual,
+                       N, M, N * (bf16_out ? 2 : 4), 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK)
+        return s;
+    using EB = typename fused::PickEpiCfg<B, true>::type;
+    using EF = typename fused::PickEpiCfg<B, false>::type;
+    if (bf16_out)
+        return launch_dependent(fused::fused_gemm_kernel<true, EB, false, false, false, true>, grid, fused::kThreads,
+                                EB::kSmemBytes, st, mx, mc, mc, mp, my, p);
+    return launch_dependent(fused::fused_gemm_kernel<false, EF, false, false, false, true>, grid, fused::kThreads,
+                            EF::kSmemBytes, st, mx, mc, mc, mp, my, p);
+}
+
 ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
                     void* y, bool bf16_out, int64_t M, int64_t K, int64_t N, void* ws, cudaStream_t st,
                     int sm_count, const LoraArgs* la = nullptr, const LoraPlan* lp = nullptr,
@@ -616,7 +651,7 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
                        CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK)
         return s;
     CUtensorMap my;
-    const bool split = pl.split_k > 1 || ep != nullptr;
+    const bool split = pl.split_k > 1;
     float* part = reinterpret_cast<float*>(base + pl.off_part);
     if (split) {
         // fp32 partials [split_k][M][N]: 32 x 32 blocks, clipped at M and N within every slice
@@ -676,6 +711,17 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
         set_dispatch("path=tc_fused%s bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=%d launches=%d why=%s",
                      la ? "_lora" : ep ? "_epilogue" : "", bits, fused::BW, fused::BT, fused::BK, nx, nc, cfg_steps, fused::NA, grid,
                      pl.split_k, 4, pl.why);
+        return launch_status();
+    }
+    if (ep) {
+        s = bits == 4 ? launch_epilogue<4>(fgrid, st, mx, mc, mp, my, p, *ep, bf16_out, M, N)
+                      : launch_epilogue<8>(fgrid, st, mx, mc, mp, my, p, *ep, bf16_out, M, N);
+        if (s != QL_OK) return s;
+        prof_end(st);
+        set_dispatch("path=tc_fused_epilogue bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=1 launches=3 why=%s",
+                     bits, fused::BW, fused::BT, fused::BK,
+                     bf16_out ? fused::PickEpiCfg<4, true>::type::kNX : fused::PickEpiCfg<4, false>::type::kNX,
+                     fused::PickEpiCfg<4, true>::type::kNC, cfg_steps, fused::NA, grid, pl.why);
         return launch_status();
     }
     using B4 = fused::PickCfg<4, true>::type;
@@ -1134,7 +1180,6 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
         lp = lora_plan(pl, M, K, la->r, la->L, dev->sm_count);
         need = lp.workspace;
     }
-    if (ep && pl.path == QL_PATH_TC_FUSED && pl.split_k == 1) need += static_cast<size_t>(M) * N * 4;
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return QL_ERR_WORKSPACE;
         if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
@@ -1546,9 +1591,7 @@ EpilogueArgs epilogue_args(const void* bias, int32_t activation, const void* gat
 }
 
 size_t epilogue_workspace_impl(int64_t M, int64_t K, int64_t N, int32_t group, int bits) {
-    size_t n = workspace_impl(M, K, N, group, QL_PATH_AUTO, 0, bits);
-    if (n != static_cast<size_t>(-1) && M > 64) n += static_cast<size_t>(M) * N * 4;
-    return n;
+    return workspace_impl(M, K, N, group, QL_PATH_AUTO, 0, bits);
 }
 
 }  // namespace

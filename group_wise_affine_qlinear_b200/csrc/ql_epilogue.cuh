@@ -44,6 +44,10 @@ __device__ __forceinline__ float gelu_tanh(float z) {
     return __fdividef(z, 1.0f + __expf(-u2));
 }
 
+template <int kAct>
+__device__ __forceinline__ float activate_as(float z) {
+    return kAct == QL_ACT_SILU ? silu(z) : kAct == QL_ACT_GELU ? gelu(z) : kAct == QL_ACT_GELU_TANH ? gelu_tanh(z) : z;
+}
 __device__ __forceinline__ float activate(int act, float z) {
     switch (act) {
         case QL_ACT_SILU: return silu(z);

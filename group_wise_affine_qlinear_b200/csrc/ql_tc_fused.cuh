@@ -71,10 +71,16 @@
 // token's row is zero outside its own adapter's parts.  So a tile pays for the adapters in it (one step per 32 / r of them),
 // nothing travels through memory a second time, and y is rounded once.  B comes by TMA through the code ring (a code
 // stage per extra step), t by TMA too, eight rows at a time, but for the eights that meet several adapters.
+//
+// Epilogue mode (kEpi): y = residual + gate[seg] * act(acc + bias), on the accumulator's way out.  A block of the
+// residual (32 tokens x 32 columns, a chunk's) comes by TMA into the staging block that the chunk's outputs then take its
+// place in, one chunk ahead; a lane's bias and gate are one value each per group.  Three staging blocks per warp (one
+// stored from, one worked on, one filled) take the room of an activation stage.
 #pragma once
 
 #include "ql_ptx.cuh"
 #include "ql_dequant_f16.cuh"
+#include "ql_epilogue.cuh"
 
 namespace ql {
 namespace fused {
@@ -140,6 +146,18 @@ template <> struct PickCfg<4, false> { using type = Cfg<4, 2, 4, 4, 1>; };
 template <> struct PickCfg<8, true> { using type = Cfg<5, 2, 8, 2, 2>; };
 template <> struct PickCfg<8, false> { using type = Cfg<4, 2, 8, 4, 1>; };
 
+// Epilogue mode: a barrier per staging block behind the others.
+template <class Base>
+struct EpiCfg : Base {
+    static constexpr uint32_t kOffRes = Base::kOffMisc + 16;
+    static constexpr uint32_t kSmemBytes = Base::kSmemBytes + kEpiWarps * Base::kNB * 8;
+    static_assert(Base::kNB >= 2 && kOffRes % 8 == 0 && kSmemBytes <= 232448, "staging and shared memory budget");
+};
+template <int B, bool kBf16Out>
+struct PickEpiCfg;
+template <int B> struct PickEpiCfg<B, true> { using type = EpiCfg<Cfg<4, 2, B, 2, 3>>; };
+template <int B> struct PickEpiCfg<B, false> { using type = EpiCfg<Cfg<3, 2, B, 4, 2>>; };
+
 struct Params {
     float* rowscale;      // [M] 2^e_m
     void* y;              // [M][N] bf16 or fp32
@@ -161,8 +179,13 @@ struct LoraParams : Params {
 };
 // Columns of a box of B: an extra step needs at most four parts of an adapter.
 __host__ __device__ constexpr int part_cols(int r8) { return r8 < 4 ? 8 * r8 : 32; }
-template <bool kLora> struct PickParams { using type = Params; };
-template <> struct PickParams<true> { using type = LoraParams; };
+struct EpiParams : Params {
+    epi::Epilogue e;
+    CUtensorMap map_res;         // the residual as [M][N] of y's type, boxes of 32 x 32
+};
+template <bool kLora, bool kEpi> struct PickParams { using type = Params; };
+template <> struct PickParams<true, false> { using type = LoraParams; };
+template <> struct PickParams<false, true> { using type = EpiParams; };
 
 __device__ __forceinline__ void tile_coords(int t, int num_w, int& t_blk, int& w_blk) {
     // weight tiles fastest: a wave of CTAs shares one or two activation row blocks
@@ -191,14 +214,15 @@ __device__ __forceinline__ uint32_t bf16_part(float v0, float v1, bool lo) {
 // kSplitK: every tile's K-steps are cut into p.splits slices, each its own work unit; a unit writes the
 // fp32 partial of its slice through map_y, a 3-D map over partials [splits][M][N], and a separate
 // reduction sums the slices in order (for shapes with fewer tiles than SMs).
-template <bool kBf16Out, class C, bool kSwiGLU = false, bool kSplitK = false, bool kLora = false>
+template <bool kBf16Out, class C, bool kSwiGLU = false, bool kSplitK = false, bool kLora = false, bool kEpi = false>
 __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_codes,
     const __grid_constant__ CUtensorMap map_codes2, const __grid_constant__ CUtensorMap map_params,
-    const __grid_constant__ CUtensorMap map_y, const __grid_constant__ typename PickParams<kLora>::type p) {
+    const __grid_constant__ CUtensorMap map_y, const __grid_constant__ typename PickParams<kLora, kEpi>::type p) {
     constexpr int NX = C::kNX, NC = C::kNC;
     static_assert(!kSwiGLU || C::kBits == 4, "the SwiGLU pair is built for 4-bit codes");
     static_assert(!kSplitK || (!kSwiGLU && !kBf16Out), "split-K units write fp32 partials of a plain layer");
+    static_assert(!kEpi || (!kSwiGLU && !kSplitK && !kLora), "the epilogue mode is a plain layer's");
     static_assert(kBf16Out == (C::kOutBytes == 2), "the staging blocks are sized for the output type");
     constexpr int kCodeWords = BK * C::kBits / 32;      // 32-bit code words of one row per K-step
     extern __shared__ uint8_t smem_raw[];
@@ -259,6 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
         // an accumulator is drained by all 8 epilogue warps (a lane quarter and half of the tokens each)
         for (int g = 0; g < NG; ++g) ptx::mbar_init(&acc_empty[g], kEpiWarps);
         for (int g = 0; g < NG; ++g) ptx::mbar_init(drain + g, 1);
+        if constexpr (kEpi) {
+            for (int i = 0; i < kEpiWarps * C::kNB; ++i) ptx::mbar_init(reinterpret_cast<uint64_t*>(smem + C::kOffRes) + i, 1);
+        }
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -776,6 +803,165 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
             }
         }
         if (lane == 0) ptx::bulk_wait_group_all();   // every store has completed before the CTA exits
+    } else if (kEpi && warp >= kWarpEpi0) {
+        // ---------------------------------------------------------------- epilogue with bias, activation, gate, residual
+        test_delay(kDelayEpilogue);   // the checked build can hold this role back (qlinear_test_delay)
+        if constexpr (kEpi) {
+            // As below: warp (quarter, half) drains its lanes of group 0, then of group 1, chunks of 32 tokens.  Its
+            // chunks are numbered q over all tiles; chunk q uses staging block q % kNB, the block's barrier its use q / kNB.
+            constexpr int kHalf = BT / 32 / 2, NB = C::kNB;
+            const int quarter = warp & 3;
+            const int half = (warp - kWarpEpi0) >> 2;
+            uint8_t* epi_stage = smem + C::kOffEpi + (warp - kWarpEpi0) * NB * C::kStageBytes;
+            uint64_t* res_full = reinterpret_cast<uint64_t*>(smem + C::kOffRes) + (warp - kWarpEpi0) * NB;
+            const bool has_res = p.e.residual != nullptr;
+            const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+            uint32_t q = 0, asked = 0;                 // chunks done; residual blocks asked for
+            const auto ask = [&](int x, int y) {       // lane 0: the residual block of the next chunk
+                const uint32_t b = asked++ % NB;
+                ptx::mbar_arrive_expect_tx(&res_full[b], C::kStageBytes);
+                ptx::tma_load_2d(epi_stage + b * C::kStageBytes, &p.map_res, &res_full[b], x, y);
+            };
+            const auto ask_tile = [&](int t) {
+                if (t >= num_tiles) return;
+                int t_blk, w_blk;
+                tile_coords(t, p.num_w, t_blk, w_blk);
+                ask(w_blk * BW + quarter * 32, t_blk * BT + 32 * kHalf * half);
+            };
+            ptx::grid_dependency_wait();               // the row scales come from the kernels before this one
+            if (has_res && lane == 0) ask_tile(blockIdx.x);
+            bool ok = true;
+            int j = 0;
+            for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++j) {
+                int t_blk, w_blk;
+                tile_coords(t, p.num_w, t_blk, w_blk);
+                const int m0 = t_blk * BT + 32 * kHalf * half;         // this warp's first token
+                // row scale and segment of token m0 + 32 c + lane, fetched a chunk ahead
+                float rs_next;
+                int seg_next;
+                const auto fetch_row = [&](int m) {
+                    rs_next = m < p.M ? p.rowscale[m] : 0.0f;
+                    seg_next = m < p.M ? epi::segment_of(p.e, m) : -2;
+                };
+                fetch_row(m0 + lane);
+                const int n_first = w_blk * BW + quarter * 32 + lane;  // this lane's column of group 0
+                int held = max(__shfl_sync(0xFFFFFFFFu, seg_next, 0), 0);
+                float bias[NG], gate[NG];
+                const auto load_gate = [&] {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const int n = n_first + g * BWG;
+                        gate[g] = p.e.gate != nullptr && n < p.N
+                                      ? epi::param(p.e.gate, p.e.params_f32, static_cast<int64_t>(held) * p.N + n) : 1.0f;
+                    }
+                };
+                load_gate();
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int n = n_first + g * BWG;
+                    bias[g] = p.e.bias != nullptr && n < p.N ? epi::param(p.e.bias, p.e.params_f32, n) : 0.0f;
+                }
+                if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&acc_full[0], j & 1, abort_flag))) break;
+                ptx::tc_fence_after_sync();
+#pragma unroll 1
+                for (int i = 0; i < NG * kHalf; ++i, ++q) {
+                    const int g = i / kHalf, c = i - g * kHalf;
+                    const int n_base = w_blk * BW + g * BWG + quarter * 32, m_base = m0 + 32 * c;
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(tmem_base + kAccCol + static_cast<uint32_t>(g * BT + 32 * (kHalf * half + c)) + lane_addr, v);
+                    const float rs = rs_next;
+                    const int seg = seg_next;
+                    fetch_row(m0 + 32 * (c + 1 < kHalf ? c + 1 : 0) + lane);   // group 1 walks the same tokens
+                    const float bias_n = g == 0 ? bias[0] : bias[1];
+                    uint8_t* stage = epi_stage + (q % NB) * C::kStageBytes;
+                    if (lane == 0) {
+                        if (has_res) {
+                            // block (q + 1) % NB was last stored from as chunk q + 1 - NB
+                            ptx::bulk_wait_group_read<NB - 2>();
+                            if (c + 1 < kHalf) ask(n_base, m_base + 32);
+                            else if (g == 0) ask(n_base + BWG, m0);
+                            else ask_tile(t + gridDim.x);
+                        } else {
+                            ptx::bulk_wait_group_read<NB - 1>();
+                        }
+                    }
+                    __syncwarp();
+                    ptx::tmem_wait_ld();
+                    if (has_res && !__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&res_full[q % NB], (q / NB) & 1u, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    if (c + 1 == kHalf) {              // the group's last values are in registers: its MMAs may go on
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&acc_empty[g]);
+                    }
+                    // One round per segment among the chunk's tokens (rows past M ride along, clipped by the store).
+                    const uint32_t past = __ballot_sync(0xFFFFFFFFu, seg == -2);
+                    const uint32_t live = __ballot_sync(0xFFFFFFFFu, seg >= 0);
+                    for (uint32_t todo = live; todo != 0;) {
+                        const int s = __shfl_sync(0xFFFFFFFFu, seg, __ffs(todo) - 1);
+                        const uint32_t rows = __ballot_sync(0xFFFFFFFFu, seg == s);
+                        todo &= ~rows;
+                        if (s != held) {
+                            held = s;
+                            load_gate();
+                        }
+                        const float gate_n = g == 0 ? gate[0] : gate[1];
+                        const uint32_t mask = rows | past;
+                        const auto finish = [&](auto act) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const float z = fmaf(__uint_as_float(v[k]), __shfl_sync(0xFFFFFFFFu, rs, k), bias_n);
+                                const float a = epi::activate_as<decltype(act)::value>(z);
+                                if constexpr (kBf16Out) {
+                                    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(stage) + k * 32 + lane;
+                                    const float r = has_res ? __bfloat162float(*o) : 0.0f;
+                                    if ((mask >> k) & 1u) *o = __float2bfloat16_rn(fmaf(gate_n, a, r));
+                                } else {
+                                    float* o = reinterpret_cast<float*>(stage) + k * 32 + lane;
+                                    const float r = has_res ? *o : 0.0f;
+                                    if ((mask >> k) & 1u) *o = fmaf(gate_n, a, r);
+                                }
+                            }
+                        };
+                        using std::integral_constant;
+                        switch (p.e.act) {
+                            case QL_ACT_SILU: finish(integral_constant<int, QL_ACT_SILU>{}); break;
+                            case QL_ACT_GELU: finish(integral_constant<int, QL_ACT_GELU>{}); break;
+                            case QL_ACT_GELU_TANH: finish(integral_constant<int, QL_ACT_GELU_TANH>{}); break;
+                            default: finish(integral_constant<int, QL_ACT_NONE>{}); break;
+                        }
+                    }
+                    if ((live | past) == 0xFFFFFFFFu) {
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::tma_store_2d(&map_y, stage, n_base, m_base);
+                    } else {                           // padding among the tokens: the others' rows one by one
+                        __syncwarp();
+                        if (n_base + lane < p.N) {
+                            for (uint32_t left = live; left != 0; left &= left - 1) {
+                                const int k = __ffs(left) - 1;
+                                const int64_t at = static_cast<int64_t>(m_base + k) * p.N + n_base + lane;
+                                if constexpr (kBf16Out)
+                                    static_cast<__nv_bfloat16*>(p.y)[at] = reinterpret_cast<const __nv_bfloat16*>(stage)[k * 32 + lane];
+                                else
+                                    static_cast<float*>(p.y)[at] = reinterpret_cast<const float*>(stage)[k * 32 + lane];
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) ptx::bulk_commit_group();   // (empty for rows stored one by one)
+                }
+            }
+            if (lane == 0) {
+                if (has_res) {                         // no copy lands after the CTA's end
+                    for (uint32_t i = asked > static_cast<uint32_t>(NB) ? asked - NB : 0u; i < asked; ++i)
+                        ptx::mbar_wait(&res_full[i % NB], (i / NB) & 1u, nullptr);
+                }
+                ptx::bulk_wait_group_all();            // every store has completed before the CTA exits
+            }
+        }
     } else if (warp >= kWarpEpi0) {
         // ---------------------------------------------------------------- epilogue
         test_delay(kDelayEpilogue);   // the checked build can hold this role back (qlinear_test_delay)

@@ -106,15 +106,22 @@ cudaError_t fused_smem_attr() {
     return e;
 }
 
-template <int B>
+template <int B, int kAct>
 cudaError_t epilogue_smem_attr() {
     using EB = typename fused::PickEpiCfg<B, true>::type;
     using EF = typename fused::PickEpiCfg<B, false>::type;
-    const cudaError_t e = cudaFuncSetAttribute(fused::fused_gemm_kernel<true, EB, false, false, false, true>,
+    const cudaError_t e = cudaFuncSetAttribute(fused::fused_gemm_kernel<true, EB, false, false, false, kAct>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, EB::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(fused::fused_gemm_kernel<false, EF, false, false, false, true>,
+    return cudaFuncSetAttribute(fused::fused_gemm_kernel<false, EF, false, false, false, kAct>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, EF::kSmemBytes);
+}
+template <int B>
+cudaError_t epilogue_smem_attrs() {
+    for (const cudaError_t e : {epilogue_smem_attr<B, QL_ACT_NONE>(), epilogue_smem_attr<B, QL_ACT_SILU>(),
+                                epilogue_smem_attr<B, QL_ACT_GELU>(), epilogue_smem_attr<B, QL_ACT_GELU_TANH>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 template <int NT>
@@ -140,7 +147,7 @@ ql_status device_info(DeviceInfo** out) {
         if (fused_smem_attr<4>() != cudaSuccess || fused_smem_attr<8>() != cudaSuccess ||
             fused_smem_attr<4, true>() != cudaSuccess || fused_smem_attr<4, false, true>() != cudaSuccess ||
             fused_smem_attr<8, false, true>() != cudaSuccess || fused_smem_attr<4, true, true>() != cudaSuccess ||
-            epilogue_smem_attr<4>() != cudaSuccess || epilogue_smem_attr<8>() != cudaSuccess ||
+            epilogue_smem_attrs<4>() != cudaSuccess || epilogue_smem_attrs<8>() != cudaSuccess ||
             prepare_smem_attr<1>() != cudaSuccess || prepare_smem_attr<2>() != cudaSuccess ||
             prepare_smem_attr<4>() != cudaSuccess)
             return QL_ERR_CUDA;
@@ -602,27 +609,31 @@ ql_status launch_fused(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const 
                             FC::kSmemBytes, st, mx, mc, mc2, mp, my, static_cast<const fused::Params&>(p));
 }
 
-// The fused kernel in epilogue mode.
-template <int B>
-ql_status launch_epilogue(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& mc, const CUtensorMap& mp,
-                          const CUtensorMap& my, const fused::Params& base, const epi::Epilogue& e, bool bf16_out, int64_t M,
-                          int64_t N) {
-    fused::EpiParams p;
-    static_cast<fused::Params&>(p) = base;
-    p.e = e;
-    p.map_res = my;
-    ql_status s;
-    if (e.residual &&
-        (s = encode_2d(&p.map_res, bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, e.residual,
-                       N, M, N * (bf16_out ? 2 : 4), 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK)
-        return s;
+// The fused kernel in epilogue mode (which writes y without a map).
+template <int B, int kAct>
+ql_status launch_epilogue_act(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& mc, const CUtensorMap& mp,
+                              const fused::EpiParams& p, bool bf16_out) {
     using EB = typename fused::PickEpiCfg<B, true>::type;
     using EF = typename fused::PickEpiCfg<B, false>::type;
     if (bf16_out)
-        return launch_dependent(fused::fused_gemm_kernel<true, EB, false, false, false, true>, grid, fused::kThreads,
-                                EB::kSmemBytes, st, mx, mc, mc, mp, my, p);
-    return launch_dependent(fused::fused_gemm_kernel<false, EF, false, false, false, true>, grid, fused::kThreads,
-                            EF::kSmemBytes, st, mx, mc, mc, mp, my, p);
+        return launch_dependent(fused::fused_gemm_kernel<true, EB, false, false, false, kAct>, grid, fused::kThreads,
+                                EB::kSmemBytes, st, mx, mc, mc, mp, mx, p);
+    return launch_dependent(fused::fused_gemm_kernel<false, EF, false, false, false, kAct>, grid, fused::kThreads,
+                            EF::kSmemBytes, st, mx, mc, mc, mp, mx, p);
+}
+
+template <int B>
+ql_status launch_epilogue(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& mc, const CUtensorMap& mp,
+                          const fused::Params& base, const epi::Epilogue& e, bool bf16_out) {
+    fused::EpiParams p;
+    static_cast<fused::Params&>(p) = base;
+    p.e = e;
+    switch (e.act) {
+        case QL_ACT_SILU: return launch_epilogue_act<B, QL_ACT_SILU>(grid, st, mx, mc, mp, p, bf16_out);
+        case QL_ACT_GELU: return launch_epilogue_act<B, QL_ACT_GELU>(grid, st, mx, mc, mp, p, bf16_out);
+        case QL_ACT_GELU_TANH: return launch_epilogue_act<B, QL_ACT_GELU_TANH>(grid, st, mx, mc, mp, p, bf16_out);
+        default: return launch_epilogue_act<B, QL_ACT_NONE>(grid, st, mx, mc, mp, p, bf16_out);
+    }
 }
 
 ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const void* scales, const void* biases,
@@ -714,8 +725,8 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
         return launch_status();
     }
     if (ep) {
-        s = bits == 4 ? launch_epilogue<4>(fgrid, st, mx, mc, mp, my, p, *ep, bf16_out, M, N)
-                      : launch_epilogue<8>(fgrid, st, mx, mc, mp, my, p, *ep, bf16_out, M, N);
+        s = bits == 4 ? launch_epilogue<4>(fgrid, st, mx, mc, mp, p, *ep, bf16_out)
+                      : launch_epilogue<8>(fgrid, st, mx, mc, mp, p, *ep, bf16_out);
         if (s != QL_OK) return s;
         prof_end(st);
         set_dispatch("path=tc_fused_epilogue bits=%d tile=%dw x %dt x %dk stages=x%d/c%dx%d/a%d ctas=%d splitk=1 launches=3 why=%s",

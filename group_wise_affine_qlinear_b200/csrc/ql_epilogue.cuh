@@ -23,25 +23,39 @@ struct Epilogue {
     int params_f32;          // type of bias and gate: 0 bf16, 1 fp32
 };
 
-// The hardware's exponential and division err by a few fp32 units, the weights' rounding to f16 by 2^-12: of no
-// consequence.  All three give z (or z - 0) for large z, and -0 where e^-z overflows.
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+// The hardware's base-2 exponential and reciprocal (2 units of fp32 each; the argument's rounding adds |v| 2^-24): of no
+// consequence beside the weights' rounding to f16.
+__device__ __forceinline__ float exp2_fast(float v) {
+    float o;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
+    return o;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+    float o;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
+    return o;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// z / (1 + e^-z); where e^-z overflows the reciprocal is 0 and the result -0.
+__device__ __forceinline__ float silu(float z) { return z * rcp_fast(1.0f + exp2_fast(-kLog2e * z)); }
 
 // z Phi(z) with 1 - erf from Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26 (absolute error below
 // 1.5e-7): where the library's erff takes some forty instructions and a branch, this takes a dozen.
 __device__ __forceinline__ float gelu(float z) {
     const float a = fabsf(z) * 0.70710678f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, a, 1.0f));
-    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                                0.254829592f);
-    const float tail = 0.5f * poly * __expf(-a * a);       // 1 - Phi(|z|)
-    return z >= 0.0f ? z - fminf(z, 1e4f) * tail : z * tail;   // (an infinite z times a zero tail would be NaN)
+    const float t = rcp_fast(fmaf(0.3275911f, a, 1.0f));
+    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f), 0.5f * 1.421413741f),
+                                        0.5f * -0.284496736f), 0.5f * 0.254829592f);
+    const float tail = poly * exp2_fast(-0.5f * kLog2e * z * z);       // 1 - Phi(|z|)
+    // z - z tail above zero, z tail below (an infinite z times a zero tail would be NaN)
+    return fmaf(-fminf(fabsf(z), 1e4f), tail, fmaxf(z, 0.0f));
 }
 
 // 0.5 z (1 + tanh(u)) = z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3)
 __device__ __forceinline__ float gelu_tanh(float z) {
-    const float u2 = 1.59576912f * fmaf(0.044715f * z * z, z, z);
-    return __fdividef(z, 1.0f + __expf(-u2));
+    const float u = z * fmaf(0.044715f * 1.59576912f * -kLog2e, z * z, 1.59576912f * -kLog2e);    // -2 u log2(e)
+    return z * rcp_fast(1.0f + exp2_fast(u));
 }
 
 template <int kAct>

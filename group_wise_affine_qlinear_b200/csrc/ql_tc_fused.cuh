@@ -72,10 +72,7 @@
 // nothing travels through memory a second time, and y is rounded once.  B comes by TMA through the code ring (a code
 // stage per extra step), t by TMA too, eight rows at a time, but for the eights that meet several adapters.
 //
-// Epilogue mode (kEpi): y = residual + gate[seg] * act(acc + bias), on the accumulator's way out.  A block of the
-// residual (32 tokens x 32 columns, a chunk's) comes by TMA into the staging block that the chunk's outputs then take its
-// place in, one chunk ahead; a lane's bias and gate are one value each per group.  Three staging blocks per warp (one
-// stored from, one worked on, one filled) take the room of an activation stage.
+// Epilogue mode (kAct): y = residual + gate[seg] * act(acc + bias), on the accumulator's way out (epilogue_role).
 #pragma once
 
 #include "ql_ptx.cuh"
@@ -145,17 +142,19 @@ template <> struct PickCfg<4, true> { using type = Cfg<5, 2, 4, 2, 2>; };
 template <> struct PickCfg<4, false> { using type = Cfg<4, 2, 4, 4, 1>; };
 template <> struct PickCfg<8, true> { using type = Cfg<5, 2, 8, 2, 2>; };
 template <> struct PickCfg<8, false> { using type = Cfg<4, 2, 8, 4, 1>; };
-
-// Epilogue mode: a barrier per staging block behind the others.
+// Epilogue mode: two staging blocks per warp, one worked on while the next one's residual arrives, and two buffers of a
+// tile's vectors (row scales of 96 tokens, bias and gate of 2 x 32 columns); they take the room of an activation stage.
+constexpr uint32_t kEpiVectorBytes = BT / 2 * 4 + 2 * NG * 32 * 4;
 template <class Base>
 struct EpiCfg : Base {
-    static constexpr uint32_t kOffRes = Base::kOffMisc + 16;
-    static constexpr uint32_t kSmemBytes = Base::kSmemBytes + kEpiWarps * Base::kNB * 8;
-    static_assert(Base::kNB >= 2 && kOffRes % 8 == 0 && kSmemBytes <= 232448, "staging and shared memory budget");
+    static_assert(Base::kNB == 2, "two staging blocks");
+    static constexpr uint32_t kOffVec = Base::kOffMisc + 16;
+    static constexpr uint32_t kSmemBytes = Base::kSmemBytes + kEpiWarps * 2 * kEpiVectorBytes;
+    static_assert(kOffVec % 8 == 0 && kSmemBytes <= 232448, "shared memory budget");
 };
 template <int B, bool kBf16Out>
 struct PickEpiCfg;
-template <int B> struct PickEpiCfg<B, true> { using type = EpiCfg<Cfg<4, 2, B, 2, 3>>; };
+template <int B> struct PickEpiCfg<B, true> { using type = EpiCfg<Cfg<4, 2, B, 2, 2>>; };
 template <int B> struct PickEpiCfg<B, false> { using type = EpiCfg<Cfg<3, 2, B, 4, 2>>; };
 
 struct Params {
@@ -181,7 +180,6 @@ struct LoraParams : Params {
 __host__ __device__ constexpr int part_cols(int r8) { return r8 < 4 ? 8 * r8 : 32; }
 struct EpiParams : Params {
     epi::Epilogue e;
-    CUtensorMap map_res;         // the residual as [M][N] of y's type, boxes of 32 x 32
 };
 template <bool kLora, bool kEpi> struct PickParams { using type = Params; };
 template <> struct PickParams<true, false> { using type = LoraParams; };
@@ -210,15 +208,274 @@ __device__ __forceinline__ uint32_t bf16_part(float v0, float v1, bool lo) {
     return lo ? pack_bf16x2(f0 ? v0 - h0 : 0.0f, f1 ? v1 - h1 : 0.0f) : pack_bf16x2(h0, h1);
 }
 
+constexpr int kNoEpilogue = -1;     // kAct of a plain layer; else a ql_activation
+
+// Registers per thread in epilogue mode: its warps take what the TMA and MMA warps (one warpgroup) do not need.
+constexpr int kEpiRegs = 120, kIssueRegs = 48, kLaunchRegs = 96;
+static_assert(kDequantWarps * kLaunchRegs + 4 * kIssueRegs + kEpiWarps * kEpiRegs <= (kThreads / 32) * kLaunchRegs,
+              "the warps' shares fit what the block is launched with");
+template <bool kEpi>
+__device__ __forceinline__ bool give_registers() {
+    if constexpr (kEpi) ptx::fewer_registers<kIssueRegs>();
+    return true;
+}
+
+// The epilogue warps of the epilogue mode.  Warp (quarter, half) drains its lanes of group 0, then of group 1, in chunks of
+// 32 tokens x 32 columns, as in the plain epilogue; chunk q of its run passes through staging block q % 2, to which the
+// residual of its tokens is copied while chunk q - 1 is worked on, and from which its outputs go to y, 16 bytes a lane.
+// Lane l works on columns 8 i + l / 4 (i < 4) and, for j < 4, on tokens 8 j + 2 (l % 4) and + 1 of a chunk: the fragment of
+// the accumulator that transposing matrix stores (and loads, for the residual) take to a token's row, eight elements an
+// instruction.  A row's 16-byte pieces are permuted by its number, so that neither matrices nor rows meet in a bank.
+template <bool kBf16Out, int kAct>
+__device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage0, uint32_t stage_bytes, uint32_t vec0,
+                                              uint32_t tmem_base,
+                                              uint64_t* acc_full, uint64_t* acc_empty, volatile int* abort_flag, int quarter,
+                                              int half, int lane) {
+    constexpr int kHalf = BT / 32 / 2, kPast = -2, kElem = kBf16Out ? 2 : 4;
+    constexpr int kPieces = 32 * kElem / 16, kRows = 32 / kPieces;     // a copy: kPieces lanes per row, kRows rows at a time
+    const int lt = 2 * (lane & 3), ln = lane >> 2;
+    const uint32_t mat_off = 64u * (lane & 7) + 16u * ((lane >> 3) ^ ((lane >> 1) & 3));                // bf16
+    const int row0 = lane / kPieces, piece = lane % kPieces;
+    // (the copies' rows row0 + kRows k differ in a multiple of 8 or 4: one permutation or two for all of them)
+    const auto piece_at = [&](int k) {
+        const int row = row0 + kRows * k;
+        return static_cast<uint32_t>(row * 32 * kElem + 16 * (piece ^ (kBf16Out ? (row >> 1) & 3 : row & 7)));
+    };
+    const int num_tiles = p.num_t * p.num_w, N = p.N;
+    const bool has_res = p.e.residual != nullptr;
+    const int64_t row_step = static_cast<int64_t>(N) * kElem;
+    const uint32_t acc = tmem_base + kAccCol + static_cast<uint32_t>(32 * kHalf * half) + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int m_off = 32 * kHalf * half, n_off = quarter * 32;         // this warp's part of a tile
+
+    // the residual of 32 tokens from m on and 32 columns from n on
+    const auto copy_residual = [&](uint32_t block, int m, int n) {
+        const int left = p.M - m - row0, col = n + piece * (16 / kElem);
+        const uint8_t* from = static_cast<const uint8_t*>(p.e.residual) + (m + row0) * row_step + static_cast<int64_t>(col) * kElem;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const bool in = kRows * k < left && col < N;
+            ptx::copy16_async(stage0 + block * stage_bytes + piece_at(k), in ? from + kRows * k * row_step : p.e.residual, in);
+        }
+    };
+    // What a tile needs beside its accumulators is copied, asynchronously too, while the tile before is drained: its row
+    // scales, and both groups' bias and gate (as they are; the gate of the tile's first token), in one of two buffers.
+    // (Fetched into registers they cost more of them than there are, and the loads' latency with the spills.)
+    constexpr uint32_t kRsAt = 0, kBiasAt = 32 * kHalf * 4, kGateAt = kBiasAt + NG * 128;
+    static_assert(kGateAt + NG * 128 == kEpiVectorBytes, "the buffers' size");
+    const bool wide = p.e.params_f32 != 0;
+    const auto copy_rows = [&](uint32_t to, int t_blk) {
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) {
+            const int m = t_blk * BT + m_off + 32 * c + lane;
+            ptx::copy4_async(to + kRsAt + 128u * c + 4u * lane, p.rowscale + min(m, p.M - 1));
+        }
+    };
+    const auto copy_vector = [&](uint32_t to, const void* from, int row, int n) {      // 32 columns from n on
+        if (from == nullptr) return;
+        const int col = wide ? n + lane : n + 2 * (lane & 15);                         // (those past N are not stored)
+        const int64_t at = static_cast<int64_t>(row) * N + (col < N ? col : 0);
+        ptx::copy4_async(to + (wide ? 4u * lane : 4u * (lane & 15)), static_cast<const uint8_t*>(from) + (wide ? 4 * at : 2 * at));
+    };
+    const auto vector_at = [&](const void* given, uint32_t at, float none) {           // of the lane's columns
+        float4 o = make_float4(none, none, none, none);
+        if (given != nullptr) {
+            if (wide)
+                o = make_float4(ptx::ld_shared_f32(at + 4u * ln), ptx::ld_shared_f32(at + 4u * ln + 32u),
+                                ptx::ld_shared_f32(at + 4u * ln + 64u), ptx::ld_shared_f32(at + 4u * ln + 96u));
+            else
+                o = make_float4(ptx::ld_shared_bf16(at + 2u * ln), ptx::ld_shared_bf16(at + 2u * ln + 16u),
+                                ptx::ld_shared_bf16(at + 2u * ln + 32u), ptx::ld_shared_bf16(at + 2u * ln + 48u));
+        }
+        return o;
+    };
+    // Segment of token 32 c + lane of a tile; kPast beyond M.
+    const auto segment = [&](int t_blk, int c) {
+        const int m = t_blk * BT + m_off + 32 * c + lane;
+        return m < p.M ? epi::segment_of(p.e, m) : kPast;
+    };
+
+    ptx::grid_dependency_wait();                       // the row scales come from the kernels before this one
+    int t_blk, w_blk, seg[kHalf];
+    tile_coords(blockIdx.x, p.num_w, t_blk, w_blk);
+#pragma unroll
+    for (int c = 0; c < kHalf; ++c) seg[c] = segment(t_blk, c);
+    int held = max(__shfl_sync(0xFFFFFFFFu, seg[0], 0), 0);            // segment of the gate at hand
+    copy_rows(vec0, t_blk);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        copy_vector(vec0 + kBiasAt + 128u * g, p.e.bias, 0, w_blk * BW + g * BWG + n_off);
+        copy_vector(vec0 + kGateAt + 128u * g, p.e.gate, held, w_blk * BW + g * BWG + n_off);
+    }
+    if (has_res) copy_residual(0, t_blk * BT + m_off, w_blk * BW + n_off);
+    ptx::copy_async_commit();
+    uint32_t block = 0, phase = 0;
+    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, phase ^= 1u) {
+        int t_next, w_next;
+        tile_coords(t, p.num_w, t_blk, w_blk);
+        tile_coords(t + static_cast<int>(gridDim.x), p.num_w, t_next, w_next);     // (past the last tile: rows past M)
+        const int m0 = t_blk * BT + m_off, tile_seg = held;
+        const uint32_t vec = vec0 + phase * kEpiVectorBytes, vec_next = vec0 + (phase ^ 1u) * kEpiVectorBytes;
+        uint32_t live[kHalf], uniform = 0;             // live tokens; bit c: chunk c's are all of segment tile_seg
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) {
+            live[c] = __ballot_sync(0xFFFFFFFFu, seg[c] >= 0);
+            if (__all_sync(0xFFFFFFFFu, seg[c] < 0 || seg[c] == tile_seg)) uniform |= 1u << c;
+        }
+        if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(acc_full, phase, abort_flag))) break;
+        ptx::tc_fence_after_sync();
+        uint32_t v[2][16];                             // a chunk's values: TMEM lanes 16 h .. + 15 of the warp's 32
+        ptx::tmem_ld_16x256b_x4(acc, v[0]);
+        ptx::tmem_ld_16x256b_x4(acc + (16u << 16), v[1]);
+#pragma unroll 1
+        for (int g = 0; g < NG; ++g) {
+            const int n0 = w_blk * BW + g * BWG + n_off;
+            uint8_t* y = static_cast<uint8_t*>(p.y) + (m0 + row0) * row_step + (n0 + piece * (16 / kElem)) * static_cast<int64_t>(kElem);
+            const bool col_in = n0 + piece * (16 / kElem) < N;
+            float4 bias, gate;
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c, block ^= 1u) {
+                const uint32_t stage = stage0 + block * stage_bytes;
+                const bool last = c + 1 == kHalf;
+                // the next chunk's residual (the other block was read before the last __syncwarp), the next tile's rows
+                if (has_res) {
+                    if (!last) copy_residual(block ^ 1u, m0 + 32 * (c + 1), n0);
+                    else if (g == 0) copy_residual(block ^ 1u, m0, n0 + BWG);
+                    else copy_residual(block ^ 1u, t_next * BT + m_off, w_next * BW + n_off);
+                }
+                if (g == 1 && c == 0) {
+                    copy_rows(vec_next, t_next);
+#pragma unroll
+                    for (int i = 0; i < kHalf; ++i) seg[i] = segment(t_next, i);
+                }
+                if (g == 1 && last) {
+                    held = max(__shfl_sync(0xFFFFFFFFu, seg[0], 0), 0);
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        copy_vector(vec_next + kBiasAt + 128u * i, p.e.bias, 0, w_next * BW + i * BWG + n_off);
+                        copy_vector(vec_next + kGateAt + 128u * i, p.e.gate, held, w_next * BW + i * BWG + n_off);
+                    }
+                }
+                ptx::copy_async_commit();
+                ptx::tmem_wait_ld();
+                if (last) {                            // the group's last values are in registers: its MMAs may go on
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&acc_empty[g]);
+                }
+                ptx::copy_async_wait<1>();             // all copies but the ones just begun
+                __syncwarp();
+                if (c == 0) {
+                    bias = vector_at(p.e.bias, vec + kBiasAt + 128u * g, 0.0f);
+                    gate = vector_at(p.e.gate, vec + kGateAt + 128u * g, 1.0f);
+                }
+                const float b4[4] = {bias.x, bias.y, bias.z, bias.w};
+                // act(acc * row scale + bias), in place
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 rs = ptx::ld_shared_f32x2(vec + kRsAt + 128u * c + 32u * j + 4u * lt);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t* a = &v[i >> 1][4 * j + 2 * (i & 1)];
+                        a[0] = __float_as_uint(epi::activate_as<kAct>(fmaf(__uint_as_float(a[0]), rs.x, b4[i])));
+                        a[1] = __float_as_uint(epi::activate_as<kAct>(fmaf(__uint_as_float(a[1]), rs.y, b4[i])));
+                    }
+                }
+                // residual + gate * act into the block; kRes: it holds the residual; kAll: for every token, else for
+                // those in `mask`, the others keep what the block holds
+                const auto finish = [&](auto res, auto all, uint32_t mask, const float4 w) {
+                    constexpr bool kRes = decltype(res)::value, kAll = decltype(all)::value;
+                    const float w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool in0 = kAll || ((mask >> (8 * j + lt)) & 1u) != 0;
+                        const bool in1 = kAll || ((mask >> (8 * j + lt + 1)) & 1u) != 0;
+                        if constexpr (kBf16Out) {
+                            uint32_t b[4] = {0u, 0u, 0u, 0u};
+                            if constexpr (kRes) ptx::ldmatrix_x4_trans(stage + 512 * j + mat_off, b);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t* a = &v[i >> 1][4 * j + 2 * (i & 1)];
+                                const float o0 = bf16_lo(b[i]), o1 = bf16_hi(b[i]);
+                                const float y0 = kRes ? fmaf(w4[i], __uint_as_float(a[0]), o0) : w4[i] * __uint_as_float(a[0]);
+                                const float y1 = kRes ? fmaf(w4[i], __uint_as_float(a[1]), o1) : w4[i] * __uint_as_float(a[1]);
+                                b[i] = pack_bf16x2(in0 ? y0 : o0, in1 ? y1 : o1);
+                            }
+                            ptx::stmatrix_x4_trans(stage + 512 * j + mat_off, b);
+                        } else {
+                            uint32_t at[8];
+                            float r[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int token = lt + (i & 1);
+                                at[i] = stage + 1024u * j + 128u * token + 4u * (ln & 3) + 16u * ((2u * (i >> 1) + (ln >> 2)) ^ token);
+                                r[i] = kRes ? ptx::ld_shared_f32(at[i]) : 0.0f;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float y = fmaf(w4[i >> 1], __uint_as_float(v[i >> 2][4 * j + (i & 3)]), r[i]);
+                                ptx::st_shared_f32(at[i], ((i & 1) ? in1 : in0) ? y : r[i]);
+                            }
+                        }
+                    }
+                };
+                if ((uniform >> c) & 1u) {
+                    if (has_res) finish(std::true_type{}, std::true_type{}, 0u, gate);
+                    else finish(std::false_type{}, std::true_type{}, 0u, gate);
+                } else {                               // one round per segment among the chunk's tokens
+                    if (!has_res) {
+#pragma unroll
+                        for (int k = 0; k < kPieces; ++k) ptx::st_shared_zero16(stage + piece_at(k));
+                        __syncwarp();
+                    }
+                    const int seg_c = segment(t_blk, c);
+                    for (uint32_t todo = live[c]; todo != 0;) {
+                        const int s = __shfl_sync(0xFFFFFFFFu, seg_c, __ffs(todo) - 1);
+                        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, seg_c == s);
+                        todo &= ~mask;
+                        float w[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+                        if (p.e.gate != nullptr) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                w[i] = epi::param(p.e.gate, p.e.params_f32, static_cast<int64_t>(s) * N + min(n0 + ln + 8 * i, N - 1));
+                        }
+                        finish(std::true_type{}, std::false_type{}, mask, make_float4(w[0], w[1], w[2], w[3]));
+                        __syncwarp();                  // the next round reads what other lanes wrote
+                    }
+                }
+                if (!last || g == 0) {
+                    const uint32_t next = acc + (last ? static_cast<uint32_t>(BT) : g * static_cast<uint32_t>(BT) + 32u * (c + 1));
+                    ptx::tmem_ld_16x256b_x4(next, v[0]);
+                    ptx::tmem_ld_16x256b_x4(next + (16u << 16), v[1]);
+                }
+                __syncwarp();
+                const uint32_t rows = col_in ? live[c] >> row0 : 0u;
+                uint4 o[4];
+#pragma unroll
+                for (int k0 = 0; k0 < kPieces; k0 += 4) {              // four rows' loads, then their stores
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = ptx::ld_shared_v4(stage + piece_at(k0 + k));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if ((rows >> (kRows * (k0 + k))) & 1u)
+                            *reinterpret_cast<uint4*>(y + (32 * c + kRows * (k0 + k)) * row_step) = o[k];
+                }
+                __syncwarp();                          // the block may be filled again
+            }
+        }
+    }
+    ptx::copy_async_wait<0>();                         // no copy lands after the CTA's end
+}
+
 // map_codes2: the up weight's codes in SwiGLU mode (128-row boxes, like map_codes there); unused otherwise.
 // kSplitK: every tile's K-steps are cut into p.splits slices, each its own work unit; a unit writes the
 // fp32 partial of its slice through map_y, a 3-D map over partials [splits][M][N], and a separate
 // reduction sums the slices in order (for shapes with fewer tiles than SMs).
-template <bool kBf16Out, class C, bool kSwiGLU = false, bool kSplitK = false, bool kLora = false, bool kEpi = false>
+template <bool kBf16Out, class C, bool kSwiGLU = false, bool kSplitK = false, bool kLora = false, int kAct = kNoEpilogue>
 __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_codes,
     const __grid_constant__ CUtensorMap map_codes2, const __grid_constant__ CUtensorMap map_params,
-    const __grid_constant__ CUtensorMap map_y, const __grid_constant__ typename PickParams<kLora, kEpi>::type p) {
+    const __grid_constant__ CUtensorMap map_y, const __grid_constant__ typename PickParams<kLora, kAct != kNoEpilogue>::type p) {
+    constexpr bool kEpi = kAct != kNoEpilogue;
     constexpr int NX = C::kNX, NC = C::kNC;
     static_assert(!kSwiGLU || C::kBits == 4, "the SwiGLU pair is built for 4-bit codes");
     static_assert(!kSplitK || (!kSwiGLU && !kBf16Out), "split-K units write fp32 partials of a plain layer");
@@ -283,9 +540,6 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
         // an accumulator is drained by all 8 epilogue warps (a lane quarter and half of the tokens each)
         for (int g = 0; g < NG; ++g) ptx::mbar_init(&acc_empty[g], kEpiWarps);
         for (int g = 0; g < NG; ++g) ptx::mbar_init(drain + g, 1);
-        if constexpr (kEpi) {
-            for (int i = 0; i < kEpiWarps * C::kNB; ++i) ptx::mbar_init(reinterpret_cast<uint64_t*>(smem + C::kOffRes) + i, 1);
-        }
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -442,6 +696,16 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
                 }
             }
         }
+    } else if (kEpi && warp >= kWarpEpi0) {
+        // ---------------------------------------------------------------- epilogue with bias, activation, gate, residual
+        test_delay(kDelayEpilogue);   // the checked build can hold this role back (qlinear_test_delay)
+        if constexpr (kEpi) {
+            ptx::more_registers<kEpiRegs>();
+            const int e = warp - kWarpEpi0;
+            epilogue_role<kBf16Out, kAct>(p, ptx::smem_addr(smem + C::kOffEpi) + e * C::kNB * C::kStageBytes, C::kStageBytes,
+                                          ptx::smem_addr(smem + C::kOffVec) + e * 2 * kEpiVectorBytes, tmem_base, acc_full, acc_empty, abort_flag, warp & 3, e >> 2, lane);
+        }
+    } else if (!give_registers<kEpi>()) {
     } else if (kLora && warp == kWarpTmaX) {
         // ---------------------------------------------------------------- activation producer, adapter mode
         test_delay(kDelayActivations);   // the checked build can hold this role back (qlinear_test_delay)
@@ -803,165 +1067,6 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
             }
         }
         if (lane == 0) ptx::bulk_wait_group_all();   // every store has completed before the CTA exits
-    } else if (kEpi && warp >= kWarpEpi0) {
-        // ---------------------------------------------------------------- epilogue with bias, activation, gate, residual
-        test_delay(kDelayEpilogue);   // the checked build can hold this role back (qlinear_test_delay)
-        if constexpr (kEpi) {
-            // As below: warp (quarter, half) drains its lanes of group 0, then of group 1, chunks of 32 tokens.  Its
-            // chunks are numbered q over all tiles; chunk q uses staging block q % kNB, the block's barrier its use q / kNB.
-            constexpr int kHalf = BT / 32 / 2, NB = C::kNB;
-            const int quarter = warp & 3;
-            const int half = (warp - kWarpEpi0) >> 2;
-            uint8_t* epi_stage = smem + C::kOffEpi + (warp - kWarpEpi0) * NB * C::kStageBytes;
-            uint64_t* res_full = reinterpret_cast<uint64_t*>(smem + C::kOffRes) + (warp - kWarpEpi0) * NB;
-            const bool has_res = p.e.residual != nullptr;
-            const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-            uint32_t q = 0, asked = 0;                 // chunks done; residual blocks asked for
-            const auto ask = [&](int x, int y) {       // lane 0: the residual block of the next chunk
-                const uint32_t b = asked++ % NB;
-                ptx::mbar_arrive_expect_tx(&res_full[b], C::kStageBytes);
-                ptx::tma_load_2d(epi_stage + b * C::kStageBytes, &p.map_res, &res_full[b], x, y);
-            };
-            const auto ask_tile = [&](int t) {
-                if (t >= num_tiles) return;
-                int t_blk, w_blk;
-                tile_coords(t, p.num_w, t_blk, w_blk);
-                ask(w_blk * BW + quarter * 32, t_blk * BT + 32 * kHalf * half);
-            };
-            ptx::grid_dependency_wait();               // the row scales come from the kernels before this one
-            if (has_res && lane == 0) ask_tile(blockIdx.x);
-            bool ok = true;
-            int j = 0;
-            for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++j) {
-                int t_blk, w_blk;
-                tile_coords(t, p.num_w, t_blk, w_blk);
-                const int m0 = t_blk * BT + 32 * kHalf * half;         // this warp's first token
-                // row scale and segment of token m0 + 32 c + lane, fetched a chunk ahead
-                float rs_next;
-                int seg_next;
-                const auto fetch_row = [&](int m) {
-                    rs_next = m < p.M ? p.rowscale[m] : 0.0f;
-                    seg_next = m < p.M ? epi::segment_of(p.e, m) : -2;
-                };
-                fetch_row(m0 + lane);
-                const int n_first = w_blk * BW + quarter * 32 + lane;  // this lane's column of group 0
-                int held = max(__shfl_sync(0xFFFFFFFFu, seg_next, 0), 0);
-                float bias[NG], gate[NG];
-                const auto load_gate = [&] {
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const int n = n_first + g * BWG;
-                        gate[g] = p.e.gate != nullptr && n < p.N
-                                      ? epi::param(p.e.gate, p.e.params_f32, static_cast<int64_t>(held) * p.N + n) : 1.0f;
-                    }
-                };
-                load_gate();
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const int n = n_first + g * BWG;
-                    bias[g] = p.e.bias != nullptr && n < p.N ? epi::param(p.e.bias, p.e.params_f32, n) : 0.0f;
-                }
-                if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&acc_full[0], j & 1, abort_flag))) break;
-                ptx::tc_fence_after_sync();
-#pragma unroll 1
-                for (int i = 0; i < NG * kHalf; ++i, ++q) {
-                    const int g = i / kHalf, c = i - g * kHalf;
-                    const int n_base = w_blk * BW + g * BWG + quarter * 32, m_base = m0 + 32 * c;
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(tmem_base + kAccCol + static_cast<uint32_t>(g * BT + 32 * (kHalf * half + c)) + lane_addr, v);
-                    const float rs = rs_next;
-                    const int seg = seg_next;
-                    fetch_row(m0 + 32 * (c + 1 < kHalf ? c + 1 : 0) + lane);   // group 1 walks the same tokens
-                    const float bias_n = g == 0 ? bias[0] : bias[1];
-                    uint8_t* stage = epi_stage + (q % NB) * C::kStageBytes;
-                    if (lane == 0) {
-                        if (has_res) {
-                            // block (q + 1) % NB was last stored from as chunk q + 1 - NB
-                            ptx::bulk_wait_group_read<NB - 2>();
-                            if (c + 1 < kHalf) ask(n_base, m_base + 32);
-                            else if (g == 0) ask(n_base + BWG, m0);
-                            else ask_tile(t + gridDim.x);
-                        } else {
-                            ptx::bulk_wait_group_read<NB - 1>();
-                        }
-                    }
-                    __syncwarp();
-                    ptx::tmem_wait_ld();
-                    if (has_res && !__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&res_full[q % NB], (q / NB) & 1u, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
-                    if (c + 1 == kHalf) {              // the group's last values are in registers: its MMAs may go on
-                        ptx::tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&acc_empty[g]);
-                    }
-                    // One round per segment among the chunk's tokens (rows past M ride along, clipped by the store).
-                    const uint32_t past = __ballot_sync(0xFFFFFFFFu, seg == -2);
-                    const uint32_t live = __ballot_sync(0xFFFFFFFFu, seg >= 0);
-                    for (uint32_t todo = live; todo != 0;) {
-                        const int s = __shfl_sync(0xFFFFFFFFu, seg, __ffs(todo) - 1);
-                        const uint32_t rows = __ballot_sync(0xFFFFFFFFu, seg == s);
-                        todo &= ~rows;
-                        if (s != held) {
-                            held = s;
-                            load_gate();
-                        }
-                        const float gate_n = g == 0 ? gate[0] : gate[1];
-                        const uint32_t mask = rows | past;
-                        const auto finish = [&](auto act) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const float z = fmaf(__uint_as_float(v[k]), __shfl_sync(0xFFFFFFFFu, rs, k), bias_n);
-                                const float a = epi::activate_as<decltype(act)::value>(z);
-                                if constexpr (kBf16Out) {
-                                    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(stage) + k * 32 + lane;
-                                    const float r = has_res ? __bfloat162float(*o) : 0.0f;
-                                    if ((mask >> k) & 1u) *o = __float2bfloat16_rn(fmaf(gate_n, a, r));
-                                } else {
-                                    float* o = reinterpret_cast<float*>(stage) + k * 32 + lane;
-                                    const float r = has_res ? *o : 0.0f;
-                                    if ((mask >> k) & 1u) *o = fmaf(gate_n, a, r);
-                                }
-                            }
-                        };
-                        using std::integral_constant;
-                        switch (p.e.act) {
-                            case QL_ACT_SILU: finish(integral_constant<int, QL_ACT_SILU>{}); break;
-                            case QL_ACT_GELU: finish(integral_constant<int, QL_ACT_GELU>{}); break;
-                            case QL_ACT_GELU_TANH: finish(integral_constant<int, QL_ACT_GELU_TANH>{}); break;
-                            default: finish(integral_constant<int, QL_ACT_NONE>{}); break;
-                        }
-                    }
-                    if ((live | past) == 0xFFFFFFFFu) {
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) ptx::tma_store_2d(&map_y, stage, n_base, m_base);
-                    } else {                           // padding among the tokens: the others' rows one by one
-                        __syncwarp();
-                        if (n_base + lane < p.N) {
-                            for (uint32_t left = live; left != 0; left &= left - 1) {
-                                const int k = __ffs(left) - 1;
-                                const int64_t at = static_cast<int64_t>(m_base + k) * p.N + n_base + lane;
-                                if constexpr (kBf16Out)
-                                    static_cast<__nv_bfloat16*>(p.y)[at] = reinterpret_cast<const __nv_bfloat16*>(stage)[k * 32 + lane];
-                                else
-                                    static_cast<float*>(p.y)[at] = reinterpret_cast<const float*>(stage)[k * 32 + lane];
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    if (lane == 0) ptx::bulk_commit_group();   // (empty for rows stored one by one)
-                }
-            }
-            if (lane == 0) {
-                if (has_res) {                         // no copy lands after the CTA's end
-                    for (uint32_t i = asked > static_cast<uint32_t>(NB) ? asked - NB : 0u; i < asked; ++i)
-                        ptx::mbar_wait(&res_full[i % NB], (i / NB) & 1u, nullptr);
-                }
-                ptx::bulk_wait_group_all();            // every store has completed before the CTA exits
-            }
-        }
     } else if (warp >= kWarpEpi0) {
         // ---------------------------------------------------------------- epilogue
         test_delay(kDelayEpilogue);   // the checked build can hold this role back (qlinear_test_delay)

@@ -55,6 +55,45 @@ def forward8_epilogue(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
 def _forward_epilogue(x, codes, scales, biases, bias, activation, gate, residual, segment_ids, out, workspace, out_dtype,
                       stream, bits):
     L = lib()
+    # one pass over arguments that are right; where it fails, the checks by name say what is wrong
+    try:
+        M, K = x.shape
+        N = codes.shape[0]
+        dev, act = x.get_device(), ACTIVATIONS[activation]
+        like = residual if residual is not None else out
+        yt = out_dtype if out_dtype is not None else torch.bfloat16 if like is None else like.dtype
+        P = bias.dtype if bias is not None else torch.bfloat16 if gate is None else gate.dtype
+        T = 1 if gate is None else gate.shape[0]
+        rows, vec = (M, N), (N, K // GROUP)
+        fit = (dev >= 0 and (yt is torch.bfloat16 or yt is torch.float32) and (P is torch.bfloat16 or P is torch.float32) and
+               (T == 1 or (T > 1 and segment_ids is not None)) and
+               _fit(dev, (x, torch.bfloat16, (M, K)), (codes, torch.int32, (N, K * bits // 32)),
+                    (scales, torch.float16, vec), (biases, torch.float16, vec)) and
+               (bias is None or _fit(dev, (bias, P, (N,)))) and (gate is None or _fit(dev, (gate, P, (T, N)))) and
+               (residual is None or _fit(dev, (residual, yt, rows))) and (out is None or _fit(dev, (out, yt, rows))) and
+               (segment_ids is None or _fit(dev, (segment_ids, torch.int32, (M,)))))
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        fit = False
+    if not fit:
+        _refuse(x, codes, scales, biases, bias, activation, gate, residual, segment_ids, out, out_dtype, bits)
+    _need_workspace(workspace, dev)
+    name = "qlinear_epilogue_forward" if bits == 4 else "qlinear8_epilogue_forward"
+
+    def call(st):
+        y = _new(x, rows, yt) if out is None else out
+        ws = x.new_empty(_workspace(dev, M, K, N, bits) // 2) if workspace is None else workspace
+        # without a gate every segment is as good as any other
+        _check(getattr(L, name)(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(), _ptr(bias), act,
+                                _ptr(gate), _BF16 if P is torch.bfloat16 else _F32, _ptr(residual), _ptr(segment_ids),
+                                T if gate is not None else 2 ** 31 - 1, y.data_ptr(),
+                                _BF16 if yt is torch.bfloat16 else _F32, M, K, N, GROUP, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), st), name)
+        return y
+    return _on_stream(dev, stream, call)
+
+
+def _refuse(x, codes, scales, biases, bias, activation, gate, residual, segment_ids, out, out_dtype, bits):
+    """Raises for the first argument of _forward_epilogue() that does not fit, by its name."""
     _need_dims(x, 2, "x")
     _need_dims(codes, 2, "codes")
     N, K = _weights_shape(codes, scales, bits)
@@ -76,32 +115,12 @@ def _forward_epilogue(x, codes, scales, biases, bias, activation, gate, residual
         raise ValueError("gate holds no segments")
     if segment_ids is None and T != 1:
         raise ValueError("a gate of several segments needs segment_ids")
-    dev = x.get_device()
-    optional = [(t, dtype, shape, name) for t, dtype, shape, name in
-                ((bias, P, (N,), "bias"), (gate, P, (T, N), "gate"), (residual, out_dtype, (M, N), "residual"),
-                 (segment_ids, torch.int32, (M,), "segment_ids"), (out, out_dtype, (M, N), "out")) if t is not None]
-    if not (dev >= 0 and _fit(dev, (x, torch.bfloat16, (M, K)), (codes, torch.int32, (N, K * bits // 32)),
-                              (scales, torch.float16, (N, K // GROUP)), (biases, torch.float16, (N, K // GROUP)),
-                              *[o[:3] for o in optional])):
-        _need_cuda(x, "x", torch.bfloat16, (M, K))
-        _need_cuda(codes, "codes", torch.int32, (N, K * bits // 32))
-        _need_cuda(scales, "scales", torch.float16, (N, K // GROUP))
-        _need_cuda(biases, "biases", torch.float16, (N, K // GROUP))
-        for t, dtype, shape, name in optional:
+    tensors = [(x, torch.bfloat16, (M, K), "x"), (codes, torch.int32, (N, K * bits // 32), "codes"),
+               (scales, torch.float16, (N, K // GROUP), "scales"), (biases, torch.float16, (N, K // GROUP), "biases"),
+               (bias, P, (N,), "bias"), (gate, P, (T, N), "gate"), (residual, out_dtype, (M, N), "residual"),
+               (segment_ids, torch.int32, (M,), "segment_ids"), (out, out_dtype, (M, N), "out")]
+    for i, (t, dtype, shape, name) in enumerate(tensors):
+        if t is not None or i < 4:
             _need_cuda(t, name, dtype, shape)
-        _same_device(x.device, [("codes", codes), ("scales", scales), ("biases", biases)] +
-                     [(name, t) for t, _, _, name in optional])
-    _need_workspace(workspace, dev)
-    name = "qlinear_epilogue_forward" if bits == 4 else "qlinear8_epilogue_forward"
-
-    def call(st):
-        y = _new(x, (M, N), out_dtype) if out is None else out
-        ws = x.new_empty(_workspace(dev, M, K, N, bits) // 2) if workspace is None else workspace
-        # without a gate every segment is as good as any other
-        _check(getattr(L, name)(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(), _ptr(bias),
-                                ACTIVATIONS[activation], _ptr(gate), _BF16 if P == torch.bfloat16 else _F32,
-                                _ptr(residual), _ptr(segment_ids), T if gate is not None else 2 ** 31 - 1, y.data_ptr(),
-                                _BF16 if out_dtype == torch.bfloat16 else _F32, M, K, N, GROUP, ws.data_ptr(),
-                                ws.numel() * ws.element_size(), st), name)
-        return y
-    return _on_stream(dev, stream, call)
+    _same_device(x.device, [(name, t) for t, _, _, name in tensors])
+    raise ValueError("the arguments do not fit together")

@@ -2,11 +2,11 @@
 from __future__ import annotations
 
 import math
-from ctypes import byref
+import struct
 
 import torch
 
-from ._lib import Heads, _BF16, _F32, _check, _dtype_code, _need_cuda, _need_dims, _on_stream, _ptr, lib
+from ._lib import _BF16, _F32, _check, _dtype_code, _fit, _need_cuda, _need_dims, _on_stream, _ptr, _same_device, lib
 
 HEAD_MAX_D = 512
 _POSITIONS = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
@@ -70,79 +70,125 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor | None = None, positions: to
                   q_out, k_out, stream)
 
 
-def _check_heads(t, name: str, dtype, M: int, D: int, dev: int) -> None:
-    """t is [M][H][D] of that type on device `dev`, its heads' elements side by side."""
-    _need_dims(t, 3, name)
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others, got {t.device}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[0] != M or t.shape[2] != D:
-        raise ValueError(f"{name} must have {M} tokens of heads of {D}, got shape {tuple(t.shape)}")
-    if t.stride(2) != 1 and D > 1:
-        raise ValueError(f"the elements of a head of {name} must lie side by side")
+_ENTRY = struct.Struct("@PPqqqqPi4x")       # ql_heads
+
+
+def _entry(t: torch.Tensor, o: torch.Tensor, weight) -> bytes:
+    """ql_heads of one tensor of heads, as it is read and as it is written."""
+    a, b, _ = t.stride()
+    c, d, _ = o.stride()
+    return _ENTRY.pack(t.data_ptr(), o.data_ptr(), a, b, c, d, 0 if weight is None else weight.data_ptr(), t.shape[1])
+
+
+def _side_by_side(t: torch.Tensor, dtype, shape, dev: int) -> bool:
+    """t is [M][H][D] of that shape, type and device, the elements of a head side by side."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and (t.stride(2) == 1 or shape[2] == 1)
 
 
 def _heads(name, q, k, positions, rotary, norm, q_weight, k_weight, eps, adjacent, segment_ids, q_out, k_out, stream):
     L = lib()
-    _need_dims(q, 3, "q" if norm else "x")
-    M, _, D = q.shape
-    dt, dev = _dtype_code(q, "q" if norm else "x"), q.get_device()
-    _check_heads(q, "q" if norm else "x", q.dtype, M, D, dev)
-    if q_out is not None:
-        _check_heads(q_out, "q_out" if norm else "out", q.dtype, M, D, dev)
-        if q_out.shape != q.shape:
-            raise ValueError("an output must have its input's shape")
-    if k is not None:
-        _check_heads(k, "k", q.dtype, M, D, dev)
-        if k_out is not None:
-            _check_heads(k_out, "k_out", q.dtype, M, D, dev)
-            if k_out.shape != k.shape:
-                raise ValueError("an output must have its input's shape")
-    elif k_weight is not None or k_out is not None:
-        raise ValueError("k_weight and k_out need k")
-    W = q_weight.dtype if isinstance(q_weight, torch.Tensor) else k_weight.dtype if isinstance(k_weight, torch.Tensor) \
-        else torch.float32
-    if W not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"the weights must be bfloat16 or float32, got {W}")
     turns = axes = None
-    A = P = pos_type = 0
-    if (positions is None) != (rotary is None):
-        raise ValueError("positions and rotary belong together")
-    if rotary is not None:
-        turns, axes = rotary
-        _need_dims(positions, 2, "positions")
-        _need_dims(turns, 1, "rotary's turns")
-        A, P = positions.shape[0], turns.shape[0]
-        if positions.dtype not in _POSITIONS:
-            raise ValueError(f"positions must be int32, int64 or float32, got {positions.dtype}")
-        pos_type = _POSITIONS[positions.dtype]
-        if A < 1 or P < 1 or 2 * P > D:
-            raise ValueError(f"rotary turns {P} pairs of heads of {D} by {A} axes")
-    elif not norm:
-        raise ValueError("positions and rotary must be given")
-    for t, dtype, shape, what in ((q_weight, W, (D,), "q_weight"), (k_weight, W, (D,), "k_weight"),
-                                  (positions, None if positions is None else positions.dtype, (A, M), "positions"),
-                                  (turns, torch.float64, (P,), "rotary's turns"), (axes, torch.int32, (P,), "rotary's axes"),
-                                  (segment_ids, torch.int32, (M,), "segment_ids")):
-        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or
-                              t.get_device() != dev or not t.is_contiguous()):
-            _need_cuda(t, what, dtype, shape)
-            raise ValueError(f"{what} must be on {q.device}, got {t.device}")
-
-    def entry(t, o, w):
-        st, so = t.stride(), o.stride()
-        return Heads(t.data_ptr(), o.data_ptr(), st[0], st[1], so[0], so[1], _ptr(w), t.shape[1])
+    A = P = 0
+    # one pass over arguments that are right; where it fails, the checks by name say what is wrong
+    try:
+        dt, shape, dev = q.dtype, q.shape, q.get_device()
+        M, _, D = shape
+        fit = (dev >= 0 and (dt is torch.bfloat16 or dt is torch.float32) and (q.stride(2) == 1 or D == 1) and
+               (q_out is None or _side_by_side(q_out, dt, shape, dev)))
+        if k is None:
+            fit = fit and k_out is None and k_weight is None
+        else:
+            kshape = k.shape
+            fit = (fit and kshape[0] == M and kshape[2] == D and _side_by_side(k, dt, kshape, dev) and
+                   (k_out is None or _side_by_side(k_out, dt, kshape, dev)))
+        given = q_weight if q_weight is not None else k_weight
+        W = torch.float32 if given is None else given.dtype
+        fit = (fit and (W is torch.bfloat16 or W is torch.float32) and
+               (q_weight is None or _fit(dev, (q_weight, W, (D,)))) and
+               (k_weight is None or _fit(dev, (k_weight, W, (D,)))) and
+               (segment_ids is None or _fit(dev, (segment_ids, torch.int32, (M,)))))
+        pos_type = 0
+        if rotary is not None:
+            turns, axes = rotary
+            A, P = positions.shape[0], turns.shape[0]
+            pos_type = _POSITIONS[positions.dtype]
+            fit = (fit and A >= 1 and 1 <= P and 2 * P <= D and
+                   _fit(dev, (positions, positions.dtype, (A, M)), (turns, torch.float64, (P,)), (axes, torch.int32, (P,))))
+        else:
+            fit = fit and norm and positions is None
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        fit = False
+    if not fit:
+        _refuse(q, k, positions, rotary, norm, q_weight, k_weight, segment_ids, q_out, k_out)
 
     def call(st):
-        qo = q.new_empty(q.shape) if q_out is None else q_out
+        qo = q.new_empty(shape) if q_out is None else q_out
         ko = k_out if k is None or k_out is not None else k.new_empty(k.shape)
-        hq = entry(q, qo, q_weight)
-        tail = (_ptr(positions), pos_type, A, _ptr(turns), _ptr(axes), P, 1 if adjacent else 0, _ptr(segment_ids), M, D, st)
+        dtype = _BF16 if dt is torch.bfloat16 else _F32
+        pos, tu, ax = (None, None, None) if rotary is None else (positions.data_ptr(), turns.data_ptr(), axes.data_ptr())
+        seg, adj = _ptr(segment_ids), 1 if adjacent else 0
         if norm:
-            hk = None if k is None else byref(entry(k, ko, k_weight))
-            _check(L.qlinear_qk_norm_rotary(byref(hq), hk, dt, _BF16 if W is torch.bfloat16 else _F32, eps, *tail), name)
+            _check(L.qlinear_qk_norm_rotary(_entry(q, qo, q_weight), None if k is None else _entry(k, ko, k_weight), dtype,
+                                            _BF16 if W is torch.bfloat16 else _F32, eps, pos, pos_type, A, tu, ax, P, adj,
+                                            seg, M, D, st), name)
         else:
-            _check(L.qlinear_rotary_axes(byref(hq), dt, *tail), name)
+            _check(L.qlinear_rotary_axes(_entry(q, qo, None), dtype, pos, pos_type, A, tu, ax, P, adj, seg, M, D, st), name)
         return qo, ko
     return _on_stream(dev, stream, call)
+
+
+def _refuse(q, k, positions, rotary, norm, q_weight, k_weight, segment_ids, q_out, k_out):
+    """Raises for the first argument of _heads() that does not fit, by its name."""
+    qn, on = ("q", "q_out") if norm else ("x", "out")
+    _need_dims(q, 3, qn)
+    M, _, D = q.shape
+    _dtype_code(q, qn)
+    for t, of, what in ((q, q, qn), (q_out, q, on), (k, k, "k"), (k_out, k, "k_out")):
+        if t is None:
+            continue
+        if of is None:
+            raise ValueError(f"{what} needs k")
+        _need_dims(t, 3, what)
+        if not t.is_cuda or t.device != q.device:
+            raise ValueError(f"{what} must be a CUDA tensor on the device of the others, got {t.device}")
+        if t.dtype is not q.dtype:
+            raise ValueError(f"{what} must be {q.dtype}, got {t.dtype}")
+        if t.shape[0] != M or t.shape[2] != D:
+            raise ValueError(f"{what} must have {M} tokens of heads of {D}, got shape {tuple(t.shape)}")
+        if t.shape != of.shape:
+            raise ValueError(f"{what} must have its input's shape {tuple(of.shape)}, got {tuple(t.shape)}")
+        if t.stride(2) != 1:
+            raise ValueError(f"the elements of a head of {what} must lie side by side")
+    if k is None and k_weight is not None:
+        raise ValueError("k_weight needs k")
+    given = q_weight if q_weight is not None else k_weight
+    if given is not None:
+        _need_dims(given, 1, "q_weight" if q_weight is not None else "k_weight")
+        if given.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"the weights must be bfloat16 or float32, got {given.dtype}")
+        for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if t is not None:
+                _need_cuda(t, what, given.dtype, (D,))
+                _same_device(q.device, ((what, t),))
+    if segment_ids is not None:
+        _need_cuda(segment_ids, "segment_ids", torch.int32, (M,))
+        _same_device(q.device, (("segment_ids", segment_ids),))
+    if (positions is None) != (rotary is None):
+        raise ValueError("positions and rotary belong together")
+    if rotary is None:
+        raise ValueError("positions and rotary must be given")
+    if not isinstance(rotary, (tuple, list)) or len(rotary) != 2:
+        raise ValueError("rotary must be (turns, axes)")
+    turns, axes = rotary
+    _need_dims(positions, 2, "positions")
+    _need_dims(turns, 1, "rotary's turns")
+    if positions.dtype not in _POSITIONS:
+        raise ValueError(f"positions must be int32, int64 or float32, got {positions.dtype}")
+    A, P = positions.shape[0], turns.shape[0]
+    if A < 1 or P < 1 or 2 * P > D:
+        raise ValueError(f"rotary turns {P} pairs of heads of {D} by {A} axes")
+    for t, dtype, shape, what in ((positions, positions.dtype, (A, M), "positions"), (turns, torch.float64, (P,), "rotary's turns"),
+                                  (axes, torch.int32, (P,), "rotary's axes")):
+        _need_cuda(t, what, dtype, shape)
+        _same_device(q.device, ((what, t),))
+    raise ValueError("the arguments do not fit together")

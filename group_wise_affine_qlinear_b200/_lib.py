@@ -30,13 +30,6 @@ _lock = threading.Lock()
 _lib = None
 
 
-class Heads(ctypes.Structure):
-    """ql_heads of include/qlinear.h: one tensor of heads, as it is read and as it is written."""
-    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_token", ctypes.c_int64),
-                ("in_head", ctypes.c_int64), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
-                ("weight", ctypes.c_void_p), ("heads", ctypes.c_int32)]
-
-
 class QLinearError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -136,9 +129,9 @@ def load_library(path: str) -> ctypes.CDLL:
     L.qlinear8_epilogue_forward.argtypes = epilogue
     L.qlinear8_epilogue_forward.restype = ctypes.c_int
     rotary = [vp, ctypes.c_int, i32, vp, vp, i32, i32, vp, i64, i64, vp]       # positions .. stream
-    L.qlinear_rotary_axes.argtypes = [ctypes.POINTER(Heads), ctypes.c_int] + rotary
+    L.qlinear_rotary_axes.argtypes = [vp, ctypes.c_int] + rotary          # (a ql_heads: its bytes, or a pointer)
     L.qlinear_rotary_axes.restype = ctypes.c_int
-    L.qlinear_qk_norm_rotary.argtypes = [ctypes.POINTER(Heads)] * 2 + [ctypes.c_int, ctypes.c_int, f32] + rotary
+    L.qlinear_qk_norm_rotary.argtypes = [vp, vp] + [ctypes.c_int, ctypes.c_int, f32] + rotary
     L.qlinear_qk_norm_rotary.restype = ctypes.c_int
     L.qlinear_test_stall.argtypes = [i32, ctypes.c_uint64]
     L.qlinear_test_stall.restype = ctypes.c_int

@@ -43,8 +43,7 @@ __device__ __forceinline__ float silu(float z) { return z * rcp_fast(1.0f + exp2
 // z Phi(z) with 1 - erf from Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26 (absolute error below
 // 1.5e-7): where the library's erff takes some forty instructions and a branch, this takes a dozen.
 __device__ __forceinline__ float gelu(float z) {
-    const float a = fabsf(z) * 0.70710678f;
-    const float t = rcp_fast(fmaf(0.3275911f, a, 1.0f));
+    const float t = rcp_fast(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
     const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f), 0.5f * 1.421413741f),
                                         0.5f * -0.284496736f), 0.5f * 0.254829592f);
     const float tail = poly * exp2_fast(-0.5f * kLog2e * z * z);       // 1 - Phi(|z|)

@@ -385,22 +385,25 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
                 const auto finish = [&](auto res, auto all, uint32_t mask, const float4 w) {
                     constexpr bool kRes = decltype(res)::value, kAll = decltype(all)::value;
                     const float w4[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t b[4][4] = {};
+                    if constexpr (kRes && kBf16Out) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) ptx::ldmatrix_x4_trans(stage + 512 * j + mat_off, b[j]);
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const bool in0 = kAll || ((mask >> (8 * j + lt)) & 1u) != 0;
                         const bool in1 = kAll || ((mask >> (8 * j + lt + 1)) & 1u) != 0;
                         if constexpr (kBf16Out) {
-                            uint32_t b[4] = {0u, 0u, 0u, 0u};
-                            if constexpr (kRes) ptx::ldmatrix_x4_trans(stage + 512 * j + mat_off, b);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const uint32_t* a = &v[i >> 1][4 * j + 2 * (i & 1)];
-                                const float o0 = bf16_lo(b[i]), o1 = bf16_hi(b[i]);
+                                const float o0 = bf16_lo(b[j][i]), o1 = bf16_hi(b[j][i]);
                                 const float y0 = kRes ? fmaf(w4[i], __uint_as_float(a[0]), o0) : w4[i] * __uint_as_float(a[0]);
                                 const float y1 = kRes ? fmaf(w4[i], __uint_as_float(a[1]), o1) : w4[i] * __uint_as_float(a[1]);
-                                b[i] = pack_bf16x2(in0 ? y0 : o0, in1 ? y1 : o1);
+                                b[j][i] = pack_bf16x2(in0 ? y0 : o0, in1 ? y1 : o1);
                             }
-                            ptx::stmatrix_x4_trans(stage + 512 * j + mat_off, b);
+                            ptx::stmatrix_x4_trans(stage + 512 * j + mat_off, b[j]);
                         } else {
                             uint32_t at[8];
                             float r[8];

@@ -9,7 +9,6 @@ import torch
 
 import group_wise_affine_qlinear_b200 as ql
 from group_wise_affine_qlinear_b200 import build as qb
-from group_wise_affine_qlinear_b200._lib import Heads
 from oracle import qlinear_oracle as O
 
 
@@ -17,6 +16,13 @@ from oracle import qlinear_oracle as O
 def L():
     qb.build()
     return ql.lib()
+
+
+class Heads(ctypes.Structure):
+    """ql_heads of include/qlinear.h."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_token", ctypes.c_int64),
+                ("in_head", ctypes.c_int64), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("heads", ctypes.c_int32)]
 
 
 # ------------------------------------------------------------------ the oracle
@@ -220,6 +226,19 @@ def test_rotary_refusals(L):
 
 
 # ------------------------------------------------------------------ the Python binding
+
+def test_the_binding_lays_out_a_set_of_heads():
+    """The bytes that the binding passes are the C struct's."""
+    from group_wise_affine_qlinear_b200 import _heads
+    x = torch.zeros((4, 6, 32), dtype=torch.bfloat16)
+    t, o, w = x[:, 1:4], torch.zeros((3, 4, 32), dtype=torch.bfloat16).transpose(0, 1), torch.zeros(32)
+    raw = _heads._entry(t, o, w)
+    assert len(raw) == ctypes.sizeof(Heads)
+    h = Heads.from_buffer_copy(raw)
+    assert (h.in_, h.out, h.weight, h.heads) == (t.data_ptr(), o.data_ptr(), w.data_ptr(), 3)
+    assert (h.in_token, h.in_head, h.out_token, h.out_head) == (192, 32, 32, 128)
+    assert Heads.from_buffer_copy(_heads._entry(t, o, None)).weight is None
+
 
 def test_host_tensors_are_refused():
     x = torch.zeros((4, 256), dtype=torch.bfloat16)

@@ -1499,14 +1499,19 @@ ql_status check_heads(const ql_heads& q, int64_t M, int64_t D, int64_t unit, ql_
     return by_token || by_head ? QL_OK : QL_ERR_INVALID_ARG;
 }
 
+template <bool kF32, bool kAdjacent, int G>
+void launch_heads_lanes(const rotary::Params& p, dim3 grid, cudaStream_t st) {
+    if (p.D == 16 * G) rotary::heads_kernel<kF32, kAdjacent, G, true><<<grid, 32 * rotary::kWarps, 0, st>>>(p);
+    else rotary::heads_kernel<kF32, kAdjacent, G, false><<<grid, 32 * rotary::kWarps, 0, st>>>(p);
+}
+
 template <bool kF32, bool kAdjacent>
 ql_status launch_heads(const rotary::Params& p, int G, int64_t units, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>((units + rotary::kWarps - 1) / rotary::kWarps));
-    constexpr int kBlock = 32 * rotary::kWarps;
-    if (G == 4) rotary::heads_kernel<kF32, kAdjacent, 4><<<grid, kBlock, 0, st>>>(p);
-    else if (G == 8) rotary::heads_kernel<kF32, kAdjacent, 8><<<grid, kBlock, 0, st>>>(p);
-    else if (G == 16) rotary::heads_kernel<kF32, kAdjacent, 16><<<grid, kBlock, 0, st>>>(p);
-    else rotary::heads_kernel<kF32, kAdjacent, 32><<<grid, kBlock, 0, st>>>(p);
+    if (G == 4) launch_heads_lanes<kF32, kAdjacent, 4>(p, grid, st);
+    else if (G == 8) launch_heads_lanes<kF32, kAdjacent, 8>(p, grid, st);
+    else if (G == 16) launch_heads_lanes<kF32, kAdjacent, 16>(p, grid, st);
+    else launch_heads_lanes<kF32, kAdjacent, 32>(p, grid, st);
     return launch_status();
 }
 

@@ -44,6 +44,13 @@ __device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy16_async(void* dst, const void* src, bool inside) {
     copy16_async(smem_addr(dst), src, inside);
 }
+template <bool kThroughL1>
+__device__ __forceinline__ void copy16_async_of(void* dst, const void* src) {
+    if constexpr (kThroughL1)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the thread's last n groups have landed.
 template <int n>

@@ -19,6 +19,7 @@ namespace rotary {
 
 constexpr int kMaxD = 512;             // 32 lanes x 16 elements
 constexpr int kWarps = 4;
+constexpr int kStages = 4;
 
 struct Heads {
     const void* in;
@@ -43,33 +44,93 @@ struct Params {
     float eps, inv_d;
 };
 
-__device__ __forceinline__ double position(const Params& p, int axis, int64_t m) {
-    const int64_t i = axis * p.M + m;
+__device__ __forceinline__ double position(const Params& p, int64_t i) {
     if (p.pos_type == QL_POS_I32) return static_cast<double>(__ldg(static_cast<const int*>(p.pos) + i));
     if (p.pos_type == QL_POS_I64) return static_cast<double>(__ldg(static_cast<const long long*>(p.pos) + i));
     return static_cast<double>(__ldg(static_cast<const float*>(p.pos) + i));
 }
 
-// A token's heads (or its part of them) per warp, 32 / G heads at a time.  kAdjacent: pairs (2 i, 2 i + 1).
-template <bool kF32, bool kAdjacent, int G>
-__global__ void __launch_bounds__(32 * kWarps) heads_kernel(const Params p) {
-    using norm::Raw;
-    constexpr int kPer = 32 / G;                       // heads at a time
-    constexpr int kOwn = 8 / kPer;                     // angles a lane computes; the others' come by shuffles
+__device__ __forceinline__ float rsqrt_fast(float v) {  // 2 units; a subnormal counts as zero
+    float o;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
+    return o;
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+    const float2 f = norm::halves(v);
+    return norm::pair_of(f.y, f.x);
+}
+
+// A token's heads (or its part of them) per warp, kPer = 32 / G heads at a time.  kAdjacent: pairs (2 i, 2 i + 1).  kFull:
+// D = 16 G, every lane has both of its pieces.
+template <bool kF32, bool kAdjacent, int G, bool kFull>
+__global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const Params p) {
+    using norm::F8;
+    __shared__ uint4 ring[kWarps][kStages][kF32 ? 4 : 2][32];
+    __shared__ float4 kept[kWarps][4][32];             // cosines and sines of a lane
+    constexpr int kPer = 32 / G;
+    constexpr int kOwn = 8 / kPer;                     // angles a lane forms; the others' come by shuffles
+    constexpr int kSize = kF32 ? 4 : 2;
     const int lane = static_cast<int>(threadIdx.x & 31), slot = lane & (G - 1), which = lane / G;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t m = unit / p.parts;
-    const int part = static_cast<int>(unit - m * p.parts);
+    int64_t m = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    int part = 0;
+    if (p.parts > 1) {
+        part = static_cast<int>(m % p.parts);
+        m /= p.parts;
+    }
     if (m >= p.M || (p.seg != nullptr && __ldg(p.seg + m) < 0)) return;
 
     // the lane's two pieces of 8 elements: 8 pairs of the turned part, or what is left behind it
     const bool turned = slot < p.P / 8;
     const int ea = kAdjacent || !turned ? 16 * slot : 8 * slot;
     const int eb = turned && !kAdjacent ? ea + p.P : ea + 8;
-    const bool has_a = ea < p.D && slot * 16 < p.D, has_b = has_a && eb < p.D;
+    const bool has_a = kFull || 16 * slot < p.D, has_b = kFull || (has_a && eb < p.D);
 
-    float c[8], s[8];
+    // the warp's groups of kPer heads: [lo, hi) of the queries', then of the keys'
+    const int nq = (p.set[0].heads + kPer - 1) / kPer, groups = nq + (p.set[1].heads + kPer - 1) / kPer;
+    int g0 = 0, g1 = groups;
+    if (p.parts > 1) {
+        g0 = static_cast<int>(static_cast<int64_t>(part) * groups / p.parts);
+        g1 = static_cast<int>(static_cast<int64_t>(part + 1) * groups / p.parts);
+    }
+    const auto head_in = [&](int set, int g) {
+        const Heads& hs = p.set[set];
+        return static_cast<const uint8_t*>(hs.in) + (m * hs.in_token + static_cast<int64_t>(g * kPer + which) * hs.in_head + ea) * kSize;
+    };
+    // The groups pass through a ring in shared memory, every lane copying and reading its own pieces: kStages - 1 of them
+    // are on their way at any time, the first while the angles are formed.
+    const int warp = static_cast<int>(threadIdx.x >> 5);
+    // (Lanes past a head's end or the last head copy nothing.  The two vectors of 8 fp32, and the two pieces of 16
+    // neighbours, share their 32-byte sectors: those copies go through L1, so that a sector is fetched once.)
+    constexpr bool kThroughL1 = kF32 || kAdjacent;
+    int fset = g0 < nq ? 0 : 1, fstage = 0, fend = fset ? g1 : min(g1, nq), fg = g0;       // what is copied next
+    int fleft = p.set[fset].heads - (g0 - fset * nq) * kPer - which;                       // > 0: the lane's head exists
+    int64_t fstep = p.set[fset].in_head * (kPer * kSize);
+    const uint8_t* from = head_in(fset, g0 - fset * nq);
+    const auto fetch = [&] {
+        if (fg < fend) {
+            uint4 (*to)[32] = ring[warp][fstage];
+#pragma unroll
+            for (int v = 0; v < (kF32 ? 2 : 1); ++v) {
+                if (fleft > 0 && has_a) ptx::copy16_async_of<kThroughL1>(&to[v][lane], from + 16 * v);
+                if (fleft > 0 && has_b) ptx::copy16_async_of<kThroughL1>(&to[(kF32 ? 2 : 1) + v][lane], from + (eb - ea) * kSize + 16 * v);
+            }
+            fleft -= kPer;
+            from += fstep;
+            if (++fg == nq && fg < g1) {
+                fend = g1;
+                fleft = p.set[1].heads - which;
+                fstep = p.set[1].in_head * (kPer * kSize);
+                from = head_in(1, 0);
+            }
+        }
+        fstage = (fstage + 1) % kStages;
+        ptx::copy_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+
     {
+        float c[8], s[8];
         float oc[kOwn], os[kOwn];
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
@@ -79,7 +140,7 @@ __global__ void __launch_bounds__(32 * kWarps) heads_kernel(const Params p) {
             if (turned) {
                 const int axis = __ldg(p.axes + pair);
                 if (static_cast<unsigned>(axis) < static_cast<unsigned>(p.A)) {
-                    double t = position(p, axis, m) * __ldg(p.turns + pair);
+                    double t = position(p, axis * p.M + m) * __ldg(p.turns + pair);
                     t -= rint(t);
                     sincospif(2.0f * static_cast<float>(t), &os[i], &oc[i]);
                 } else {
@@ -92,85 +153,100 @@ __global__ void __launch_bounds__(32 * kWarps) heads_kernel(const Params p) {
             c[i] = __shfl_sync(0xFFFFFFFFu, oc[i % kOwn], (i / kOwn) * G + slot);
             s[i] = __shfl_sync(0xFFFFFFFFu, os[i % kOwn], (i / kOwn) * G + slot);
         }
-    }
-
-    const int first[2] = {0, (p.set[0].heads + kPer - 1) / kPer};
-    const int groups = first[1] + (p.set[1].heads + kPer - 1) / kPer;
-    const int g0 = static_cast<int>(static_cast<int64_t>(part) * groups / p.parts);
-    const int g1 = static_cast<int>(static_cast<int64_t>(part + 1) * groups / p.parts);
-    for (int k = 0; k < 2; ++k) {
-        const Heads& hs = p.set[k];
-        const int lo = max(g0, first[k]), hi = k == 0 ? min(g1, first[1]) : g1;
-        if (lo >= hi) continue;
-        norm::F8 wa = norm::splat(1.0f), wb = wa;
-        if (p.norm && hs.weight != nullptr) {
-            if (has_a) wa = norm::load_params(hs.weight, p.weight_f32, ea);
-            if (has_b) wb = norm::load_params(hs.weight, p.weight_f32, eb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            kept[warp][i][lane] = make_float4(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]);
+            kept[warp][2 + i][lane] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
         }
-        for (int g = lo; g < hi; ++g) {
-            const int h = (g - first[k]) * kPer + which;
-            const bool live = h < hs.heads;
-            norm::F8 a = norm::splat(0.0f), b = a;
-            const int64_t at = m * hs.in_token + h * hs.in_head;
-            Raw<kF32> ra, rb;
-            if (live && has_a) {
-                norm::fetch<kF32>(hs.in, at + ea, ra);
-                if (has_b) norm::fetch<kF32>(hs.in, at + eb, rb);
-                a = norm::unpack<kF32>(ra);
-                if (has_b) b = norm::unpack<kF32>(rb);
+    }
+    int stage = 0;
+
+    for (int set = 0; set < 2; ++set) {
+        const Heads& hs = p.set[set];
+        const int lo = set == 0 ? g0 : max(g0 - nq, 0), hi = set == 0 ? min(g1, nq) : g1 - nq;
+        if (lo >= hi) continue;
+        // Weights and angles in one: with (a, b) a lane's pieces, their outputs are a ca + b sa and b cb + a sb; neighbours
+        // are pairs within a piece, there x (cos, cos) + swapped x (-sin, sin), and the weights of the swapped x swapped.
+        F8 ca = norm::splat(1.0f), cb = ca, sa, sb;
+        if (p.norm && hs.weight != nullptr) {
+            if (has_a) ca = norm::load_params(hs.weight, p.weight_f32, ea);
+            if (has_b) cb = norm::load_params(hs.weight, p.weight_f32, eb);
+        }
+        if (turned) {
+            float c[8], s[8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                *reinterpret_cast<float4*>(c + 4 * i) = kept[warp][i][lane];
+                *reinterpret_cast<float4*>(s + 4 * i) = kept[warp][2 + i][lane];
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kAdjacent) {
+                    sa.p[i] = norm::mul2(swapped(ca.p[i]), norm::pair_of(-s[i], s[i]));
+                    sb.p[i] = norm::mul2(swapped(cb.p[i]), norm::pair_of(-s[4 + i], s[4 + i]));
+                    ca.p[i] = norm::mul2(ca.p[i], norm::pair_of(c[i], c[i]));
+                    cb.p[i] = norm::mul2(cb.p[i], norm::pair_of(c[4 + i], c[4 + i]));
+                } else {
+                    const uint64_t cc = norm::pair_of(c[2 * i], c[2 * i + 1]);
+                    sa.p[i] = norm::mul2(cb.p[i], norm::pair_of(-s[2 * i], -s[2 * i + 1]));
+                    sb.p[i] = norm::mul2(ca.p[i], norm::pair_of(s[2 * i], s[2 * i + 1]));
+                    ca.p[i] = norm::mul2(ca.p[i], cc);
+                    cb.p[i] = norm::mul2(cb.p[i], cc);
+                }
+            }
+        }
+        uint8_t* to = static_cast<uint8_t*>(hs.out) +
+                      (m * hs.out_token + static_cast<int64_t>(lo * kPer + which) * hs.out_head + ea) * kSize;
+        const int64_t out_step = hs.out_head * (kPer * kSize);
+        int left = hs.heads - lo * kPer - which;       // > 0: the lane's head exists
+        for (int g = lo; g < hi; ++g, left -= kPer, to += out_step) {
+            fetch();                                   // into what was read a group ago
+            ptx::copy_async_wait<kStages - 1>();
+            norm::Raw<kF32> ra, rb;
+#pragma unroll
+            for (int v = 0; v < (kF32 ? 2 : 1); ++v) {
+                ra.q[v] = ring[warp][stage][v][lane];
+                rb.q[v] = ring[warp][stage][(kF32 ? 2 : 1) + v][lane];
+            }
+            stage = (stage + 1) % kStages;
+            F8 a = norm::unpack<kF32>(ra), b = norm::unpack<kF32>(rb);
+            if (!has_a) a = norm::splat(0.0f);         // (for the sum of squares)
+            if (!has_b) b = norm::splat(0.0f);
+            F8 inv;
             if (p.norm) {
-                const norm::F8 v[2] = {a, b};
+                const F8 v[2] = {a, b};
                 float ss = norm::sum_squares<2>(v);
 #pragma unroll
                 for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-                const norm::F8 inv = norm::splat(rsqrtf(fmaf(ss, p.inv_d, p.eps)));
-                a = norm::mul(norm::mul(a, inv), wa);
-                b = norm::mul(norm::mul(b, inv), wb);
+                inv = norm::splat(rsqrt_fast(fmaf(ss, p.inv_d, p.eps)));
             }
-            if (turned) {
-                float fa[8], fb[8];
+            F8 ya, yb;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 u = norm::halves(a.p[i]), v = norm::halves(b.p[i]);
-                    fa[2 * i] = u.x;
-                    fa[2 * i + 1] = u.y;
-                    fb[2 * i] = v.x;
-                    fb[2 * i + 1] = v.y;
+            for (int i = 0; i < 4; ++i) {
+                ya.p[i] = norm::mul2(a.p[i], ca.p[i]);
+                yb.p[i] = norm::mul2(b.p[i], cb.p[i]);
+                if (turned) {
+                    ya.p[i] = norm::fma2(kAdjacent ? swapped(a.p[i]) : b.p[i], sa.p[i], ya.p[i]);
+                    yb.p[i] = norm::fma2(kAdjacent ? swapped(b.p[i]) : a.p[i], sb.p[i], yb.p[i]);
                 }
-                if constexpr (kAdjacent) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        a.p[i] = norm::pair_of(fa[2 * i] * c[i] - fa[2 * i + 1] * s[i], fa[2 * i + 1] * c[i] + fa[2 * i] * s[i]);
-                        b.p[i] = norm::pair_of(fb[2 * i] * c[4 + i] - fb[2 * i + 1] * s[4 + i],
-                                               fb[2 * i + 1] * c[4 + i] + fb[2 * i] * s[4 + i]);
-                    }
+                if (p.norm) {
+                    ya.p[i] = norm::mul2(ya.p[i], inv.p[i]);
+                    yb.p[i] = norm::mul2(yb.p[i], inv.p[i]);
+                }
+            }
+            const auto store = [&](const F8& v, uint8_t* q) {
+                if constexpr (kF32) {
+                    reinterpret_cast<ulonglong2*>(q)[0] = make_ulonglong2(v.p[0], v.p[1]);
+                    reinterpret_cast<ulonglong2*>(q)[1] = make_ulonglong2(v.p[2], v.p[3]);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        a.p[i] = norm::pair_of(fa[2 * i] * c[2 * i] - fb[2 * i] * s[2 * i],
-                                               fa[2 * i + 1] * c[2 * i + 1] - fb[2 * i + 1] * s[2 * i + 1]);
-                        b.p[i] = norm::pair_of(fb[2 * i] * c[2 * i] + fa[2 * i] * s[2 * i],
-                                               fb[2 * i + 1] * c[2 * i + 1] + fa[2 * i + 1] * s[2 * i + 1]);
-                    }
+                    *reinterpret_cast<uint4*>(q) = norm::pack_bf16x8(v);
                 }
-            }
-            if (live && has_a) {
-                const int64_t to = m * hs.out_token + h * hs.out_head;
-                const auto store = [&](const norm::F8& v, int64_t i) {
-                    if constexpr (kF32) {
-                        ulonglong2* q = reinterpret_cast<ulonglong2*>(static_cast<float*>(hs.out) + i);
-                        q[0] = make_ulonglong2(v.p[0], v.p[1]);
-                        q[1] = make_ulonglong2(v.p[2], v.p[3]);
-                    } else {
-                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(hs.out) + i) = norm::pack_bf16x8(v);
-                    }
-                };
-                store(a, to + ea);
-                if (has_b) store(b, to + eb);
-            }
+            };
+            if (left > 0 && has_a) store(ya, to);
+            if (left > 0 && has_b) store(yb, to + (eb - ea) * kSize);
         }
     }
+    ptx::copy_async_wait<0>();
 }
 
 }  // namespace rotary

@@ -15,6 +15,7 @@
 #include "ql_common.cuh"
 #include "ql_dequant.cuh"
 #include "ql_epilogue.cuh"
+#include "ql_few.cuh"
 #include "ql_gemv.cuh"
 #include "ql_lora.cuh"
 #include "ql_norm.cuh"
@@ -1151,6 +1152,34 @@ ql_status check_epilogue(const EpilogueArgs& a) {
     return QL_OK;
 }
 
+// Few tokens of a weight of up to 32 MiB of codes go through the one-launch kernel.  Against the streaming path, whole calls
+// of 1 token in a graph: 4 bits 512 -> 4608 3.0 us to 7.0, 4608 -> 4608 7.0 to 11.4, 12288 -> 4608 14.7 to 15.2, 4608 ->
+// 13824 17.2 to 16.6, 53248 -> 4608 57 to 40; 8 bits 512 -> 18432 5.2 to 9.3, 4608 -> 4608 9.1 to 11.7; of 8 tokens 4.0 to
+// 7.3, 7.7 to 12.2, 16.1 to 16.1, 19.1 to 16.9, 60 to 41; 6.4 to 9.8, 9.7 to 12.4.
+bool few_pays(int64_t M, int64_t K, int64_t N, int bits) { return M <= few::kMaxM && code_bytes(K, N, bits) <= (32u << 20); }
+
+// Warps of a CTA that share 16 rows (1 to 8), each of four groups of K at least.
+int few_slices(int64_t G) { return G >= 32 ? 8 : G >= 16 ? 4 : G >= 8 ? 2 : 1; }
+
+ql_status run_few(const void* x, const uint32_t* codes, const void* scales, const void* biases, void* y, bool bf16_out,
+                  int64_t M, int64_t K, int64_t N, int bits, const epi::Epilogue& e, cudaStream_t st) {
+    const int slices = few_slices(K / kGroup);
+    const int rows = few::kRows * few::kWarps / slices;
+    const unsigned grid = static_cast<unsigned>((N + rows - 1) / rows);
+    const auto launch = [&](auto k) {
+        k<<<grid, 32 * few::kWarps, 0, st>>>(static_cast<const __nv_bfloat16*>(x), codes, static_cast<const unsigned short*>(scales),
+                                             static_cast<const unsigned short*>(biases), y, static_cast<int>(M),
+                                             static_cast<int>(K), static_cast<int>(N), slices, e);
+    };
+    prof_begin(st);
+    if (bits == 4) launch(bf16_out ? few::few_kernel<4, true> : few::few_kernel<4, false>);
+    else launch(bf16_out ? few::few_kernel<8, true> : few::few_kernel<8, false>);
+    prof_end(st);
+    set_dispatch("path=few_epilogue bits=%d rows=%d slices=%d ctas=%u launches=1 why=auto:M<=%d,codes<=32MiB", bits, few::kRows,
+                 slices, grid, few::kMaxM);
+    return launch_status();
+}
+
 // Whether [p, p + n) meets the epilogue's vectors or segments.
 bool epilogue_overlaps(const EpilogueArgs& a, int64_t M, int64_t N, const void* p, size_t n) {
     const size_t vb = static_cast<size_t>(N) * (a.e.params_f32 ? 4 : 2);
@@ -1202,6 +1231,7 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
     }
     const bool bf16 = out_dtype == QL_BF16;
     const epi::Epilogue* e = ep ? &ep->e : nullptr;
+    if (e && few_pays(M, K, N, bits)) return run_few(x, codes, scales, biases, y, bf16, M, K, N, bits, *e, stream);
     if (pl.path == QL_PATH_GEMV)
         return run_gemv(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count);
     if (pl.path == QL_PATH_TC_SKINNY)
@@ -1584,8 +1614,9 @@ ql_status heads_impl(const ql_heads* q, const ql_heads* k, ql_dtype dtype, int32
     const int G = slots <= 4 ? 4 : slots <= 8 ? 8 : slots <= 16 ? 16 : 32;
     const int per = 32 / G;
     const int groups = (p.set[0].heads + per - 1) / per + (p.set[1].heads + per - 1) / per;
-    // a warp per token; few tokens share their heads among up to 32 warps per SM
-    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(groups, 32ll * dev->sm_count / M)));
+    // a warp per token; the heads of few tokens are shared by warps, up to 8 per SM (512 tokens of 36 heads of 256: 14.3 us
+    // with 9 warps a token, 12.3 with 2; every warp forms its token's angles anew)
+    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(groups, 8ll * dev->sm_count / M)));
     const int64_t units = M * p.parts;
     if ((units + rotary::kWarps - 1) / rotary::kWarps > (1ll << 31) - 1) return QL_ERR_UNSUPPORTED;
     if (dtype == QL_F32)

@@ -1,0 +1,158 @@
+// A packed projection of up to 8 tokens with its epilogue, in one launch.
+//
+//   y[m][n] = epilogue( sum_g s(n,g) D(n,m,g) + (b(n,g) - 128 s(n,g)) X(m,g) )
+//   D = sum_{k in g} (128 + q(n,k)) x[m][k],   X = sum_{k in g} x[m][k]
+//
+// which is sum_k (s q + b) x, rearranged by group: 128 + q, for a code of 4 bits, is the bf16 whose mantissa holds q, so a
+// pair of weights takes a shift and one logical operation, and the activations are used as they are.  The tensor core
+// (mma m16n8k16, 16 weight rows x 8 tokens, fp32) sums a group's products exactly up to its own fp32 additions; X comes
+// from the same operands times ones.  8-bit codes are two nibbles, q = 16 h + l, of a product each.
+//
+// What bounds such a call is not the 0.56 bytes a weight that it reads but the launches: the streaming path's conversion,
+// stream and reduction, three kernels, take 11 us for 1 token of 4608 x 4608 (12 MB, 2 us at the memory's rate).  Here a
+// warp takes 16 rows and a slice of their groups; the warps of a CTA that share rows add up in shared memory, in order.
+#pragma once
+
+#include "ql_epilogue.cuh"
+
+namespace ql {
+namespace few {
+
+constexpr int kMaxM = 8;
+constexpr int kWarps = 8;
+constexpr int kRows = 16;              // of a warp
+constexpr int kAhead = 4;              // groups whose loads are on their way together
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 128 + q for the two codes of 4 bits at bits 0 and 16.
+__device__ __forceinline__ uint32_t weights_of(uint32_t v) { return (v & 0x000F000Fu) | 0x43004300u; }
+
+// Lane l = 4 r + t of a warp holds, of weight rows r and r + 8 and of token r, the 16 columns 16 t .. of a group: which of
+// a product's 16 columns an operand's register stands for is free as long as both operands agree.
+template <int B>
+struct Group {
+    uint32_t w[2][B == 4 ? 2 : 4];     // codes of rows r, r + 8
+    uint4 x[2];                        // token r
+};
+
+template <int B, bool kBf16Out>
+__global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* __restrict__ x, const uint32_t* __restrict__ codes,
+                                                          const unsigned short* __restrict__ scales,
+                                                          const unsigned short* __restrict__ biases, void* y, int M, int K, int N,
+                                                          int slices, const epi::Epilogue e) {
+    __shared__ float red[kWarps][kMaxM][kRows];
+    const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+    const int r = lane >> 2, t = lane & 3;
+    const int G = K / kGroup, slice = warp % slices, block = warp / slices;
+    const int blocks = kWarps / slices;                // of 16 rows per CTA
+    const int n0 = (static_cast<int>(blockIdx.x) * blocks + block) * kRows;
+    constexpr int kWords = B == 4 ? 2 : 4;             // a lane's, of a row's group
+
+    const auto load = [&](int g, Group<B>& o) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t n = min(n0 + r + 8 * h, N - 1);              // (rows past N are not stored)
+            const uint32_t* c = codes + n * (K * B / 32) + g * (2 * B) + kWords * t;
+            if constexpr (B == 4) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(c));
+                o.w[h][0] = v.x;
+                o.w[h][1] = v.y;
+            } else {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(c));
+                o.w[h][0] = v.x;
+                o.w[h][1] = v.y;
+                o.w[h][2] = v.z;
+                o.w[h][3] = v.w;
+            }
+        }
+        o.x[0] = o.x[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < M) {
+            const uint4* v = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(r) * K + g * kGroup + 16 * t);
+            o.x[0] = __ldg(v);
+            o.x[1] = __ldg(v + 1);
+        }
+    };
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};           // rows r, r, r + 8, r + 8 of tokens 2 t, 2 t + 1, ...
+    const auto work = [&](const Group<B>& o, const uint32_t (&sb)[2], int i4) {
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f}, one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr uint32_t kOnes = 0x3F803F80u;
+        const uint32_t xw[8] = {o.x[0].x, o.x[0].y, o.x[0].z, o.x[0].w, o.x[1].x, o.x[1].y, o.x[1].z, o.x[1].w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint32_t b0, b1;
+            if constexpr (B == 4) {
+                // word u / 2 of each row, its code pairs (j, j + 4) for j = 2 (u % 2) and + 1
+                const uint32_t lo = xw[4 * (u >> 1) + (u & 1)], up = xw[4 * (u >> 1) + 2 + (u & 1)];
+                b0 = __byte_perm(lo, up, 0x5410);
+                b1 = __byte_perm(lo, up, 0x7632);
+                const uint32_t p = o.w[0][u >> 1] >> (8 * (u & 1)), q = o.w[1][u >> 1] >> (8 * (u & 1));
+                mma_bf16(d, weights_of(p), weights_of(q), weights_of(p >> 4), weights_of(q >> 4), b0, b1);
+            } else {
+                // word u of each row, its code pairs (0, 2) and (1, 3), by nibbles
+                b0 = __byte_perm(xw[2 * u], xw[2 * u + 1], 0x5410);
+                b1 = __byte_perm(xw[2 * u], xw[2 * u + 1], 0x7632);
+                const uint32_t p = o.w[0][u], q = o.w[1][u];
+                mma_bf16(d, weights_of(p), weights_of(q), weights_of(p >> 8), weights_of(q >> 8), b0, b1);
+                mma_bf16(hi, weights_of(p >> 4), weights_of(q >> 4), weights_of(p >> 12), weights_of(q >> 12), b0, b1);
+            }
+            mma_bf16(one, kOnes, kOnes, kOnes, kOnes, b0, b1);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 p = half2_of(__shfl_sync(0xFFFFFFFFu, sb[i >> 1], 4 * r + i4));
+            const float s = __low2float(p), b = __high2float(p);
+            const float v = B == 4 ? d[i] : fmaf(16.0f, hi[i], d[i]);
+            acc[i] = fmaf(s, v, fmaf(fmaf(s, B == 4 ? -128.0f : -17.0f * 128.0f, b), one[i], acc[i]));
+        }
+    };
+    // The slice's groups four at a time, every load of the four on its way before the first is used.  Lane t of a row's four
+    // takes the (scale, bias) of the t-th of them: one request instead of four, each of which touches eight rows' lines.
+    static_assert(kAhead == 4, "a group for each lane of a row's four");
+    const int g_end = static_cast<int>(static_cast<int64_t>(slice + 1) * G / slices);
+    for (int g = static_cast<int>(static_cast<int64_t>(slice) * G / slices); g < g_end; g += kAhead) {
+        Group<B> o[kAhead];
+        uint32_t sb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t at = static_cast<int64_t>(min(n0 + r + 8 * h, N - 1)) * G + min(g + t, g_end - 1);
+            sb[h] = __ldg(scales + at) | static_cast<uint32_t>(__ldg(biases + at)) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (g + i < g_end) load(g + i, o[i]);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (g + i < g_end) work(o[i], sb, i);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[warp][2 * t + (i & 1)][r + 8 * (i >> 1)] = acc[i];
+    __syncthreads();
+    // the outputs of a row block: kRows rows of every token, summed over the slices in order
+    for (int i = static_cast<int>(threadIdx.x); i < blocks * M * kRows; i += 32 * kWarps) {
+        const int row = i % kRows, m = i / kRows % M, bl = i / (kRows * M);
+        const int n = (static_cast<int>(blockIdx.x) * blocks + bl) * kRows + row;
+        if (n >= N) continue;
+        const int seg = epi::segment_of(e, m);
+        if (seg < 0) continue;
+        float z = e.bias != nullptr ? epi::param(e.bias, e.params_f32, n) : 0.0f, sum = 0.0f;
+        for (int s = 0; s < slices; ++s) sum += red[bl * slices + s][m][row];
+        z += sum;
+        const int64_t at = static_cast<int64_t>(m) * N + n;
+        const float gate = e.gate != nullptr ? epi::param(e.gate, e.params_f32, static_cast<int64_t>(seg) * N + n) : 1.0f;
+        float res = 0.0f;
+        if (e.residual != nullptr)
+            res = kBf16Out ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at])
+                           : static_cast<const float*>(e.residual)[at];
+        const float o = fmaf(gate, epi::activate(e.act, z), res);
+        if constexpr (kBf16Out)
+            static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(o);
+        else
+            static_cast<float*>(y)[at] = o;
+    }
+}
+
+}  // namespace few
+}  // namespace ql

@@ -81,13 +81,17 @@ def _forward_epilogue(x, codes, scales, biases, bias, activation, gate, residual
 
     def call(st):
         y = _new(x, rows, yt) if out is None else out
-        ws = x.new_empty(_workspace(dev, M, K, N, bits) // 2) if workspace is None else workspace
+        ws, n = None, 0
+        if workspace is not None:
+            ws, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif need := _workspace(dev, M, K, N, bits):
+            scratch = x.new_empty(need // 2)               # held until the call below has been enqueued
+            ws, n = scratch.data_ptr(), need
         # without a gate every segment is as good as any other
         _check(getattr(L, name)(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(), _ptr(bias), act,
                                 _ptr(gate), _BF16 if P is torch.bfloat16 else _F32, _ptr(residual), _ptr(segment_ids),
                                 T if gate is not None else 2 ** 31 - 1, y.data_ptr(),
-                                _BF16 if yt is torch.bfloat16 else _F32, M, K, N, GROUP, ws.data_ptr(),
-                                ws.numel() * ws.element_size(), st), name)
+                                _BF16 if yt is torch.bfloat16 else _F32, M, K, N, GROUP, ws, n, st), name)
         return y
     return _on_stream(dev, stream, call)
 

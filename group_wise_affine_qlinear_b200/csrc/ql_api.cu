@@ -1220,6 +1220,7 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
         lp = lora_plan(pl, M, K, la->r, la->L, dev->sm_count);
         need = lp.workspace;
     }
+    if (ep && few_pays(M, K, N, bits)) need = 0;
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return QL_ERR_WORKSPACE;
         if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
@@ -1638,7 +1639,8 @@ EpilogueArgs epilogue_args(const void* bias, int32_t activation, const void* gat
 }
 
 size_t epilogue_workspace_impl(int64_t M, int64_t K, int64_t N, int32_t group, int bits) {
-    return workspace_impl(M, K, N, group, QL_PATH_AUTO, 0, bits);
+    const size_t n = workspace_impl(M, K, N, group, QL_PATH_AUTO, 0, bits);
+    return n != static_cast<size_t>(-1) && few_pays(M, K, N, bits) ? 0 : n;
 }
 
 }  // namespace

@@ -73,6 +73,7 @@ struct DeviceInfo {
     int sm_count = 0;
     bool fused_attr_set = false;
     bool skinny_attr_set = false;
+    bool epilogue_attr_set = false;
 };
 
 template <int NT, int B>
@@ -107,22 +108,20 @@ cudaError_t fused_smem_attr() {
     return e;
 }
 
-template <int B, int kAct>
-cudaError_t epilogue_smem_attr() {
-    using EB = typename fused::PickEpiCfg<B, true>::type;
-    using EF = typename fused::PickEpiCfg<B, false>::type;
-    const cudaError_t e = cudaFuncSetAttribute(fused::fused_gemm_kernel<true, EB, false, false, false, kAct>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, EB::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(fused::fused_gemm_kernel<false, EF, false, false, false, kAct>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, EF::kSmemBytes);
+// Shared memory of the epilogue mode's kernels.  Their warps redistribute the registers that a block is launched with: an
+// instantiation with fewer than that would wait for them until the end of days, so it is refused here.
+template <int B, int kAct, bool kBf16Out>
+bool epilogue_ready() {
+    using C = typename fused::PickEpiCfg<B, kBf16Out>::type;
+    auto k = fused::fused_gemm_kernel<kBf16Out, C, false, false, false, kAct>;
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, k) == cudaSuccess && a.numRegs >= fused::kLaunchRegs &&
+           cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) == cudaSuccess;
 }
-template <int B>
-cudaError_t epilogue_smem_attrs() {
-    for (const cudaError_t e : {epilogue_smem_attr<B, QL_ACT_NONE>(), epilogue_smem_attr<B, QL_ACT_SILU>(),
-                                epilogue_smem_attr<B, QL_ACT_GELU>(), epilogue_smem_attr<B, QL_ACT_GELU_TANH>()})
-        if (e != cudaSuccess) return e;
-    return cudaSuccess;
+template <int B, bool kBf16Out>
+bool epilogues_ready() {
+    return epilogue_ready<B, QL_ACT_NONE, kBf16Out>() && epilogue_ready<B, QL_ACT_SILU, kBf16Out>() &&
+           epilogue_ready<B, QL_ACT_GELU, kBf16Out>() && epilogue_ready<B, QL_ACT_GELU_TANH, kBf16Out>();
 }
 
 template <int NT>
@@ -148,7 +147,6 @@ ql_status device_info(DeviceInfo** out) {
         if (fused_smem_attr<4>() != cudaSuccess || fused_smem_attr<8>() != cudaSuccess ||
             fused_smem_attr<4, true>() != cudaSuccess || fused_smem_attr<4, false, true>() != cudaSuccess ||
             fused_smem_attr<8, false, true>() != cudaSuccess || fused_smem_attr<4, true, true>() != cudaSuccess ||
-            epilogue_smem_attrs<4>() != cudaSuccess || epilogue_smem_attrs<8>() != cudaSuccess ||
             prepare_smem_attr<1>() != cudaSuccess || prepare_smem_attr<2>() != cudaSuccess ||
             prepare_smem_attr<4>() != cudaSuccess)
             return QL_ERR_CUDA;
@@ -163,6 +161,15 @@ ql_status device_info(DeviceInfo** out) {
     }
     *out = &d;
     return QL_OK;
+}
+
+// The same for the epilogue mode of the fused kernel, at its first call on a device.
+ql_status prepare_epilogue(DeviceInfo* d) {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    if (!d->epilogue_attr_set)
+        d->epilogue_attr_set = epilogues_ready<4, true>() && epilogues_ready<4, false>() && epilogues_ready<8, true>() &&
+                               epilogues_ready<8, false>();
+    return d->epilogue_attr_set ? QL_OK : QL_ERR_CUDA;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -1238,6 +1245,7 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
     if (pl.path == QL_PATH_TC_SKINNY)
         return run_skinny(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count, la, &lp,
                           e);
+    if (e && pl.split_k == 1 && (s = prepare_epilogue(dev)) != QL_OK) return s;
     return run_fused(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count, la, &lp, e);
 }
 

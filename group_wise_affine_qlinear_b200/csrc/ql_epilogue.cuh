@@ -94,27 +94,36 @@ __device__ __forceinline__ float4 param4(const void* p, int f32, int64_t i) {
 }
 
 // y = epilogue of the fp32 partials [S][M][N], summed in slice order: four columns per thread, whose bias (and gate,
-// while the segment stays the same) it holds over its rows.
+// while the segment stays the same) it holds over its rows.  What the caller gave of a row is fetched a row ahead, of the
+// first one before the wait for the partials.
 template <bool kBf16Out>
 __global__ void __launch_bounds__(256) epilogue_sum_kernel(const float* __restrict__ partial, void* y, int64_t M, int N,
                                                            int S, const Epilogue e) {
     const int n = 4 * static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
-    ptx::grid_dependency_wait();                       // the partials come from the kernel before
     if (n >= N) return;
-    const float4 bias = e.bias ? param4(e.bias, e.params_f32, n) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float4 gate = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-    int held = -1;
+    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 gate = make_float4(1.0f, 1.0f, 1.0f, 1.0f), r_next = none;
+    int held = -1, seg_next = -1;
+    const auto fetch = [&](int64_t m) {
+        if (m >= M) return;
+        seg_next = segment_of(e, m);
+        if (e.residual == nullptr) return;
+        const int64_t at = m * N + n;
+        r_next = kBf16Out ? bf16x4(*reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.residual) + at))
+                          : *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + at);
+    };
+    const float4 bias = e.bias ? param4(e.bias, e.params_f32, n) : none;
+    fetch(blockIdx.y);
+    ptx::grid_dependency_wait();                       // the partials come from the kernel before
     for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
-        const int seg = segment_of(e, m);
+        const int seg = seg_next;
+        const float4 r = r_next;
+        const int64_t at = m * N + n;
+        fetch(m + gridDim.y);
         if (seg < 0) continue;
         if (e.gate != nullptr && seg != held) gate = param4(e.gate, e.params_f32, static_cast<int64_t>(seg) * N + n);
         held = seg;
-        const int64_t at = m * N + n;
-        float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (e.residual != nullptr)
-            r = kBf16Out ? bf16x4(*reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.residual) + at))
-                         : *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + at);
-        float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 z = none;
 #pragma unroll 4
         for (int s = 0; s < S; ++s) {
             const float4 v = *reinterpret_cast<const float4*>(partial + s * M * N + at);

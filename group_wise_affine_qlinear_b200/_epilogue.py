@@ -6,7 +6,7 @@ import functools
 
 import torch
 
-from ._lib import (GROUP, _BF16, _F32, _check, _fit, _need_cuda, _need_dims, _need_workspace, _new, _on_stream, _ptr,
+from ._lib import (GROUP, _BF16, _F32, _check, _fit, _need_cuda, _need_dims, _need_workspace, _new, _on_stream,
                    _same_device, _weights_shape, lib)
 
 ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
@@ -65,19 +65,26 @@ def _forward_epilogue(x, codes, scales, biases, bias, activation, gate, residual
         P = bias.dtype if bias is not None else torch.bfloat16 if gate is None else gate.dtype
         T = 1 if gate is None else gate.shape[0]
         rows, vec = (M, N), (N, K // GROUP)
+        specs = [(x, torch.bfloat16, (M, K)), (codes, torch.int32, (N, K * bits // 32)), (scales, torch.float16, vec),
+                 (biases, torch.float16, vec)]
+        if bias is not None:
+            specs.append((bias, P, (N,)))
+        if gate is not None:
+            specs.append((gate, P, (T, N)))
+        if residual is not None:
+            specs.append((residual, yt, rows))
+        if segment_ids is not None:
+            specs.append((segment_ids, torch.int32, (M,)))
+        if out is not None:
+            specs.append((out, yt, rows))
         fit = (dev >= 0 and (yt is torch.bfloat16 or yt is torch.float32) and (P is torch.bfloat16 or P is torch.float32) and
-               (T == 1 or (T > 1 and segment_ids is not None)) and
-               _fit(dev, (x, torch.bfloat16, (M, K)), (codes, torch.int32, (N, K * bits // 32)),
-                    (scales, torch.float16, vec), (biases, torch.float16, vec)) and
-               (bias is None or _fit(dev, (bias, P, (N,)))) and (gate is None or _fit(dev, (gate, P, (T, N)))) and
-               (residual is None or _fit(dev, (residual, yt, rows))) and (out is None or _fit(dev, (out, yt, rows))) and
-               (segment_ids is None or _fit(dev, (segment_ids, torch.int32, (M,)))))
+               (T == 1 or (T > 1 and segment_ids is not None)) and _fit(dev, *specs))
     except (AttributeError, IndexError, KeyError, TypeError, ValueError):
         fit = False
     if not fit:
         _refuse(x, codes, scales, biases, bias, activation, gate, residual, segment_ids, out, out_dtype, bits)
     _need_workspace(workspace, dev)
-    name = "qlinear_epilogue_forward" if bits == 4 else "qlinear8_epilogue_forward"
+    run = L.qlinear_epilogue_forward if bits == 4 else L.qlinear8_epilogue_forward
 
     def call(st):
         y = _new(x, rows, yt) if out is None else out
@@ -88,10 +95,13 @@ def _forward_epilogue(x, codes, scales, biases, bias, activation, gate, residual
             scratch = x.new_empty(need // 2)               # held until the call below has been enqueued
             ws, n = scratch.data_ptr(), need
         # without a gate every segment is as good as any other
-        _check(getattr(L, name)(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(), _ptr(bias), act,
-                                _ptr(gate), _BF16 if P is torch.bfloat16 else _F32, _ptr(residual), _ptr(segment_ids),
-                                T if gate is not None else 2 ** 31 - 1, y.data_ptr(),
-                                _BF16 if yt is torch.bfloat16 else _F32, M, K, N, GROUP, ws, n, st), name)
+        status = run(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), biases.data_ptr(),
+                     None if bias is None else bias.data_ptr(), act, None if gate is None else gate.data_ptr(),
+                     _BF16 if P is torch.bfloat16 else _F32, None if residual is None else residual.data_ptr(),
+                     None if segment_ids is None else segment_ids.data_ptr(), 2 ** 31 - 1 if gate is None else T,
+                     y.data_ptr(), _BF16 if yt is torch.bfloat16 else _F32, M, K, N, GROUP, ws, n, st)
+        if status != 0:
+            _check(status, "qlinear_epilogue_forward" if bits == 4 else "qlinear8_epilogue_forward")
         return y
     return _on_stream(dev, stream, call)
 

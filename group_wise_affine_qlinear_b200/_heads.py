@@ -6,7 +6,7 @@ import struct
 
 import torch
 
-from ._lib import _BF16, _F32, _check, _dtype_code, _fit, _need_cuda, _need_dims, _on_stream, _ptr, _same_device, lib
+from ._lib import _BF16, _F32, _check, _dtype_code, _fit, _need_cuda, _need_dims, _on_stream, _same_device, lib
 
 HEAD_MAX_D = 512
 _POSITIONS = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
@@ -89,6 +89,7 @@ def _heads(name, q, k, positions, rotary, norm, q_weight, k_weight, eps, adjacen
     L = lib()
     turns = axes = None
     A = P = 0
+    adjacent = 1 if adjacent else 0
     # one pass over arguments that are right; where it fails, the checks by name say what is wrong
     try:
         dt, shape, dev = q.dtype, q.shape, q.get_device()
@@ -103,19 +104,23 @@ def _heads(name, q, k, positions, rotary, norm, q_weight, k_weight, eps, adjacen
                    (k_out is None or _side_by_side(k_out, dt, kshape, dev)))
         given = q_weight if q_weight is not None else k_weight
         W = torch.float32 if given is None else given.dtype
-        fit = (fit and (W is torch.bfloat16 or W is torch.float32) and
-               (q_weight is None or _fit(dev, (q_weight, W, (D,)))) and
-               (k_weight is None or _fit(dev, (k_weight, W, (D,)))) and
-               (segment_ids is None or _fit(dev, (segment_ids, torch.int32, (M,)))))
+        specs = []
+        if q_weight is not None:
+            specs.append((q_weight, W, (D,)))
+        if k_weight is not None:
+            specs.append((k_weight, W, (D,)))
+        if segment_ids is not None:
+            specs.append((segment_ids, torch.int32, (M,)))
         pos_type = 0
         if rotary is not None:
             turns, axes = rotary
             A, P = positions.shape[0], turns.shape[0]
             pos_type = _POSITIONS[positions.dtype]
-            fit = (fit and A >= 1 and 1 <= P and 2 * P <= D and
-                   _fit(dev, (positions, positions.dtype, (A, M)), (turns, torch.float64, (P,)), (axes, torch.int32, (P,))))
+            specs += ((positions, positions.dtype, (A, M)), (turns, torch.float64, (P,)), (axes, torch.int32, (P,)))
+            fit = fit and A >= 1 and 1 <= P and 2 * P <= D
         else:
             fit = fit and norm and positions is None
+        fit = fit and (W is torch.bfloat16 or W is torch.float32) and _fit(dev, *specs)
     except (AttributeError, IndexError, KeyError, TypeError, ValueError):
         fit = False
     if not fit:
@@ -126,13 +131,15 @@ def _heads(name, q, k, positions, rotary, norm, q_weight, k_weight, eps, adjacen
         ko = k_out if k is None or k_out is not None else k.new_empty(k.shape)
         dtype = _BF16 if dt is torch.bfloat16 else _F32
         pos, tu, ax = (None, None, None) if rotary is None else (positions.data_ptr(), turns.data_ptr(), axes.data_ptr())
-        seg, adj = _ptr(segment_ids), 1 if adjacent else 0
+        seg = None if segment_ids is None else segment_ids.data_ptr()
         if norm:
-            _check(L.qlinear_qk_norm_rotary(_entry(q, qo, q_weight), None if k is None else _entry(k, ko, k_weight), dtype,
-                                            _BF16 if W is torch.bfloat16 else _F32, eps, pos, pos_type, A, tu, ax, P, adj,
-                                            seg, M, D, st), name)
+            status = L.qlinear_qk_norm_rotary(_entry(q, qo, q_weight), None if k is None else _entry(k, ko, k_weight), dtype,
+                                              _BF16 if W is torch.bfloat16 else _F32, eps, pos, pos_type, A, tu, ax, P,
+                                              adjacent, seg, M, D, st)
         else:
-            _check(L.qlinear_rotary_axes(_entry(q, qo, None), dtype, pos, pos_type, A, tu, ax, P, adj, seg, M, D, st), name)
+            status = L.qlinear_rotary_axes(_entry(q, qo, None), dtype, pos, pos_type, A, tu, ax, P, adjacent, seg, M, D, st)
+        if status != 0:
+            _check(status, name)
         return qo, ko
     return _on_stream(dev, stream, call)
 

@@ -8,6 +8,9 @@ Bounds, with u = 2^-24 (half an fp32 unit) and b = 2^-8 (half a bf16 unit, relat
       relative at an argument v, times e^-v |v| <= 0.37 of |z| where v is large; its division by 2^-22; Abramowitz and
       Stegun's 1 - erf by 1.5e-7, half of it times |z|
   y   |gate| e_a + 4 u (|gate a| + |residual|), + b |y| for bf16 storage
+Up to 8 tokens the one-launch kernel multiplies exact codes, offset by 128: five additions per group off by 2 u of at most
+143 sum |x|, times the group's scale s, 2^-13 s sum |x|; below the 2^-11 sum |x w| above wherever the weights are a
+quarter of s on average (those here are 3.7 s).
 Integer layers are exact instead: every product and sum is a whole number of quarters below 2^24.
 """
 import numpy as np

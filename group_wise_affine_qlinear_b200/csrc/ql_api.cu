@@ -1621,12 +1621,21 @@ ql_status heads_impl(const ql_heads* q, const ql_heads* k, ql_dtype dtype, int32
     p.inv_d = 1.0f / static_cast<float>(D);
     const int slots = static_cast<int>((D + 15) / 16);
     const int G = slots <= 4 ? 4 : slots <= 8 ? 8 : slots <= 16 ? 16 : 32;
+    // Heads of a token that a warp holds at a time: all it has room for, or, where that leaves it fewer than 12 groups to
+    // walk and tokens are many, fewer of more tokens, so that its start (positions, angles, the first copies, some 5 groups'
+    // time) counts less and no lane is without a head.  All it has room for against this rule: 33792 tokens of 1 head of 64
+    // 30 us to 14, 20000 of 3 of 64 31 to 14, 33792 of 10 of 128 59 to 41, 20000 of 12 of 160 59 to 53, 9000 of 24 of 64 23
+    // to 17; one head at a time where 12 groups are there without: 32760 of 24 of 128 74 to 70.
     const int per = 32 / G;
-    const int groups = (p.set[0].heads + per - 1) / per + (p.set[1].heads + per - 1) / per;
-    // a warp per token; the heads of few tokens are shared by warps, up to 8 per SM (512 tokens of 36 heads of 256: 14.3 us
-    // with 9 warps a token, 12.3 with 2; every warp forms its token's angles anew)
-    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(groups, 8ll * dev->sm_count / M)));
-    const int64_t units = M * p.parts;
+    int at_once = per;
+    const auto groups_of = [&](int n) { return (p.set[0].heads + n - 1) / n + (p.set[1].heads + n - 1) / n; };
+    while (at_once > 1 && groups_of(at_once) < 12 && M / (2 * per / at_once) >= 8ll * dev->sm_count) at_once /= 2;
+    while ((1 << p.at_once_log) < at_once) ++p.at_once_log;
+    const int tokens = per / at_once, groups = groups_of(at_once);
+    // the heads of few tokens are shared by warps, up to 8 per SM (512 tokens of 36 heads of 256: 14.3 us with 9 warps a
+    // token, 12.3 with 2; every warp forms its token's angles anew)
+    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(groups, 8ll * dev->sm_count * tokens / M)));
+    const int64_t units = (M + tokens - 1) / tokens * p.parts;
     if ((units + rotary::kWarps - 1) / rotary::kWarps > (1ll << 31) - 1) return QL_ERR_UNSUPPORTED;
     if (dtype == QL_F32)
         return adjacent ? launch_heads<true, true>(p, G, units, stream) : launch_heads<true, false>(p, G, units, stream);

@@ -41,6 +41,7 @@ struct Params {
     int norm;
     int weight_f32;
     int parts;                 // warps that share a token's heads
+    int at_once_log;           // log2 of the heads of a token that a warp holds at a time
     float eps, inv_d;
 };
 
@@ -60,24 +61,27 @@ __device__ __forceinline__ uint64_t swapped(uint64_t v) {
     return norm::pair_of(f.y, f.x);
 }
 
-// A token's heads (or its part of them) per warp, kPer = 32 / G heads at a time.  kAdjacent: pairs (2 i, 2 i + 1).  kFull:
-// D = 16 G, every lane has both of its pieces.
+// A warp holds 32 / G heads at a time: `at_once` of each of its 32 / G / at_once tokens, whose heads (or, for few tokens,
+// a part of them) it walks.  kAdjacent: pairs (2 i, 2 i + 1).  kFull: D = 16 G, every lane has both of its pieces.
 template <bool kF32, bool kAdjacent, int G, bool kFull>
 __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const Params p) {
     using norm::F8;
     __shared__ uint4 ring[kWarps][kStages][kF32 ? 4 : 2][32];
-    __shared__ float4 kept[kWarps][4][32];             // cosines and sines of a lane
+    __shared__ __align__(16) float kept[kWarps][2][32][8];     // cosines and sines of a token's pairs, G slots of 8 per token
     constexpr int kPer = 32 / G;
-    constexpr int kOwn = 8 / kPer;                     // angles a lane forms; the others' come by shuffles
     constexpr int kSize = kF32 ? 4 : 2;
-    const int lane = static_cast<int>(threadIdx.x & 31), slot = lane & (G - 1), which = lane / G;
-    int64_t m = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5), slot = lane & (G - 1);
+    const int at_once = 1 << p.at_once_log, which = (lane / G) & (at_once - 1), token = lane / G >> p.at_once_log;
+    int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     int part = 0;
     if (p.parts > 1) {
-        part = static_cast<int>(m % p.parts);
-        m /= p.parts;
+        part = static_cast<int>(unit % p.parts);
+        unit /= p.parts;
     }
-    if (m >= p.M || (p.seg != nullptr && __ldg(p.seg + m) < 0)) return;
+    int64_t m = unit * (kPer >> p.at_once_log) + token;
+    const bool live = m < p.M && (p.seg == nullptr || __ldg(p.seg + m) >= 0);
+    if (!__any_sync(0xFFFFFFFFu, live)) return;
+    if (!live) m = 0;                                  // (its heads are neither read nor written)
 
     // the lane's two pieces of 8 elements: 8 pairs of the turned part, or what is left behind it
     const bool turned = slot < p.P / 8;
@@ -85,8 +89,9 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
     const int eb = turned && !kAdjacent ? ea + p.P : ea + 8;
     const bool has_a = kFull || 16 * slot < p.D, has_b = kFull || (has_a && eb < p.D);
 
-    // the warp's groups of kPer heads: [lo, hi) of the queries', then of the keys'
-    const int nq = (p.set[0].heads + kPer - 1) / kPer, groups = nq + (p.set[1].heads + kPer - 1) / kPer;
+    // the warp's groups of at_once heads: [lo, hi) of the queries', then of the keys'
+    const int nq = (p.set[0].heads + at_once - 1) >> p.at_once_log;
+    const int groups = nq + ((p.set[1].heads + at_once - 1) >> p.at_once_log);
     int g0 = 0, g1 = groups;
     if (p.parts > 1) {
         g0 = static_cast<int>(static_cast<int64_t>(part) * groups / p.parts);
@@ -94,17 +99,17 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
     }
     const auto head_in = [&](int set, int g) {
         const Heads& hs = p.set[set];
-        return static_cast<const uint8_t*>(hs.in) + (m * hs.in_token + static_cast<int64_t>(g * kPer + which) * hs.in_head + ea) * kSize;
+        return static_cast<const uint8_t*>(hs.in) + (m * hs.in_token + static_cast<int64_t>(g * at_once + which) * hs.in_head + ea) * kSize;
     };
+    const auto heads_from = [&](int set, int g) { return live ? p.set[set].heads - g * at_once - which : 0; };   // > 0: the lane has one
     // The groups pass through a ring in shared memory, every lane copying and reading its own pieces: kStages - 1 of them
     // are on their way at any time, the first while the angles are formed.
-    const int warp = static_cast<int>(threadIdx.x >> 5);
     // (Lanes past a head's end or the last head copy nothing.  The two vectors of 8 fp32, and the two pieces of 16
     // neighbours, share their 32-byte sectors: those copies go through L1, so that a sector is fetched once.)
     constexpr bool kThroughL1 = kF32 || kAdjacent;
     int fset = g0 < nq ? 0 : 1, fstage = 0, fend = fset ? g1 : min(g1, nq), fg = g0;       // what is copied next
-    int fleft = p.set[fset].heads - (g0 - fset * nq) * kPer - which;                       // > 0: the lane's head exists
-    int64_t fstep = p.set[fset].in_head * (kPer * kSize);
+    int fleft = heads_from(fset, g0 - fset * nq);
+    int64_t fstep = p.set[fset].in_head * (at_once * kSize);
     const uint8_t* from = head_in(fset, g0 - fset * nq);
     const auto fetch = [&] {
         if (fg < fend) {
@@ -114,12 +119,12 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
                 if (fleft > 0 && has_a) ptx::copy16_async_of<kThroughL1>(&to[v][lane], from + 16 * v);
                 if (fleft > 0 && has_b) ptx::copy16_async_of<kThroughL1>(&to[(kF32 ? 2 : 1) + v][lane], from + (eb - ea) * kSize + 16 * v);
             }
-            fleft -= kPer;
+            fleft -= at_once;
             from += fstep;
             if (++fg == nq && fg < g1) {
                 fend = g1;
-                fleft = p.set[1].heads - which;
-                fstep = p.set[1].in_head * (kPer * kSize);
+                fleft = heads_from(1, 0);
+                fstep = p.set[1].in_head * (at_once * kSize);
                 from = head_in(1, 0);
             }
         }
@@ -129,36 +134,25 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
 
-    {
-        float c[8], s[8];
-        float oc[kOwn], os[kOwn];
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const int pair = 8 * slot + which * kOwn + i;
-            oc[i] = 1.0f;
-            os[i] = 0.0f;
-            if (turned) {
-                const int axis = __ldg(p.axes + pair);
-                if (static_cast<unsigned>(axis) < static_cast<unsigned>(p.A)) {
-                    double t = position(p, axis * p.M + m) * __ldg(p.turns + pair);
-                    t -= rint(t);
-                    sincospif(2.0f * static_cast<float>(t), &os[i], &oc[i]);
-                } else {
-                    record_status(QL_ERR_INVALID_ARG);
-                }
+    // a token's angles, shared by the lanes of its at_once heads
+    float (*const cosines)[8] = kept[warp][0] + token * G;
+    float (*const sines)[8] = kept[warp][1] + token * G;
+    if (turned) {
+        for (int i = which; i < 8; i += at_once) {
+            float c = 1.0f, s = 0.0f;
+            const int axis = __ldg(p.axes + 8 * slot + i);
+            if (static_cast<unsigned>(axis) < static_cast<unsigned>(p.A)) {
+                double t = position(p, axis * p.M + m) * __ldg(p.turns + 8 * slot + i);
+                t -= rint(t);
+                sincospif(2.0f * static_cast<float>(t), &s, &c);
+            } else {
+                record_status(QL_ERR_INVALID_ARG);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = __shfl_sync(0xFFFFFFFFu, oc[i % kOwn], (i / kOwn) * G + slot);
-            s[i] = __shfl_sync(0xFFFFFFFFu, os[i % kOwn], (i / kOwn) * G + slot);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            kept[warp][i][lane] = make_float4(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]);
-            kept[warp][2 + i][lane] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+            cosines[slot][i] = c;
+            sines[slot][i] = s;
         }
     }
+    __syncwarp();
     int stage = 0;
 
     for (int set = 0; set < 2; ++set) {
@@ -176,8 +170,8 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
             float c[8], s[8];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                *reinterpret_cast<float4*>(c + 4 * i) = kept[warp][i][lane];
-                *reinterpret_cast<float4*>(s + 4 * i) = kept[warp][2 + i][lane];
+                *reinterpret_cast<float4*>(c + 4 * i) = *reinterpret_cast<const float4*>(&cosines[slot][4 * i]);
+                *reinterpret_cast<float4*>(s + 4 * i) = *reinterpret_cast<const float4*>(&sines[slot][4 * i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -196,10 +190,10 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
             }
         }
         uint8_t* to = static_cast<uint8_t*>(hs.out) +
-                      (m * hs.out_token + static_cast<int64_t>(lo * kPer + which) * hs.out_head + ea) * kSize;
-        const int64_t out_step = hs.out_head * (kPer * kSize);
-        int left = hs.heads - lo * kPer - which;       // > 0: the lane's head exists
-        for (int g = lo; g < hi; ++g, left -= kPer, to += out_step) {
+                      (m * hs.out_token + static_cast<int64_t>(lo * at_once + which) * hs.out_head + ea) * kSize;
+        const int64_t out_step = hs.out_head * (at_once * kSize);
+        int left = heads_from(set, lo);
+        for (int g = lo; g < hi; ++g, left -= at_once, to += out_step) {
             fetch();                                   // into what was read a group ago
             ptx::copy_async_wait<kStages - 1>();
             norm::Raw<kF32> ra, rb;

@@ -85,7 +85,8 @@ CASES = [  # M, Hq, Hk, D, P, A
     (1, 1, 1, 16, 8, 1), (1, 18, 18, 256, 128, 3), (3, 5, 1, 64, 32, 3), (7, 4, 4, 80, 40, 2), (19, 3, 1, 96, 16, 3),
     (50, 7, 7, 128, 64, 3), (33, 6, 2, 160, 80, 4), (65, 2, 1, 192, 64, 3), (200, 18, 6, 256, 64, 3), (9, 2, 2, 512, 256, 3),
     (11, 3, 3, 24, 8, 2), (5, 36, 4, 136, 64, 3), (4, 33, 11, 8, 0, 0), (6, 1, 1, 264, 128, 3), (40, 2, 2, 64, 0, 0),
-    (6000, 3, 1, 64, 32, 3), (2500, 4, 2, 256, 128, 3)]
+    (6000, 3, 1, 64, 32, 3), (2500, 4, 2, 256, 128, 3),
+    (9601, 1, 1, 64, 32, 3), (5003, 5, 1, 96, 48, 3), (4801, 9, 3, 128, 40, 3), (2407, 7, 7, 200, 64, 2)]   # several tokens a warp
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -140,7 +141,7 @@ def test_far_positions(kind, far):
     _check(ql.rotary_axes(x, pos, rot), x, None, pos, rot, False, False)
 
 
-@pytest.mark.parametrize("M", [12, 3000])
+@pytest.mark.parametrize("M", [12, 3000, 11000])
 def test_padding_rows_are_left_alone(M):
     rng = np.random.default_rng(9)
     x, rot, pos = _rand(rng, (M, 5, 64), torch.bfloat16), _rotary(rng, 32, 3), _positions(rng, 3, M, "int32")

@@ -617,7 +617,7 @@ ql_status launch_fused(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const 
                             FC::kSmemBytes, st, mx, mc, mc2, mp, my, static_cast<const fused::Params&>(p));
 }
 
-// The fused kernel in epilogue mode (which writes y without a map).
+// The fused kernel in epilogue mode.
 template <int B, int kAct>
 ql_status launch_epilogue_act(dim3 grid, cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& mc, const CUtensorMap& mp,
                               const fused::EpiParams& p, bool bf16_out) {
@@ -677,8 +677,9 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
         if ((s = encode_3d(&my, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, N, M, pl.split_k, N * 4,
                            static_cast<uint64_t>(M) * N * 4, 32, 32)) != QL_OK)
             return s;
-    } else if ((s = encode_2d(&my, bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, y, N,
-                              M, N * (bf16_out ? 2 : 4), 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK) {
+    } else if (ep == nullptr &&                        // (the epilogue mode writes y without a map)
+               (s = encode_2d(&my, bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, y, N, M,
+                              N * (bf16_out ? 2 : 4), 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) != QL_OK) {
         return s;
     }
 
@@ -1159,11 +1160,19 @@ ql_status check_epilogue(const EpilogueArgs& a) {
     return QL_OK;
 }
 
-// Few tokens of a weight of up to 32 MiB of codes go through the one-launch kernel.  Against the streaming path, whole calls
-// of 1 token in a graph: 4 bits 512 -> 4608 3.0 us to 7.0, 4608 -> 4608 7.0 to 11.4, 12288 -> 4608 14.7 to 15.2, 4608 ->
-// 13824 17.2 to 16.6, 53248 -> 4608 57 to 40; 8 bits 512 -> 18432 5.2 to 9.3, 4608 -> 4608 9.1 to 11.7; of 8 tokens 4.0 to
-// 7.3, 7.7 to 12.2, 16.1 to 16.1, 19.1 to 16.9, 60 to 41; 6.4 to 9.8, 9.7 to 12.4.
-bool few_pays(int64_t M, int64_t K, int64_t N, int bits) { return M <= few::kMaxM && code_bytes(K, N, bits) <= (32u << 20); }
+// Few tokens of a small weight go through the one-launch kernel, whose products cost it more with every 8 tokens, and twice
+// for 8-bit codes.  Against the streaming path, whole calls in a graph (a launch is 2 to 3 us of the host's besides):
+//   1 token    4 bits 512 -> 4608 3.0 us to 7.0, 4608 -> 4608 7.0 to 11.4, 12288 -> 4608 14.7 to 15.2, 4608 -> 13824 17.2 to
+//              16.6, 53248 -> 4608 57 to 40; 8 bits 512 -> 18432 5.2 to 9.3, 4608 -> 4608 9.1 to 11.7
+//   8 tokens   4.1 to 7.3, 7.9 to 12.1, 16.1 to 16.1, 20.1 to 17.0, 60 to 41; 6.2 to 9.7, 9.6 to 12.4
+//   16 tokens  512 -> 4608 5.6 to 8.7, 2304 -> 2304 5.0 to 9.9, 4608 -> 4608 9.9 to 12.9, 4608 -> 13824 25.9 to 18.1;
+//              8 bits 512 -> 18432 11.0 to 11.2, 4608 -> 4608 15.3 to 13.6
+//   32 tokens  8.6 to 9.6, 7.3 to 10.7, 19.7 to 14.0, 55 to 21; 17.6 to 14.1, 23.6 to 14.7
+bool few_pays(int64_t M, int64_t K, int64_t N, int bits) {
+    if (M > few::kMaxM) return false;
+    const size_t mib = M <= 8 ? 32 : (M <= 16 ? 16 : 4) * 4 / bits;
+    return code_bytes(K, N, bits) <= mib << 20;
+}
 
 // Warps of a CTA that share 16 rows (1 to 8), each of four groups of K at least.
 int few_slices(int64_t G) { return G >= 32 ? 8 : G >= 16 ? 4 : G >= 8 ? 2 : 1; }
@@ -1179,11 +1188,16 @@ ql_status run_few(const void* x, const uint32_t* codes, const void* scales, cons
                                              static_cast<int>(K), static_cast<int>(N), slices, e);
     };
     prof_begin(st);
-    if (bits == 4) launch(bf16_out ? few::few_kernel<4, true> : few::few_kernel<4, false>);
-    else launch(bf16_out ? few::few_kernel<8, true> : few::few_kernel<8, false>);
+    const auto launch_blocks = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        if (bits == 4) launch(bf16_out ? few::few_kernel<4, NT, true> : few::few_kernel<4, NT, false>);
+        else launch(bf16_out ? few::few_kernel<8, NT, true> : few::few_kernel<8, NT, false>);
+    };
+    if (M <= 8) launch_blocks(std::integral_constant<int, 1>{});
+    else if (M <= 16) launch_blocks(std::integral_constant<int, 2>{});
+    else launch_blocks(std::integral_constant<int, 4>{});
     prof_end(st);
-    set_dispatch("path=few_epilogue bits=%d rows=%d slices=%d ctas=%u launches=1 why=auto:M<=%d,codes<=32MiB", bits, few::kRows,
-                 slices, grid, few::kMaxM);
+    set_dispatch("path=few_epilogue bits=%d rows=%d slices=%d ctas=%u launches=1 why=auto:few", bits, few::kRows, slices, grid);
     return launch_status();
 }
 

@@ -1,4 +1,4 @@
-// A packed projection of up to 8 tokens with its epilogue, in one launch.
+// A packed projection of a few tokens (up to 32) with its epilogue, in one launch.
 //
 //   y[m][n] = epilogue( sum_g s(n,g) D(n,m,g) + (b(n,g) - 128 s(n,g)) X(m,g) )
 //   D = sum_{k in g} (128 + q(n,k)) x[m][k],   X = sum_{k in g} x[m][k]
@@ -18,7 +18,7 @@
 namespace ql {
 namespace few {
 
-constexpr int kMaxM = 8;
+constexpr int kMaxM = 32;              // four blocks of 8 tokens
 constexpr int kWarps = 8;
 constexpr int kRows = 16;              // of a warp
 constexpr int kAhead = 4;              // groups whose loads are on their way together
@@ -30,20 +30,24 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // 128 + q for the two codes of 4 bits at bits 0 and 16.
 __device__ __forceinline__ uint32_t weights_of(uint32_t v) { return (v & 0x000F000Fu) | 0x43004300u; }
 
-// Lane l = 4 r + t of a warp holds, of weight rows r and r + 8 and of token r, the 16 columns 16 t .. of a group: which of
-// a product's 16 columns an operand's register stands for is free as long as both operands agree.
+// Lane l = 4 r + t of a warp holds, of weight rows r and r + 8 and of tokens r, r + 8, .., the 16 columns 16 t .. of a
+// group: which of a product's 16 columns an operand's register stands for is free as long as both operands agree.
 template <int B>
-struct Group {
-    uint32_t w[2][B == 4 ? 2 : 4];     // codes of rows r, r + 8
-    uint4 x[2];                        // token r
+struct Codes {
+    uint32_t w[2][B == 4 ? 2 : 4];     // of rows r, r + 8
+};
+template <int NT>
+struct Tokens {
+    uint4 x[NT][2];
 };
 
-template <int B, bool kBf16Out>
+// NT: blocks of 8 tokens.
+template <int B, int NT, bool kBf16Out>
 __global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* __restrict__ x, const uint32_t* __restrict__ codes,
                                                           const unsigned short* __restrict__ scales,
                                                           const unsigned short* __restrict__ biases, void* y, int M, int K, int N,
                                                           int slices, const epi::Epilogue e) {
-    __shared__ float red[kWarps][kMaxM][kRows];
+    __shared__ float red[kWarps][8 * NT][kRows];
     const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
     const int r = lane >> 2, t = lane & 3;
     const int G = K / kGroup, slice = warp % slices, block = warp / slices;
@@ -51,7 +55,7 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* _
     const int n0 = (static_cast<int>(blockIdx.x) * blocks + block) * kRows;
     constexpr int kWords = B == 4 ? 2 : 4;             // a lane's, of a row's group
 
-    const auto load = [&](int g, Group<B>& o) {
+    const auto load = [&](int g, Codes<B>& o) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t n = min(n0 + r + 8 * h, N - 1);              // (rows past N are not stored)
@@ -68,52 +72,70 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* _
                 o.w[h][3] = v.w;
             }
         }
-        o.x[0] = o.x[1] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < M) {
-            const uint4* v = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(r) * K + g * kGroup + 16 * t);
-            o.x[0] = __ldg(v);
-            o.x[1] = __ldg(v + 1);
-        }
     };
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};           // rows r, r, r + 8, r + 8 of tokens 2 t, 2 t + 1, ...
-    const auto work = [&](const Group<B>& o, const uint32_t (&sb)[2], int i4) {
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f}, one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr uint32_t kOnes = 0x3F803F80u;
-        const uint32_t xw[8] = {o.x[0].x, o.x[0].y, o.x[0].z, o.x[0].w, o.x[1].x, o.x[1].y, o.x[1].z, o.x[1].w};
+    const auto load_x = [&](int g, Tokens<NT>& o) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            uint32_t b0, b1;
-            if constexpr (B == 4) {
-                // word u / 2 of each row, its code pairs (j, j + 4) for j = 2 (u % 2) and + 1
-                const uint32_t lo = xw[4 * (u >> 1) + (u & 1)], up = xw[4 * (u >> 1) + 2 + (u & 1)];
-                b0 = __byte_perm(lo, up, 0x5410);
-                b1 = __byte_perm(lo, up, 0x7632);
-                const uint32_t p = o.w[0][u >> 1] >> (8 * (u & 1)), q = o.w[1][u >> 1] >> (8 * (u & 1));
-                mma_bf16(d, weights_of(p), weights_of(q), weights_of(p >> 4), weights_of(q >> 4), b0, b1);
-            } else {
-                // word u of each row, its code pairs (0, 2) and (1, 3), by nibbles
-                b0 = __byte_perm(xw[2 * u], xw[2 * u + 1], 0x5410);
-                b1 = __byte_perm(xw[2 * u], xw[2 * u + 1], 0x7632);
-                const uint32_t p = o.w[0][u], q = o.w[1][u];
-                mma_bf16(d, weights_of(p), weights_of(q), weights_of(p >> 8), weights_of(q >> 8), b0, b1);
-                mma_bf16(hi, weights_of(p >> 4), weights_of(q >> 4), weights_of(p >> 12), weights_of(q >> 12), b0, b1);
+        for (int i = 0; i < NT; ++i) {
+            o.x[i][0] = o.x[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (r + 8 * i < M) {
+                const uint4* v = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(r + 8 * i) * K + g * kGroup + 16 * t);
+                o.x[i][0] = __ldg(v);
+                o.x[i][1] = __ldg(v + 1);
             }
-            mma_bf16(one, kOnes, kOnes, kOnes, kOnes, b0, b1);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 p = half2_of(__shfl_sync(0xFFFFFFFFu, sb[i >> 1], 4 * r + i4));
-            const float s = __low2float(p), b = __high2float(p);
-            const float v = B == 4 ? d[i] : fmaf(16.0f, hi[i], d[i]);
-            acc[i] = fmaf(s, v, fmaf(fmaf(s, B == 4 ? -128.0f : -17.0f * 128.0f, b), one[i], acc[i]));
         }
     };
-    // The slice's groups four at a time, every load of the four on its way before the first is used.  Lane t of a row's four
-    // takes the (scale, bias) of the t-th of them: one request instead of four, each of which touches eight rows' lines.
+    float acc[NT][4] = {};                             // rows r, r, r + 8, r + 8 of tokens 2 t, 2 t + 1, ... of a block
+    const auto work = [&](const Codes<B>& o, const Tokens<NT>& xs, const uint32_t (&sb)[2], int i4) {
+        float s[2], b[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const __half2 p = half2_of(__shfl_sync(0xFFFFFFFFu, sb[h], 4 * r + i4));
+            s[h] = __low2float(p);
+            b[h] = fmaf(s[h], B == 4 ? -128.0f : -17.0f * 128.0f, __high2float(p));
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (NT > 1 && 8 * j >= M) break;
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f}, one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            constexpr uint32_t kOnes = 0x3F803F80u;
+            const uint4 x0 = xs.x[j][0], x1 = xs.x[j][1];
+            const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t b0, b1;
+                if constexpr (B == 4) {
+                    // word u / 2 of each row, its code pairs (k, k + 4) for k = 2 (u % 2) and + 1
+                    const uint32_t lo = xw[4 * (u >> 1) + (u & 1)], up = xw[4 * (u >> 1) + 2 + (u & 1)];
+                    b0 = __byte_perm(lo, up, 0x5410);
+                    b1 = __byte_perm(lo, up, 0x7632);
+                    const uint32_t p = o.w[0][u >> 1] >> (8 * (u & 1)), q = o.w[1][u >> 1] >> (8 * (u & 1));
+                    mma_bf16(d, weights_of(p), weights_of(q), weights_of(p >> 4), weights_of(q >> 4), b0, b1);
+                } else {
+                    // word u of each row, its code pairs (0, 2) and (1, 3), by nibbles
+                    b0 = __byte_perm(xw[2 * u], xw[2 * u + 1], 0x5410);
+                    b1 = __byte_perm(xw[2 * u], xw[2 * u + 1], 0x7632);
+                    const uint32_t p = o.w[0][u], q = o.w[1][u];
+                    mma_bf16(d, weights_of(p), weights_of(q), weights_of(p >> 8), weights_of(q >> 8), b0, b1);
+                    mma_bf16(hi, weights_of(p >> 4), weights_of(q >> 4), weights_of(p >> 12), weights_of(q >> 12), b0, b1);
+                }
+                mma_bf16(one, kOnes, kOnes, kOnes, kOnes, b0, b1);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = B == 4 ? d[i] : fmaf(16.0f, hi[i], d[i]);
+                acc[j][i] = fmaf(s[i >> 1], v, fmaf(b[i >> 1], one[i], acc[j][i]));
+            }
+        }
+    };
+    // The slice's groups four at a time, the codes of the four on their way before the first is used; the activations too
+    // where they are one block's, else a group ahead.  Lane t of a row's four takes the (scale, bias) of the t-th group:
+    // one request instead of four, each of which touches eight rows' lines.
     static_assert(kAhead == 4, "a group for each lane of a row's four");
     const int g_end = static_cast<int>(static_cast<int64_t>(slice + 1) * G / slices);
+    constexpr int kAheadX = NT == 1 ? kAhead : 2;
     for (int g = static_cast<int>(static_cast<int64_t>(slice) * G / slices); g < g_end; g += kAhead) {
-        Group<B> o[kAhead];
+        Codes<B> o[kAhead];
+        Tokens<NT> xs[kAheadX];
         uint32_t sb[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -121,14 +143,20 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* _
             sb[h] = __ldg(scales + at) | static_cast<uint32_t>(__ldg(biases + at)) << 16;
         }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
+        for (int i = 0; i < kAhead; ++i) {
             if (g + i < g_end) load(g + i, o[i]);
+            if (i < kAheadX && g + i < g_end) load_x(g + i, xs[i]);
+        }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (g + i < g_end) work(o[i], sb, i);
+        for (int i = 0; i < kAhead; ++i) {
+            if (g + i < g_end) work(o[i], xs[i % kAheadX], sb, i);
+            if (NT > 1 && i + kAheadX < kAhead && g + i + kAheadX < g_end) load_x(g + i + kAheadX, xs[i % kAheadX]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[warp][2 * t + (i & 1)][r + 8 * (i >> 1)] = acc[i];
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[warp][8 * j + 2 * t + (i & 1)][r + 8 * (i >> 1)] = acc[j][i];
     __syncthreads();
     // the outputs of a row block: kRows rows of every token, summed over the slices in order
     for (int i = static_cast<int>(threadIdx.x); i < blocks * M * kRows; i += 32 * kWarps) {

@@ -142,10 +142,10 @@ def test_epilogue_workspace_sizes(L):
                       (L.qlinear8_epilogue_workspace_size, L.qlinear8_workspace_size)):
         for args in ((0, 256, 256, 64), (16, 100, 256, 64), (16, 256, 12, 64), (16, 256, 256, 32)):
             assert fn(*args) == big, args
-        for args in ((9, 256, 256, 64), (300, 512, 256, 64), (8, 53248, 4608, 64)):
+        for args in ((33, 256, 256, 64), (300, 512, 256, 64), (8, 53248, 4608, 64)):
             assert plain(*args) <= fn(*args) < big, args
-        assert fn(8, 256, 256, 64) == 0                    # one launch, no scratch
-    assert ql.epilogue_workspace_size(9, 256, 64) > 0 and ql.epilogue_workspace_size(9, 256, 64, bits=8) > 0
+        assert fn(8, 256, 256, 64) == fn(32, 256, 256, 64) == 0    # one launch, no scratch
+    assert ql.epilogue_workspace_size(33, 256, 64) > 0 and ql.epilogue_workspace_size(33, 256, 64, bits=8) > 0
     with pytest.raises(ValueError):
         ql.epilogue_workspace_size(0, 256, 64)
 

@@ -1,4 +1,4 @@
-"""Projections of up to 8 tokens with an epilogue, in one launch, and the rule that picks it.
+"""Projections of up to 32 tokens with an epilogue, in one launch, and the rule that picks it.
 
 Integer layers are exact (whole quarters below 2^24).  Random ones: a group's sum of (128 + q) x or, for 8-bit codes, of
 its nibbles' takes 64 products, each addition off by 2 u = 2^-23 at most of sums up to 143 (2288) sum |x|; with the
@@ -30,7 +30,7 @@ def _cuda():
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 7, 8])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 24, 25, 32])
 @pytest.mark.parametrize("K,N", [(64, 8), (64, 136), (448, 24), (512, 1032), (576, 8), (960, 264), (1024, 40), (2048, 72),
                                  (4672, 520)])
 def test_exact_integers(M, K, N, bits):
@@ -42,12 +42,14 @@ def test_exact_integers(M, K, N, bits):
     ids = torch.from_numpy(seg).cuda()
     before = kw["residual"].clone()
     CALL[bits](x, *w, segment_ids=ids, out=kw["residual"], **kw)
-    assert ql.last_dispatch().startswith("path=few_epilogue")
+    few = K * N * bits // 8 <= (32 if M <= 8 else (16 if M <= 16 else 4) * 4 // bits) << 20
+    assert ql.last_dispatch().startswith("path=few_epilogue" if few else "path=tc_skinny_epilogue")
     _check_exact(kw["residual"], y, seg, out, before)
 
 
 @pytest.mark.parametrize("act", [None, "silu", "gelu", "gelu_tanh"])
-@pytest.mark.parametrize("M,K,N,bits", [(1, 4608, 264, 4), (8, 512, 1032, 8), (5, 2176, 72, 4), (3, 128, 520, 8)])
+@pytest.mark.parametrize("M,K,N,bits", [(1, 4608, 264, 4), (8, 512, 1032, 8), (5, 2176, 72, 4), (3, 128, 520, 8),
+                                         (13, 1088, 264, 8), (30, 576, 264, 4)])
 def test_random_layers(M, K, N, bits, act):
     rng = np.random.default_rng(M + K + N)
     xb, codes, s, b = (random_layer if bits == 4 else random_layer8)(rng, M, K, N)
@@ -65,16 +67,17 @@ def test_random_layers(M, K, N, bits, act):
 
 def test_one_token_does_not_reach_another():
     rng = np.random.default_rng(1)
-    x, w, kw, seg, lin = _exact_case(rng, 8, 512, 136, 4, "bf16", "bf16", padding=False)
-    ids = torch.from_numpy(seg).cuda()
-    clean = ql.forward_epilogue(x, *w, segment_ids=ids, **kw)
-    x[2, 100], x[5, 7] = float("inf"), float("nan")
-    kw["residual"][6, 3] = float("nan")
-    got = ql.forward_epilogue(x, *w, segment_ids=ids, **kw)
-    assert not torch.isfinite(got[2]).any() and torch.isnan(got[5]).all() and torch.isnan(got[6, 3])
-    for m in (0, 1, 3, 4, 7):
-        assert torch.equal(got[m], clean[m])
-    assert torch.equal(got[6, 4:], clean[6, 4:])
+    for M in (8, 27):
+        x, w, kw, seg, lin = _exact_case(rng, M, 512, 136, 4, "bf16", "bf16", padding=False)
+        ids = torch.from_numpy(seg).cuda()
+        clean = ql.forward_epilogue(x, *w, segment_ids=ids, **kw)
+        x[2, 100], x[5, 7] = float("inf"), float("nan")
+        kw["residual"][6, 3] = float("nan")
+        got = ql.forward_epilogue(x, *w, segment_ids=ids, **kw)
+        assert not torch.isfinite(got[2]).any() and torch.isnan(got[5]).all() and torch.isnan(got[6, 3])
+        for m in set(range(M)) - {2, 5, 6}:
+            assert torch.equal(got[m], clean[m])
+        assert torch.equal(got[6, 4:], clean[6, 4:])
 
 
 def test_magnitudes():
@@ -88,7 +91,7 @@ def test_magnitudes():
 
 
 def test_the_rule():
-    """Few tokens of a weight of up to 32 MiB of codes; more tokens or larger weights are streamed."""
+    """Few tokens of a small weight; more tokens or larger weights are streamed."""
     def path(M, K, N, bits):
         c = torch.zeros((N, K * bits // 32), dtype=torch.int32, device="cuda")
         s = torch.zeros((N, K // 64), dtype=torch.float16, device="cuda")
@@ -96,7 +99,11 @@ def test_the_rule():
         return ql.last_dispatch().split()[0]
     assert path(8, 8192, 8192, 4) == "path=few_epilogue" and path(8, 8192, 8200, 4) == "path=tc_skinny_epilogue"
     assert path(8, 8192, 4096, 8) == "path=few_epilogue" and path(8, 8192, 4104, 8) == "path=tc_skinny_epilogue"
-    assert path(9, 64, 8, 4) == "path=tc_skinny_epilogue" and path(65, 64, 8, 4) == "path=tc_fused_epilogue"
+    assert path(16, 8192, 4096, 4) == "path=few_epilogue" and path(16, 8192, 4104, 4) == "path=tc_skinny_epilogue"
+    assert path(16, 2048, 4096, 8) == "path=few_epilogue" and path(16, 2048, 4104, 8) == "path=tc_skinny_epilogue"
+    assert path(32, 2048, 4096, 4) == "path=few_epilogue" and path(17, 2048, 4104, 4) == "path=tc_skinny_epilogue"
+    assert path(32, 2048, 1024, 8) == "path=few_epilogue" and path(17, 2048, 1032, 8) == "path=tc_skinny_epilogue"
+    assert path(33, 64, 8, 4) == "path=tc_skinny_epilogue" and path(65, 64, 8, 4) == "path=tc_fused_epilogue"
 
 
 def test_replays_with_other_values():

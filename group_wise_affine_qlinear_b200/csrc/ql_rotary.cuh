@@ -5,11 +5,16 @@
 //   pair i turns by the angle 2 pi turns[i] pos[axes[i]][m]:  (a, b) <- (a cos - b sin, b cos + a sin)
 //
 // All of it in fp32, but the angle: position times turns is formed in 64 bits and its whole turns are dropped before it
-// is rounded (at position 2^20 a product in 32 bits is off by up to a sixteenth of a turn's radian).  Rounded once.
+// is rounded (at position 2^20 a product in 32 bits is off by up to 0.06 rad).  Rounded once.
 //
-// A head is some hundred bytes to a kilobyte that is read and written once, so DRAM bounds it.  G lanes hold a head in
-// registers from load to store, each two pieces of 8 elements that hold 8 pairs; the sines and cosines of a token
-// depend on the lane alone and stay in registers over the heads.
+// A head is some hundred bytes to a kilobyte that is read and written once, so DRAM bounds many tokens: 33792 of 24 heads
+// of 256, written by heads, 134 us, 6.2 TB/s; 32760 of 24 of 128, neighbours paired, 67 us, 6.0 TB/s; 4608 of 36 of 256
+// 41 us, 4.1 TB/s (4608 warps on 2960 places).  G lanes hold a head in registers from ring to store, each two pieces of 8
+// elements that hold 8 pairs; weights and angles of a lane are folded into four vectors per token, so an element costs two
+// packed operations and the norm's factor.  (Against it, the two 2048^2 canvases above: one load at a time 199 us, loads a
+// group ahead in registers 174, selects around the ring's copies 140; persistent warps over runs of tokens 225, persistent
+// CTAs that share a token's angles 275, two to nine warps per token 186 to 349: DRAM wants neighbouring tokens at the same
+// time, and a unit's start is not free.)
 #pragma once
 
 #include "ql_norm.cuh"

@@ -226,6 +226,14 @@ __device__ __forceinline__ bool give_registers() {
 // Lane l works on columns 8 i + l / 4 (i < 4) and, for j < 4, on tokens 8 j + 2 (l % 4) and + 1 of a chunk: the fragment of
 // the accumulator that transposing matrix stores (and loads, for the residual) take to a token's row, eight elements an
 // instruction.  A row's 16-byte pieces are permuted by its number, so that neither matrices nor rows meet in a bank.
+//
+// The drain is not hidden: tensor memory holds one accumulator per group, and the next tile's products wait for it.  A chunk
+// takes a warp 1100 cycles, 1450 with a residual; 4608 x 4608 x 4608 137 us (the plain epilogue 135), with gate and residual
+// 143, silu 145, gelu 152 (their two special functions a value are a tile's 3 us).  What cost most before: registers.  At
+// the launch's 96 a thread the compiler spilled values on their way from memory and waited for each (146 us whatever else
+// was done).  One 16-bit store per element instead of matrix stores 147 and, with gelu, 184; outputs and residual through
+// the TMA, whose rows are 64 bytes here, 145 and 150 with a residual.  No gain: storing a chunk while the next is read,
+// announcing the groups' accumulators apart, two values sharing a reciprocal.
 template <bool kBf16Out, int kAct>
 __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage0, uint32_t stage_bytes, uint32_t vec0,
                                               uint32_t tmem_base,

@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 #include <type_traits>
 
 #include "ql_common.cuh"
@@ -1522,17 +1523,29 @@ int64_t heads_span(int64_t token, int64_t head, int64_t M, int64_t H, int64_t D)
     return (M - 1) * token + (H - 1) * head + D;
 }
 
-// Whether two sets of heads (element offsets from a common base in units of one byte each) may share memory.  Spans
-// apart share none; so do rows of one period that lie apart in it, as the queries and keys of a packed projection.
+// Whether stretches of na and nb bytes, repeated every `period` bytes and the second d bytes behind the first, share none.
+bool apart_in(int64_t period, int64_t na, int64_t nb, int64_t d) {
+    if (period <= 0 || na > period || nb > period) return false;
+    const int64_t behind = ((d % period) + period) % period;
+    return behind >= na && period - behind >= nb;
+}
+
+// Whether two sets of heads may share memory (strides in elements).  They share none if their spans do not meet; nor if
+// they lie apart in a common period: rows of tokens, as the queries and keys of a packed projection; rows of heads kept one
+// behind the other; or single heads, where queries and keys alternate head by head.
 bool heads_overlap(const void* a, int64_t at, int64_t ah, int64_t aheads, const void* b, int64_t bt, int64_t bh,
                    int64_t bheads, int64_t M, int64_t D, int64_t size) {
-    const auto ax = reinterpret_cast<intptr_t>(a), bx = reinterpret_cast<intptr_t>(b);
     if (!overlap(a, heads_span(at, ah, M, aheads, D) * size, b, heads_span(bt, bh, M, bheads, D) * size)) return false;
-    if (M == 1 || at != bt || at <= 0) return true;
-    const int64_t period = at * size, na = heads_span(0, ah, 1, aheads, D) * size, nb = heads_span(0, bh, 1, bheads, D) * size;
-    if (na > period || nb > period) return true;
-    const int64_t d = (((bx - ax) % period) + period) % period;        // b's row begins d bytes behind a row of a
-    return d < na || period - d < nb;
+    // a stride that only one token or head has is never used
+    at = M > 1 ? at : 0, bt = M > 1 ? bt : 0;
+    ah = aheads > 1 ? ah : 0, bh = bheads > 1 ? bh : 0;
+    const int64_t d = reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a);
+    if (at == bt && apart_in(at * size, heads_span(0, ah, 1, aheads, D) * size, heads_span(0, bh, 1, bheads, D) * size, d))
+        return false;
+    if ((ah == bh || ah == 0 || bh == 0) && apart_in(std::max(ah, bh) * size, heads_span(at, 0, M, 1, D) * size,
+                                                     heads_span(bt, 0, M, 1, D) * size, d))
+        return false;
+    return !apart_in(std::gcd(std::gcd(at, ah), std::gcd(bt, bh)) * size, D * size, D * size, d);
 }
 
 ql_status check_heads(const ql_heads& q, int64_t M, int64_t D, int64_t unit, ql_dtype weight_dtype) {

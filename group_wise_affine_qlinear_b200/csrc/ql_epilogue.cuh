@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(256) epilogue_sum_kernel(const float* __restri
                                      fmaf(gate.z, activate(e.act, z.z + bias.z), r.z),
                                      fmaf(gate.w, activate(e.act, z.w + bias.w), r.w));
         if constexpr (kBf16Out)
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(y) + at) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(y) + at) =
+                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         else
             *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = o;
     }

@@ -104,9 +104,12 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
     }
     const auto head_in = [&](int set, int g) {
         const Heads& hs = p.set[set];
-        return static_cast<const uint8_t*>(hs.in) + (m * hs.in_token + static_cast<int64_t>(g * at_once + which) * hs.in_head + ea) * kSize;
+        return static_cast<const uint8_t*>(hs.in) +
+               (m * hs.in_token + static_cast<int64_t>(g * at_once + which) * hs.in_head + ea) * kSize;
     };
-    const auto heads_from = [&](int set, int g) { return live ? p.set[set].heads - g * at_once - which : 0; };   // > 0: the lane has one
+    const auto heads_from = [&](int set, int g) {      // > 0: the lane has one
+        return live ? p.set[set].heads - g * at_once - which : 0;
+    };
     // The groups pass through a ring in shared memory, every lane copying and reading its own pieces: kStages - 1 of them
     // are on their way at any time, the first while the angles are formed.
     // (Lanes past a head's end or the last head copy nothing.  The two vectors of 8 fp32, and the two pieces of 16
@@ -122,7 +125,8 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
 #pragma unroll
             for (int v = 0; v < (kF32 ? 2 : 1); ++v) {
                 if (fleft > 0 && has_a) ptx::copy16_async_of<kThroughL1>(&to[v][lane], from + 16 * v);
-                if (fleft > 0 && has_b) ptx::copy16_async_of<kThroughL1>(&to[(kF32 ? 2 : 1) + v][lane], from + (eb - ea) * kSize + 16 * v);
+                if (fleft > 0 && has_b)
+                    ptx::copy16_async_of<kThroughL1>(&to[(kF32 ? 2 : 1) + v][lane], from + (eb - ea) * kSize + 16 * v);
             }
             fleft -= at_once;
             from += fstep;

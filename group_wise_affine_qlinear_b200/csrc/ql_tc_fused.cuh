@@ -337,7 +337,8 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
 #pragma unroll 1
         for (int g = 0; g < NG; ++g) {
             const int n0 = w_blk * BW + g * BWG + n_off;
-            uint8_t* y = static_cast<uint8_t*>(p.y) + (m0 + row0) * row_step + (n0 + piece * (16 / kElem)) * static_cast<int64_t>(kElem);
+            uint8_t* y = static_cast<uint8_t*>(p.y) + (m0 + row0) * row_step +
+                         (n0 + piece * (16 / kElem)) * static_cast<int64_t>(kElem);
             const bool col_in = n0 + piece * (16 / kElem) < N;
             float4 bias, gate;
 #pragma unroll
@@ -714,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1) fused_gemm_kernel(
             ptx::more_registers<kEpiRegs>();
             const int e = warp - kWarpEpi0;
             epilogue_role<kBf16Out, kAct>(p, ptx::smem_addr(smem + C::kOffEpi) + e * C::kNB * C::kStageBytes, C::kStageBytes,
-                                          ptx::smem_addr(smem + C::kOffVec) + e * 2 * kEpiVectorBytes, tmem_base, acc_full, acc_empty, abort_flag, warp & 3, e >> 2, lane);
+                                          ptx::smem_addr(smem + C::kOffVec) + e * 2 * kEpiVectorBytes, tmem_base, acc_full,
+                                          acc_empty, abort_flag, warp & 3, e >> 2, lane);
         }
     } else if (!give_registers<kEpi>()) {
     } else if (kLora && warp == kWarpTmaX) {

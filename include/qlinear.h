@@ -491,8 +491,9 @@ QL_API ql_status qlinear8_epilogue_forward(const void* x, const uint32_t* codes,
  *                  `out` are left as they were
  *
  * Required (QL_ERR_INVALID_ARG): M >= 1, D >= 8, D % 8 == 0, heads >= 1, 0 <= 2 P <= D, eps >= 0 and finite,
- * A <= QL_HEAD_MAX_D, strides from 0 to 2^56 / max(M, heads).  P % 8 == 0 and D <= QL_HEAD_MAX_D (QL_ERR_UNSUPPORTED otherwise).  Heads, weights and strides 16-byte
- * aligned, the rest by their element.  k may be NULL (queries alone).  No workspace.
+ * A <= QL_HEAD_MAX_D, strides from 0 to 2^56 / max(M, heads).  P % 8 == 0 and D <= QL_HEAD_MAX_D (QL_ERR_UNSUPPORTED
+ * otherwise).  Heads, weights and strides 16-byte aligned, the rest by their element.  k may be NULL (queries alone).  No
+ * workspace.  Sums of squares leave fp32's range, above and below, as in qlinear_norm_residual.
  */
 #define QL_HEAD_MAX_D 512
 typedef enum { QL_POS_I32 = 0, QL_POS_I64 = 1, QL_POS_F32 = 2 } ql_pos_type;

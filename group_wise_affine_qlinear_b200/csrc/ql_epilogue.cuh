@@ -23,8 +23,9 @@ struct Epilogue {
     int params_f32;          // type of bias and gate: 0 bf16, 1 fp32
 };
 
-// The hardware's base-2 exponential and reciprocal (2 units of fp32 each; the argument's rounding adds |v| 2^-24): of no
-// consequence beside the weights' rounding to f16.
+// The hardware's base-2 exponential (relative error 2^-22) and reciprocal (2^-23).  Rounding the exponential's argument adds
+// its magnitude times a few 2^-24, so that the activations below keep their relative accuracy in their tails, (20 + 7 E) 2^-24
+// of the value where e^-E is the exponential.  Results under 2^-120 may come out as zero.
 __device__ __forceinline__ float exp2_fast(float v) {
     float o;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
@@ -40,13 +41,15 @@ constexpr float kLog2e = 1.44269504f;
 // z / (1 + e^-z); where e^-z overflows the reciprocal is 0 and the result -0.
 __device__ __forceinline__ float silu(float z) { return z * rcp_fast(1.0f + exp2_fast(-kLog2e * z)); }
 
-// z Phi(z) with 1 - erf from Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26 (absolute error below
-// 1.5e-7): where the library's erff takes some forty instructions and a branch, this takes a dozen.
+// z Phi(z), where 1 - Phi(|z|) = t P(t) e^(-z^2 / 2), t = 1 / (1 + 0.35 |z|): the form of Abramowitz and Stegun, Handbook of
+// Mathematical Functions, 7.1.26, with P of degree 6 fitted (minimax over 0 <= |z| <= 13.5, by linear programming) to the
+// relative error, which stays under 2^-22 (1 + z^2 / 2).  Their five terms keep 1.5e-7 of 1, but only 0.2 % of the tail itself
+// at z = -5 and 1 % at -8.  The library's erff takes some forty instructions and a branch, this takes fourteen.
 __device__ __forceinline__ float gelu(float z) {
-    const float t = rcp_fast(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
-    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f), 0.5f * 1.421413741f),
-                                        0.5f * -0.284496736f), 0.5f * 0.254829592f);
-    const float tail = poly * exp2_fast(-0.5f * kLog2e * z * z);       // 1 - Phi(|z|)
+    const float t = rcp_fast(fmaf(0.35f, fabsf(z), 1.0f));
+    const float p = fmaf(t, fmaf(t, fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.045832973f, -0.18913298f), 0.21832183f), 0.0033125462f),
+                                          0.14543160f), 0.13642566f), 0.13980844f);
+    const float tail = t * p * exp2_fast(-0.5f * kLog2e * z * z);      // 1 - Phi(|z|)
     // z - z tail above zero, z tail below (an infinite z times a zero tail would be NaN)
     return fmaf(-fminf(fabsf(z), 1e4f), tail, fmaxf(z, 0.0f));
 }

@@ -229,7 +229,7 @@ __device__ __forceinline__ bool give_registers() {
 //
 // The drain is not hidden: tensor memory holds one accumulator per group, and the next tile's products wait for it.  A chunk
 // takes a warp 1100 cycles, 1450 with a residual; 4608 x 4608 x 4608 137 us (the plain epilogue 135), with gate and residual
-// 143, silu 145, gelu 152 (their two special functions a value are a tile's 3 us).  What cost most before: registers.  At
+// 143, silu 145, gelu 154 (their two special functions a value are a tile's 3 us).  What cost most before: registers.  At
 // the launch's 96 a thread the compiler spilled values on their way from memory and waited for each (146 us whatever else
 // was done).  One 16-bit store per element instead of matrix stores 147 and, with gelu, 184; outputs and residual through
 // the TMA, whose rows are 64 bytes here, 145 and 150 with a residual.  No gain: storing a chunk while the next is read,

@@ -429,7 +429,8 @@ QL_API ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const vo
  *   z[m][n] = sum_k x[m][k] * W[n][k] + bias[n]
  *   y[m][n] = residual[m][n] + gate[seg][n] * act(z[m][n]),   seg = segment_ids[m]
  * x, codes, scales, biases and the arithmetic of the packed product as in qlinear_forward; everything behind it in
- * fp32, y rounded once.
+ * fp32, y rounded once.  An activation errs by at most (20 + 7 E) 2^-24 of its value, where e^-E is the exponential
+ * in it (E = |z|, z^2 / 2, 2 |u|), far in its tail too; values under 2^-120 may come out as zero.
  *
  *   bias          [N] of param_dtype (QL_BF16 or QL_F32); NULL: 0
  *   activation    a ql_activation: z; silu z / (1 + e^-z); gelu z Phi(z); its tanh form

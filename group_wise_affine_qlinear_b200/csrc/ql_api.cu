@@ -1161,18 +1161,34 @@ ql_status check_epilogue(const EpilogueArgs& a) {
     return QL_OK;
 }
 
-// Few tokens of a small weight go through the one-launch kernel, whose products cost it more with every 8 tokens, and twice
-// for 8-bit codes.  Against the streaming path, whole calls in a graph (a launch is 2 to 3 us of the host's besides):
-//   1 token    4 bits 512 -> 4608 3.0 us to 7.0, 4608 -> 4608 7.0 to 11.4, 12288 -> 4608 14.7 to 15.2, 4608 -> 13824 17.2 to
-//              16.6, 53248 -> 4608 57 to 40; 8 bits 512 -> 18432 5.2 to 9.3, 4608 -> 4608 9.1 to 11.7
-//   8 tokens   4.1 to 7.3, 7.9 to 12.1, 16.1 to 16.1, 20.1 to 17.0, 60 to 41; 6.2 to 9.7, 9.6 to 12.4
-//   16 tokens  512 -> 4608 5.6 to 8.7, 2304 -> 2304 5.0 to 9.9, 4608 -> 4608 9.9 to 12.9, 4608 -> 13824 25.9 to 18.1;
-//              8 bits 512 -> 18432 11.0 to 11.2, 4608 -> 4608 15.3 to 13.6
-//   32 tokens  8.6 to 9.6, 7.3 to 10.7, 19.7 to 14.0, 55 to 21; 17.6 to 14.1, 23.6 to 14.7
+// Few tokens of a small weight may go through the one-launch kernel, whose products cost it more with every 8 tokens, and
+// twice for 8-bit codes: its range is a limit of the codes' bytes.
+int64_t few_limit(int64_t M, int bits) {
+    return static_cast<int64_t>(M <= 8 ? 32 : (M <= 16 ? 16 : 4) * 4 / bits) << 20;
+}
+bool few_takes(int64_t M, int64_t K, int64_t N, int bits) {
+    return M <= few::kMaxM && static_cast<int64_t>(code_bytes(K, N, bits)) <= few_limit(M, bits);
+}
+
+// Within its range it is taken unless a wide weight of 4 bits, whose CTAs come in three waves or more, fills over two thirds
+// of it.  us a call in a graph, this kernel to the streaming path, through layers whose weights come from memory (from L2:
+// 1 to 3 us less on both sides, the same order):
+//   1 token    4608 -> 4608 8.0 to 11.7, 4608 -> 9216 14.9 to 15.9, 12288 -> 4608 16.6 to 17.1; wide: 4608 -> 10240 17.7 to 15.7,
+//              -> 12288 20.6 to 17.3, -> 13824 21.2 to 18.6, 2048 -> 32768 24.6 to 18.4
+//              8 bits 512 -> 18432 6.4 to 10.2, 4608 -> 4608 10.8 to 13.4, -> 6912 15.7 to 15.9, 2048 -> 16384 17.1 to 15.6
+//   8 tokens   4608 -> 4608 8.6 to 12.7, -> 9216 15.3 to 16.2, 12288 -> 4608 17.7 to 17.7; wide: 4608 -> 10240 18.6 to 16.5,
+//              -> 12288 21.2 to 17.9, -> 13824 21.8 to 18.9, 2048 -> 32768 25.9 to 21.3
+//              8 bits 512 -> 18432 7.2 to 11.1, 4608 -> 4608 11.0 to 13.9, -> 6912 16.0 to 16.4, 2048 -> 16384 17.6 to 16.4
+//   16 tokens  2304 -> 4608 7.1 to 12.8, 4608 -> 4608 10.7 to 14.3, 8192 -> 4096 16.0 to 16.3; wide: 5120 -> 5120 16.9 to 14.8,
+//              4096 -> 8192 17.1 to 15.7; 8 bits 2304 -> 2304 6.8 to 13.1, 1024 -> 8192 10.8 to 12.3
+//   32 tokens  2304 -> 2304 7.9 to 11.6, 2048 -> 4096 12.3 to 12.7; wide: 1024 -> 6656 13.8 to 12.0, 512 -> 16384 17.6 to 15.3
+//              8 bits 1024 -> 2048 8.6 to 10.2, 512 -> 4096 10.4 to 10.1
+// Deep weights at the very limit are better streamed too (8192 -> 8192 at 8 tokens 23.0 to 19.1, 16384 -> 4096 22.0 to 19.4);
+// from 24 MiB down they tie.
 bool few_pays(int64_t M, int64_t K, int64_t N, int bits) {
-    if (M > few::kMaxM) return false;
-    const size_t mib = M <= 8 ? 32 : (M <= 16 ? 16 : 4) * 4 / bits;
-    return code_bytes(K, N, bits) <= mib << 20;
+    if (!few_takes(M, K, N, bits)) return false;
+    const bool wide = bits == 4 && N > (M <= 8 ? 8192 : 4096);
+    return !wide || 3 * static_cast<int64_t>(code_bytes(K, N, bits)) <= 2 * few_limit(M, bits);
 }
 
 // Warps of a CTA that share 16 rows (1 to 8), each of four groups of K at least.
@@ -1242,7 +1258,9 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
         lp = lora_plan(pl, M, K, la->r, la->L, dev->sm_count);
         need = lp.workspace;
     }
-    if (ep && few_pays(M, K, N, bits)) need = 0;
+    // (in the one-launch kernel's range a call without the streaming path's workspace is taken all the same)
+    const bool few = ep && (few_pays(M, K, N, bits) || (few_takes(M, K, N, bits) && (!workspace || workspace_bytes < need)));
+    if (few) need = 0;
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return QL_ERR_WORKSPACE;
         if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
@@ -1254,7 +1272,7 @@ ql_status forward_impl(const void* x, const uint32_t* codes, const void* scales,
     }
     const bool bf16 = out_dtype == QL_BF16;
     const epi::Epilogue* e = ep ? &ep->e : nullptr;
-    if (e && few_pays(M, K, N, bits)) return run_few(x, codes, scales, biases, y, bf16, M, K, N, bits, *e, stream);
+    if (few) return run_few(x, codes, scales, biases, y, bf16, M, K, N, bits, *e, stream);
     if (pl.path == QL_PATH_GEMV)
         return run_gemv(pl, x, codes, scales, biases, y, bf16, M, K, N, workspace, stream, dev->sm_count);
     if (pl.path == QL_PATH_TC_SKINNY)

@@ -1781,6 +1781,17 @@ ql_status qlinear_test_delay(int32_t role_mask, uint64_t max_ns) {
 #endif
 }
 
+ql_status qlinear_test_extent(int64_t cut) {
+#ifdef QL_BOUNDS_CHECK
+    if (cut < 0) return QL_ERR_INVALID_ARG;
+    const long long n = cut;
+    return cudaMemcpyToSymbol(g_extent_cut, &n, sizeof(n)) == cudaSuccess ? QL_OK : QL_ERR_CUDA;
+#else
+    (void)cut;
+    return QL_ERR_UNSUPPORTED;
+#endif
+}
+
 ql_status qlinear_test_ring_depth(int32_t variant) {
 #ifdef QL_BOUNDS_CHECK
     if (variant < 0 || variant >= QL_TEST_RING_VARIANTS) return QL_ERR_INVALID_ARG;

@@ -73,9 +73,10 @@ __device__ __forceinline__ float activate(int act, float z) {
     }
 }
 
-// Segment of row m, -1 for a row to leave alone.
-__device__ __forceinline__ int segment_of(const Epilogue& e, int64_t m) {
+// Segment of row m of M, -1 for a row to leave alone.
+__device__ __forceinline__ int segment_of(const Epilogue& e, int64_t m, int64_t M) {
     if (e.seg == nullptr) return 0;
+    if (!in_bounds(m, M)) return -1;
     const int s = __ldg(e.seg + m);
     if (s >= e.T) {
         record_status(QL_ERR_INVALID_ARG);
@@ -87,6 +88,13 @@ __device__ __forceinline__ int segment_of(const Epilogue& e, int64_t m) {
 __device__ __forceinline__ float param(const void* p, int f32, int64_t i) {
     return f32 ? __ldg(static_cast<const float*>(p) + i)
                : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + i));
+}
+// Bias and gate of column n of N; 0 and 1 where there is none.
+__device__ __forceinline__ float bias_of(const Epilogue& e, int64_t N, int64_t n) {
+    return e.bias != nullptr && in_bounds(n, N) ? param(e.bias, e.params_f32, n) : 0.0f;
+}
+__device__ __forceinline__ float gate_of(const Epilogue& e, int seg, int64_t N, int64_t n) {
+    return e.gate != nullptr && in_bounds(seg * N + n, e.T * N) ? param(e.gate, e.params_f32, seg * N + n) : 1.0f;
 }
 __device__ __forceinline__ float4 bf16x4(uint2 v) {
     return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
@@ -109,13 +117,13 @@ __global__ void __launch_bounds__(256) epilogue_sum_kernel(const float* __restri
     int held = -1, seg_next = -1;
     const auto fetch = [&](int64_t m) {
         if (m >= M) return;
-        seg_next = segment_of(e, m);
-        if (e.residual == nullptr) return;
+        seg_next = segment_of(e, m, M);
         const int64_t at = m * N + n;
+        if (e.residual == nullptr || !in_bounds(at + 3, M * N)) return;
         r_next = kBf16Out ? bf16x4(*reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.residual) + at))
                           : *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + at);
     };
-    const float4 bias = e.bias ? param4(e.bias, e.params_f32, n) : none;
+    const float4 bias = e.bias && in_bounds(n + 3, N) ? param4(e.bias, e.params_f32, n) : none;
     fetch(blockIdx.y);
     ptx::grid_dependency_wait();                       // the partials come from the kernel before
     for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
@@ -124,11 +132,13 @@ __global__ void __launch_bounds__(256) epilogue_sum_kernel(const float* __restri
         const int64_t at = m * N + n;
         fetch(m + gridDim.y);
         if (seg < 0) continue;
-        if (e.gate != nullptr && seg != held) gate = param4(e.gate, e.params_f32, static_cast<int64_t>(seg) * N + n);
+        if (e.gate != nullptr && seg != held && in_bounds(static_cast<int64_t>(seg) * N + n + 3, static_cast<int64_t>(e.T) * N))
+            gate = param4(e.gate, e.params_f32, static_cast<int64_t>(seg) * N + n);
         held = seg;
         float4 z = none;
 #pragma unroll 4
         for (int s = 0; s < S; ++s) {
+            if (!in_bounds(s * M * N + at + 3, S * M * N)) continue;
             const float4 v = *reinterpret_cast<const float4*>(partial + s * M * N + at);
             z = make_float4(z.x + v.x, z.y + v.y, z.z + v.z, z.w + v.w);
         }
@@ -136,6 +146,7 @@ __global__ void __launch_bounds__(256) epilogue_sum_kernel(const float* __restri
                                      fmaf(gate.y, activate(e.act, z.y + bias.y), r.y),
                                      fmaf(gate.z, activate(e.act, z.z + bias.z), r.z),
                                      fmaf(gate.w, activate(e.act, z.w + bias.w), r.w));
+        if (!in_bounds(at + 3, M * N)) continue;
         if constexpr (kBf16Out)
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(y) + at) =
                 make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
@@ -160,13 +171,13 @@ __global__ void __launch_bounds__(256) epilogue_reduce_kernel(const float* __res
     const int64_t at = static_cast<int64_t>(t) * N + n;
     int seg = -1;
     float bias = 0.0f, gate = 1.0f, res = 0.0f;
-    if (inside) {
-        seg = segment_of(e, t);
-        if (e.bias != nullptr) bias = param(e.bias, e.params_f32, n);
+    if (inside && in_bounds(at, static_cast<int64_t>(M) * N)) {
+        seg = segment_of(e, t, M);
+        bias = bias_of(e, N, n);
         if (e.residual != nullptr)
             res = kBf16Out ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at])
                            : static_cast<const float*>(e.residual)[at];
-        if (e.gate != nullptr && seg >= 0) gate = param(e.gate, e.params_f32, static_cast<int64_t>(seg) * N + n);
+        if (seg >= 0) gate = gate_of(e, seg, N, n);
     }
     if (threadIdx.x == 0) count = skinny::list_segments(w, cpt, units, P, segmax, seg_base);
     ptx::grid_dependency_wait();                       // partials come from the kernel before

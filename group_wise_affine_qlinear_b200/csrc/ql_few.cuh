@@ -62,7 +62,12 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* _
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t n = min(n0 + r + 8 * h, N - 1);              // (rows past N are not stored)
-            const uint32_t* c = codes + n * (K * B / 32) + g * (2 * B) + kWords * t;
+            const int64_t at = n * (K * B / 32) + g * (2 * B) + kWords * t;
+            const uint32_t* c = codes + at;
+            if (!in_bounds(at + kWords - 1, static_cast<int64_t>(N) * (K * B / 32))) {
+                o = {};
+                continue;
+            }
             if constexpr (B == 4) {
                 const uint2 v = __ldg(reinterpret_cast<const uint2*>(c));
                 o.w[h][0] = v.x;
@@ -80,8 +85,9 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* _
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             o.x[i][0] = o.x[i][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (r + 8 * i < M) {
-                const uint4* v = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(r + 8 * i) * K + g * kGroup + 16 * t);
+            const int64_t at = static_cast<int64_t>(r + 8 * i) * K + g * kGroup + 16 * t;
+            if (r + 8 * i < M && in_bounds(at + 15, static_cast<int64_t>(M) * K)) {
+                const uint4* v = reinterpret_cast<const uint4*>(x + at);
                 o.x[i][0] = __ldg(v);
                 o.x[i][1] = __ldg(v + 1);
             }
@@ -143,7 +149,9 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* _
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t at = static_cast<int64_t>(min(n0 + r + 8 * h, N - 1)) * G + min(g + t, g_end - 1);
-            sb[h] = __ldg(scales + at) | static_cast<uint32_t>(__ldg(biases + at)) << 16;
+            sb[h] = 0u;
+            if (in_bounds(at, static_cast<int64_t>(N) * G))
+                sb[h] = __ldg(scales + at) | static_cast<uint32_t>(__ldg(biases + at)) << 16;
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -166,13 +174,14 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const __nv_bfloat16* _
         const int row = i % kRows, m = i / kRows % M, bl = i / (kRows * M);
         const int n = (static_cast<int>(blockIdx.x) * blocks + bl) * kRows + row;
         if (n >= N) continue;
-        const int seg = epi::segment_of(e, m);
+        const int seg = epi::segment_of(e, m, M);
         if (seg < 0) continue;
-        float z = e.bias != nullptr ? epi::param(e.bias, e.params_f32, n) : 0.0f, sum = 0.0f;
+        float z = epi::bias_of(e, N, n), sum = 0.0f;
         for (int s = 0; s < slices; ++s) sum += red[bl * slices + s][m][row];
         z += sum;
         const int64_t at = static_cast<int64_t>(m) * N + n;
-        const float gate = e.gate != nullptr ? epi::param(e.gate, e.params_f32, static_cast<int64_t>(seg) * N + n) : 1.0f;
+        if (!in_bounds(at, static_cast<int64_t>(M) * N)) continue;
+        const float gate = epi::gate_of(e, seg, N, n);
         float res = 0.0f;
         if (e.residual != nullptr)
             res = kBf16Out ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at])

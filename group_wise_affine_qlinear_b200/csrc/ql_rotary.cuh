@@ -50,6 +50,16 @@ struct Params {
     float eps, inv_d;
 };
 
+// Elements from a set's first to one past its last, as it lies in memory.
+__device__ __forceinline__ int64_t span(const Params& p, int64_t token, int64_t head, int heads) {
+    return (p.M - 1) * token + (heads - 1) * head + p.D;
+}
+// Whether 8 elements from `at` on lie within the set that starts at `base`.
+template <int kSize>
+__device__ __forceinline__ bool piece_in(const uint8_t* at, const void* base, int64_t span) {
+    return in_bounds((at - static_cast<const uint8_t*>(base)) / kSize + 7, span);
+}
+
 __device__ __forceinline__ double position(const Params& p, int64_t i) {
     if (p.pos_type == QL_POS_I32) return static_cast<double>(__ldg(static_cast<const int*>(p.pos) + i));
     if (p.pos_type == QL_POS_I64) return static_cast<double>(__ldg(static_cast<const long long*>(p.pos) + i));
@@ -122,10 +132,12 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
     const auto fetch = [&] {
         if (fg < fend) {
             uint4 (*to)[32] = ring[warp][fstage];
+            const Heads& hs = p.set[fg < nq ? 0 : 1];
+            const int64_t all = span(p, hs.in_token, hs.in_head, hs.heads);
 #pragma unroll
             for (int v = 0; v < (kF32 ? 2 : 1); ++v) {
-                if (fleft > 0 && has_a) ptx::copy16_async_of<kThroughL1>(&to[v][lane], from + 16 * v);
-                if (fleft > 0 && has_b)
+                if (fleft > 0 && has_a && piece_in<kSize>(from, hs.in, all)) ptx::copy16_async_of<kThroughL1>(&to[v][lane], from + 16 * v);
+                if (fleft > 0 && has_b && piece_in<kSize>(from + (eb - ea) * kSize, hs.in, all))
                     ptx::copy16_async_of<kThroughL1>(&to[(kF32 ? 2 : 1) + v][lane], from + (eb - ea) * kSize + 16 * v);
             }
             fleft -= at_once;
@@ -149,9 +161,10 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
     if (turned) {
         for (int i = which; i < 8; i += at_once) {
             float c = 1.0f, s = 0.0f;
-            const int axis = __ldg(p.axes + 8 * slot + i);
+            const int axis = in_bounds(8 * slot + i, p.P) ? __ldg(p.axes + 8 * slot + i) : -1;
             if (static_cast<unsigned>(axis) < static_cast<unsigned>(p.A)) {
-                double t = position(p, axis * p.M + m) * __ldg(p.turns + 8 * slot + i);
+                const int64_t at = axis * p.M + m;
+                double t = in_bounds(at, p.A * p.M) ? position(p, at) * __ldg(p.turns + 8 * slot + i) : 0.0;
                 t -= rint(t);
                 sincospif(2.0f * static_cast<float>(t), &s, &c);
             } else {
@@ -172,8 +185,8 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
         // are pairs within a piece, there x (cos, cos) + swapped x (-sin, sin), and the weights of the swapped x swapped.
         F8 ca = norm::splat(1.0f), cb = ca, sa, sb;
         if (p.norm && hs.weight != nullptr) {
-            if (has_a) ca = norm::load_params(hs.weight, p.weight_f32, ea);
-            if (has_b) cb = norm::load_params(hs.weight, p.weight_f32, eb);
+            if (has_a && in_bounds(ea + 7, p.D)) ca = norm::load_params(hs.weight, p.weight_f32, ea);
+            if (has_b && in_bounds(eb + 7, p.D)) cb = norm::load_params(hs.weight, p.weight_f32, eb);
         }
         if (turned) {
             float c[8], s[8];
@@ -245,8 +258,9 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
                     *reinterpret_cast<uint4*>(q) = norm::pack_bf16x8(v);
                 }
             };
-            if (left > 0 && has_a) store(ya, to);
-            if (left > 0 && has_b) store(yb, to + (eb - ea) * kSize);
+            const int64_t all = span(p, hs.out_token, hs.out_head, hs.heads);
+            if (left > 0 && has_a && piece_in<kSize>(to, hs.out, all)) store(ya, to);
+            if (left > 0 && has_b && piece_in<kSize>(to + (eb - ea) * kSize, hs.out, all)) store(yb, to + (eb - ea) * kSize);
         }
     }
     ptx::copy_async_wait<0>();

@@ -261,7 +261,9 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
         const uint8_t* from = static_cast<const uint8_t*>(p.e.residual) + (m + row0) * row_step + static_cast<int64_t>(col) * kElem;
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
-            const bool in = kRows * k < left && col < N;
+            const bool in = kRows * k < left && col < N &&
+                            in_bounds(static_cast<int64_t>(m + row0 + kRows * k) * N + col + 16 / kElem - 1,
+                                      static_cast<int64_t>(p.M) * N);
             ptx::copy16_async(stage0 + block * stage_bytes + piece_at(k), in ? from + kRows * k * row_step : p.e.residual, in);
         }
     };
@@ -275,13 +277,14 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
 #pragma unroll
         for (int c = 0; c < kHalf; ++c) {
             const int m = t_blk * BT + m_off + 32 * c + lane;
-            ptx::copy4_async(to + kRsAt + 128u * c + 4u * lane, p.rowscale + min(m, p.M - 1));
+            if (in_bounds(min(m, p.M - 1), p.M)) ptx::copy4_async(to + kRsAt + 128u * c + 4u * lane, p.rowscale + min(m, p.M - 1));
         }
     };
-    const auto copy_vector = [&](uint32_t to, const void* from, int row, int n) {      // 32 columns from n on
+    const auto copy_vector = [&](uint32_t to, const void* from, int rows, int row, int n) {    // 32 columns from n on
         if (from == nullptr) return;
         const int col = wide ? n + lane : n + 2 * (lane & 15);                         // (those past N are not stored)
         const int64_t at = static_cast<int64_t>(row) * N + (col < N ? col : 0);
+        if (!in_bounds(at + (wide ? 0 : 1), static_cast<int64_t>(rows) * N)) return;
         ptx::copy4_async(to + (wide ? 4u * lane : 4u * (lane & 15)), static_cast<const uint8_t*>(from) + (wide ? 4 * at : 2 * at));
     };
     const auto vector_at = [&](const void* given, uint32_t at, float none) {           // of the lane's columns
@@ -301,7 +304,7 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
     // and four segments in no order 166 us a call, so 150).
     const auto segment = [&](int t_blk, int c) {
         const int m = t_blk * BT + m_off + 32 * c + lane;
-        const int s = m < p.M ? epi::segment_of(p.e, m) : kPast;
+        const int s = m < p.M ? epi::segment_of(p.e, m, p.M) : kPast;
         return p.e.gate == nullptr ? min(s, 0) : s;
     };
 
@@ -314,8 +317,8 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
     copy_rows(vec0, t_blk);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        copy_vector(vec0 + kBiasAt + 128u * g, p.e.bias, 0, w_blk * BW + g * BWG + n_off);
-        copy_vector(vec0 + kGateAt + 128u * g, p.e.gate, held, w_blk * BW + g * BWG + n_off);
+        copy_vector(vec0 + kBiasAt + 128u * g, p.e.bias, 1, 0, w_blk * BW + g * BWG + n_off);
+        copy_vector(vec0 + kGateAt + 128u * g, p.e.gate, p.e.T, held, w_blk * BW + g * BWG + n_off);
     }
     if (has_res) copy_residual(0, t_blk * BT + m_off, w_blk * BW + n_off);
     ptx::copy_async_commit();
@@ -363,8 +366,8 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
                     held = max(__shfl_sync(0xFFFFFFFFu, seg[0], 0), 0);
 #pragma unroll
                     for (int i = 0; i < NG; ++i) {
-                        copy_vector(vec_next + kBiasAt + 128u * i, p.e.bias, 0, w_next * BW + i * BWG + n_off);
-                        copy_vector(vec_next + kGateAt + 128u * i, p.e.gate, held, w_next * BW + i * BWG + n_off);
+                        copy_vector(vec_next + kBiasAt + 128u * i, p.e.bias, 1, 0, w_next * BW + i * BWG + n_off);
+                        copy_vector(vec_next + kGateAt + 128u * i, p.e.gate, p.e.T, held, w_next * BW + i * BWG + n_off);
                     }
                 }
                 ptx::copy_async_commit();
@@ -447,12 +450,9 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
                         const int s = __shfl_sync(0xFFFFFFFFu, seg_c, __ffs(todo) - 1);
                         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, seg_c == s);
                         todo &= ~mask;
-                        float w[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-                        if (p.e.gate != nullptr) {
+                        float w[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = epi::param(p.e.gate, p.e.params_f32, static_cast<int64_t>(s) * N + min(n0 + ln + 8 * i, N - 1));
-                        }
+                        for (int i = 0; i < 4; ++i) w[i] = epi::gate_of(p.e, s, N, min(n0 + ln + 8 * i, N - 1));
                         finish(std::true_type{}, std::false_type{}, mask, make_float4(w[0], w[1], w[2], w[3]));
                         __syncwarp();                  // the next round reads what other lanes wrote
                     }
@@ -471,7 +471,9 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
                     for (int k = 0; k < 4; ++k) o[k] = ptx::ld_shared_v4(stage + piece_at(k0 + k));
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if ((rows >> (kRows * (k0 + k))) & 1u)
+                        if (((rows >> (kRows * (k0 + k))) & 1u) != 0 &&
+                            in_bounds((m0 + row0 + 32 * c + kRows * (k0 + k)) * static_cast<int64_t>(N) + n0 +
+                                          (piece + 1) * (16 / kElem) - 1, static_cast<int64_t>(p.M) * N))
                             *reinterpret_cast<uint4*>(y + (32 * c + kRows * (k0 + k)) * row_step) = o[k];
                 }
                 __syncwarp();                          // the block may be filled again

@@ -213,6 +213,15 @@ QL_API ql_status qlinear_test_ring_depth(int32_t variant);
 QL_API ql_status qlinear_test_delay(int32_t role_mask, uint64_t max_ns);
 
 /*
+ * Test hook of the checked build (libqlinear_bounds.so); the pages have no counterpart.  Takes the last `cut` elements off
+ * every extent that a kernel checks an index against, so that right accesses of them are recorded as QL_ERR_BOUNDS and
+ * skipped: which arrays' accesses are checked can be tested without a wrong one.  0 turns it off.  Synchronous (a small
+ * host-to-device copy on the legacy stream).  The shipped library returns QL_ERR_UNSUPPORTED; QL_ERR_INVALID_ARG for a
+ * negative cut.
+ */
+QL_API ql_status qlinear_test_extent(int64_t cut);
+
+/*
  * Allocation-free forward for small M.  The pages have no counterpart of this
  * call; it exists for callers that cannot allocate device memory where they
  * run the layer (a plugin living inside another engine's fixed memory pool, a

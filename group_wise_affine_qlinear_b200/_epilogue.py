@@ -112,7 +112,7 @@ def _refuse(x, codes, scales, biases, bias, activation, gate, residual, segment_
     _need_dims(codes, 2, "codes")
     N, K = _weights_shape(codes, scales, bits)
     M = x.shape[0]
-    if activation not in ACTIVATIONS:
+    if not (activation is None or isinstance(activation, str)) or activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
     for t, dims, name in ((bias, 1, "bias"), (gate, 2, "gate"), (residual, 2, "residual"), (out, 2, "out")):
         if t is not None:

@@ -48,6 +48,7 @@ def rotary_axes(x: torch.Tensor, positions: torch.Tensor, rotary, *, adjacent: b
     rotary_frequencies().  Pair i of a head, elements i and i + P (adjacent: 2 i and 2 i + 1), turns by the angle
     2 pi turns[i] positions[axes[i]]; elements from 2 P on stay.  x bf16 or fp32 with any strides of tokens and heads (a
     view of a packed projection's output, or heads kept one behind the other); out alike (None: contiguous), it may be x.
+    D is a multiple of 8 up to HEAD_MAX_D, P a multiple of 8; addresses and strides are multiples of 16 bytes.
     segment_ids int32 [M]: a negative one for a padding row, which is left alone in out.
     """
     return _heads("qlinear_rotary_axes", x, None, positions, rotary, False, None, None, 0.0, adjacent, segment_ids, out,

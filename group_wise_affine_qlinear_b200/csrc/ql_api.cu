@@ -596,7 +596,10 @@ ql_status lora_params(const LoraArgs& la, const LoraPlan& lp, uint8_t* ws, int64
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// The epilogue of split K-steps: their ordered sum, four columns per thread and several rows each.
+// The epilogue of split K-steps: their ordered sum, four columns per thread and several rows each.  A dependent launch that
+// reads the caller's vectors, segments and residual before its wait: the chain's first kernel, the parameter transpose, is a
+// plain launch, so whatever the caller enqueued before is complete when any kernel of the chain starts.  (With that first
+// launch made dependent, these reads would race.)
 ql_status launch_epilogue_sum(const float* part, void* y, bool bf16_out, int64_t M, int64_t N, int S,
                               const epi::Epilogue& e, int sm_count, cudaStream_t st) {
     const int64_t cols = (N / 4 + 255) / 256;
@@ -717,7 +720,8 @@ ql_status run_fused(const Plan& pl, const void* x, const uint32_t* codes, const 
                       : launch_fused<false, F8, false, true>(fgrid, st, mx, mc, mc, mp, my, p, la != nullptr);
         if (s != QL_OK) return s;
         prof_end(st);
-        // ordered sum of the slices, rounded once (a plain launch: it reads what the kernel above wrote)
+        // ordered sum of the slices, rounded once: a plain launch, as it reads what the kernel above wrote; with an epilogue a
+        // dependent one, which waits before it does
         const int64_t count = M * N;
         const int blocks = static_cast<int>(std::min<int64_t>((count / 4 + 255) / 256, 8 * sm_count));
         if (ep != nullptr)

@@ -106,7 +106,7 @@ __device__ __forceinline__ float4 param4(const void* p, int f32, int64_t i) {
 
 // y = epilogue of the fp32 partials [S][M][N], summed in slice order: four columns per thread, whose bias (and gate,
 // while the segment stays the same) it holds over its rows.  What the caller gave of a row is fetched a row ahead, of the
-// first one before the wait for the partials.
+// first one before the wait for the partials (its chain begins with a plain launch, see launch_epilogue_sum).
 template <bool kBf16Out>
 __global__ void __launch_bounds__(256) epilogue_sum_kernel(const float* __restrict__ partial, void* y, int64_t M, int N,
                                                            int S, const Epilogue e) {
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256) epilogue_sum_kernel(const float* __restri
 }
 
 // The weight-streaming path's reduce kernel (skinny_reduce_kernel) with the epilogue.  What the caller gave is loaded
-// before the wait for the partials.
+// before the wait for the partials: the chain's first kernel, the activations' conversion, is a plain launch.
 template <bool kBf16Out>
 __global__ void __launch_bounds__(256) epilogue_reduce_kernel(const float* __restrict__ partial,
                                                               const int* __restrict__ rowexp, void* y, int M, int N,

@@ -7,6 +7,7 @@
 // A row whose segment is negative is padding: its row of y is left as it was.
 #pragma once
 
+#include "ql_norm.cuh"
 #include "ql_ptx.cuh"
 #include "ql_tc_skinny.cuh"
 
@@ -44,7 +45,7 @@ __device__ __forceinline__ float silu(float z) { return z * rcp_fast(1.0f + exp2
 // z Phi(z), where 1 - Phi(|z|) = t P(t) e^(-z^2 / 2), t = 1 / (1 + 0.35 |z|): the form of Abramowitz and Stegun, Handbook of
 // Mathematical Functions, 7.1.26, with P of degree 6 fitted (minimax over 0 <= |z| <= 13.5, by linear programming) to the
 // relative error, which stays under 2^-22 (1 + z^2 / 2).  Their five terms keep 1.5e-7 of 1, but only 0.2 % of the tail itself
-// at z = -5 and 1 % at -8.  The library's erff takes some forty instructions and a branch, this takes fourteen.
+// at z = -5 and 1 % at -8.  The library's erff takes some forty instructions and a branch, this takes sixteen.
 __device__ __forceinline__ float gelu(float z) {
     const float t = rcp_fast(fmaf(0.35f, fabsf(z), 1.0f));
     const float p = fmaf(t, fmaf(t, fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.045832973f, -0.18913298f), 0.21832183f), 0.0033125462f),
@@ -52,6 +53,24 @@ __device__ __forceinline__ float gelu(float z) {
     const float tail = t * p * exp2_fast(-0.5f * kLog2e * z * z);      // 1 - Phi(|z|)
     // z - z tail above zero, z tail below (an infinite z times a zero tail would be NaN)
     return fmaf(-fminf(fabsf(z), 1e4f), tail, fmaxf(z, 0.0f));
+}
+// The same for two values, to the same bits: packed operations where there are some.  The fused kernel's drain is bound by
+// its instructions there: 4608 x 128 x 4608 39 us instead of 44 (41 with the five terms of 7.1.26).
+__device__ __forceinline__ float2 gelu_pair(float z0, float z1) {
+    using norm::fma2, norm::mul2, norm::pair_of, norm::halves;
+    const auto both = [](float v) { return pair_of(v, v); };
+    const uint64_t t = pair_of(rcp_fast(fmaf(0.35f, fabsf(z0), 1.0f)), rcp_fast(fmaf(0.35f, fabsf(z1), 1.0f)));
+    uint64_t p = fma2(t, both(0.045832973f), both(-0.18913298f));
+    p = fma2(t, p, both(0.21832183f));
+    p = fma2(t, p, both(0.0033125462f));
+    p = fma2(t, p, both(0.14543160f));
+    p = fma2(t, p, both(0.13642566f));
+    p = fma2(t, p, both(0.13980844f));
+    const uint64_t z = pair_of(z0, z1);
+    const float2 v = halves(mul2(mul2(both(-0.5f * kLog2e), z), z));
+    const float2 tail = halves(mul2(mul2(t, p), pair_of(exp2_fast(v.x), exp2_fast(v.y))));
+    return make_float2(fmaf(-fminf(fabsf(z0), 1e4f), tail.x, fmaxf(z0, 0.0f)),
+                       fmaf(-fminf(fabsf(z1), 1e4f), tail.y, fmaxf(z1, 0.0f)));
 }
 
 // 0.5 z (1 + tanh(u)) = z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3)
@@ -63,6 +82,11 @@ __device__ __forceinline__ float gelu_tanh(float z) {
 template <int kAct>
 __device__ __forceinline__ float activate_as(float z) {
     return kAct == QL_ACT_SILU ? silu(z) : kAct == QL_ACT_GELU ? gelu(z) : kAct == QL_ACT_GELU_TANH ? gelu_tanh(z) : z;
+}
+template <int kAct>
+__device__ __forceinline__ float2 activate_as(float z0, float z1) {
+    if constexpr (kAct == QL_ACT_GELU) return gelu_pair(z0, z1);
+    return make_float2(activate_as<kAct>(z0), activate_as<kAct>(z1));
 }
 __device__ __forceinline__ float activate(int act, float z) {
     switch (act) {

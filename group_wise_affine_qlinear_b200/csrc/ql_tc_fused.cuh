@@ -229,11 +229,13 @@ __device__ __forceinline__ bool give_registers() {
 //
 // The drain is not hidden: tensor memory holds one accumulator per group, and the next tile's products wait for it.  A chunk
 // takes a warp 1100 cycles, 1450 with a residual; 4608 x 4608 x 4608 137 us (the plain epilogue 135), with gate and residual
-// 143, silu 145, gelu 154 (their two special functions a value are a tile's 3 us).  What cost most before: registers.  At
-// the launch's 96 a thread the compiler spilled values on their way from memory and waited for each (146 us whatever else
-// was done).  One 16-bit store per element instead of matrix stores 147 and, with gelu, 184; outputs and residual through
-// the TMA, whose rows are 64 bytes here, 145 and 150 with a residual.  No gain: storing a chunk while the next is read,
-// announcing the groups' accumulators apart, two values sharing a reciprocal.
+// 143, silu 147, gelu_tanh 150, gelu 151 (their two special functions a value are a tile's 3 us).  With two K-steps a tile
+// takes 6.5 us: 3.6 its six chunks per warp, 1.2 the K-steps (0.55 to 0.6 each up to eight), the rest the hand-over between
+// products and drain; 4608 x 128 x 4608 has three such tiles one behind the other, and 6.7 us of launches and start.
+// What cost most before: registers.  At the launch's 96 a thread the compiler spilled values on their way from memory and
+// waited for each (146 us whatever else was done).  One 16-bit store per element instead of matrix stores 147 and, with gelu,
+// 184; outputs and residual through the TMA, whose rows are 64 bytes here, 145 and 150 with a residual.  No gain: storing a
+// chunk while the next is read, announcing the groups' accumulators apart, two values sharing a reciprocal.
 template <bool kBf16Out, int kAct>
 __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage0, uint32_t stage_bytes, uint32_t vec0,
                                               uint32_t tmem_base,
@@ -391,8 +393,10 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t* a = &v[i >> 1][4 * j + 2 * (i & 1)];
-                        a[0] = __float_as_uint(epi::activate_as<kAct>(fmaf(__uint_as_float(a[0]), rs.x, b4[i])));
-                        a[1] = __float_as_uint(epi::activate_as<kAct>(fmaf(__uint_as_float(a[1]), rs.y, b4[i])));
+                        const float2 o = epi::activate_as<kAct>(fmaf(__uint_as_float(a[0]), rs.x, b4[i]),
+                                                                fmaf(__uint_as_float(a[1]), rs.y, b4[i]));
+                        a[0] = __float_as_uint(o.x);
+                        a[1] = __float_as_uint(o.y);
                     }
                 }
                 // residual + gate * act into the block; kRes: it holds the residual; kAll: for every token, else for

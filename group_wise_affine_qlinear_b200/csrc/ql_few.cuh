@@ -10,8 +10,9 @@
 //
 // What bounds such a call is not the 0.56 bytes a weight that it reads but the launches: the streaming path's conversion,
 // stream and reduction, three kernels, take 11.7 us for 1 token of 4608 x 4608 whose 12 MB come from memory (1.8 us at its
-// rate), this one 8.0 (from L2 11.1 and 7.1).  Its weights are exact and not rounded to f16 as the other paths' are.  A warp takes 16 rows and a slice of their groups; the warps of a CTA that share rows add up in shared memory, in
-// order.  (With the groups dealt out in turn, a request for each scale, it took 8.1: every request touches eight rows' lines.)
+// rate), this one 8.0 (from L2 11.1 and 7.1).  Its weights are exact, not rounded to f16 as the other paths' are.  A warp
+// takes 16 rows and a slice of their groups; the warps of a CTA that share rows add up in shared memory, in order.  (With
+// the groups dealt out in turn, a request for each scale, it took 8.1 from L2: every request touches eight rows' lines.)
 #pragma once
 
 #include "ql_epilogue.cuh"

@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(32 * kWarps, kF32 ? 4 : 5) heads_kernel(const 
             const int64_t all = span(p, hs.in_token, hs.in_head, hs.heads);
 #pragma unroll
             for (int v = 0; v < (kF32 ? 2 : 1); ++v) {
-                if (fleft > 0 && has_a && piece_in<kSize>(from, hs.in, all)) ptx::copy16_async_of<kThroughL1>(&to[v][lane], from + 16 * v);
+                if (fleft > 0 && has_a && piece_in<kSize>(from, hs.in, all))
+                    ptx::copy16_async_of<kThroughL1>(&to[v][lane], from + 16 * v);
                 if (fleft > 0 && has_b && piece_in<kSize>(from + (eb - ea) * kSize, hs.in, all))
                     ptx::copy16_async_of<kThroughL1>(&to[(kF32 ? 2 : 1) + v][lane], from + (eb - ea) * kSize + 16 * v);
             }

@@ -279,7 +279,8 @@ __device__ __forceinline__ void epilogue_role(const EpiParams& p, uint32_t stage
 #pragma unroll
         for (int c = 0; c < kHalf; ++c) {
             const int m = t_blk * BT + m_off + 32 * c + lane;
-            if (in_bounds(min(m, p.M - 1), p.M)) ptx::copy4_async(to + kRsAt + 128u * c + 4u * lane, p.rowscale + min(m, p.M - 1));
+            const int at = min(m, p.M - 1);
+            if (in_bounds(at, p.M)) ptx::copy4_async(to + kRsAt + 128u * c + 4u * lane, p.rowscale + at);
         }
     };
     const auto copy_vector = [&](uint32_t to, const void* from, int rows, int row, int n) {    // 32 columns from n on

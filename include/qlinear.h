@@ -458,7 +458,7 @@ QL_API ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const vo
  * Above 64 rows the epilogue is the fused kernel's (or, where its K-steps are split, that of their sum), up to 64 the
  * streaming path's reduction.  Up to 8 rows of a weight of at most 32 MiB of codes, 16 of 16 and 32 of 4 (of 8-bit codes
  * 8 and 2) may be one launch without a workspace, which multiplies exact codes, offset by 128, by the bf16 activations in
- * fp32: activations beyond 2^110 may overflow there.  Weights of 4-bit codes over two thirds of these sizes and wider than
+ * fp32: activations beyond 2^110 may overflow there, and an infinite one makes its row NaN.  Weights of 4-bit codes over two thirds of these sizes and wider than
  * N = 8192 (above 8 rows 4096) are faster on the streaming path: the workspace size is that path's for them, and without
  * such a workspace they are one launch like the others.
  */

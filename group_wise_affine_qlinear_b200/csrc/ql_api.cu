@@ -1174,8 +1174,8 @@ bool few_takes(int64_t M, int64_t K, int64_t N, int bits) {
     return M <= few::kMaxM && static_cast<int64_t>(code_bytes(K, N, bits)) <= few_limit(M, bits);
 }
 
-// Within its range it is taken unless a wide weight of 4 bits, whose CTAs come in three waves or more, fills over two thirds
-// of it.  us a call in a graph, this kernel to the streaming path, through layers whose weights come from memory (from L2:
+// Within its range it is taken unless a wide weight of 4 bits, whose CTAs come in several waves, fills over two thirds of it.
+// us a call in a graph, this kernel to the streaming path, through layers whose weights come from memory (from L2:
 // 1 to 3 us less on both sides, the same order):
 //   1 token    4608 -> 4608 8.0 to 11.7, 4608 -> 9216 14.9 to 15.9, 12288 -> 4608 16.6 to 17.1; wide: 4608 -> 10240 17.7 to 15.7,
 //              -> 12288 20.6 to 17.3, -> 13824 21.2 to 18.6, 2048 -> 32768 24.6 to 18.4
@@ -1187,8 +1187,8 @@ bool few_takes(int64_t M, int64_t K, int64_t N, int bits) {
 //              4096 -> 8192 17.1 to 15.7; 8 bits 2304 -> 2304 6.8 to 13.1, 1024 -> 8192 10.8 to 12.3
 //   32 tokens  2304 -> 2304 7.9 to 11.6, 2048 -> 4096 12.3 to 12.7; wide: 1024 -> 6656 13.8 to 12.0, 512 -> 16384 17.6 to 15.3
 //              8 bits 1024 -> 2048 8.6 to 10.2, 512 -> 4096 10.4 to 10.1
-// Deep weights at the very limit are better streamed too (8192 -> 8192 at 8 tokens 23.0 to 19.1, 16384 -> 4096 22.0 to 19.4);
-// from 24 MiB down they tie.
+// Where the rule is off: deep weights of 24 MiB and more are better streamed too (8 tokens 6144 -> 8192 18.3 to 17.4, 13824 ->
+// 4608 19.2 to 18.9, 16384 -> 4096 22.0 to 19.4, 8192 -> 8192 23.0 to 19.1), of 8 bits 4096 -> 8192 (17.8 to 16.5).
 bool few_pays(int64_t M, int64_t K, int64_t N, int bits) {
     if (!few_takes(M, K, N, bits)) return false;
     const bool wide = bits == 4 && N > (M <= 8 ? 8192 : 4096);

@@ -25,7 +25,7 @@ struct Epilogue {
 };
 
 // The hardware's base-2 exponential (relative error 2^-22) and reciprocal (2^-23).  Rounding the exponential's argument adds
-// its magnitude times a few 2^-24, so that the activations below keep their relative accuracy in their tails, (20 + 7 E) 2^-24
+// its magnitude times a few 2^-24, so that the activations below keep their relative accuracy in their tails, (20 + 8 E) 2^-24
 // of the value where e^-E is the exponential.  Results under 2^-120 may come out as zero.
 __device__ __forceinline__ float exp2_fast(float v) {
     float o;

@@ -57,7 +57,8 @@ __device__ __forceinline__ int64_t span(const Params& p, int64_t token, int64_t 
 // Whether 8 elements from `at` on lie within the set that starts at `base`.
 template <int kSize>
 __device__ __forceinline__ bool piece_in(const uint8_t* at, const void* base, int64_t span) {
-    return in_bounds((at - static_cast<const uint8_t*>(base)) / kSize + 7, span);
+    const int64_t first = (at - static_cast<const uint8_t*>(base)) / kSize;
+    return in_bounds(first, span) && in_bounds(first + 7, span);
 }
 
 __device__ __forceinline__ double position(const Params& p, int64_t i) {

@@ -438,7 +438,7 @@ QL_API ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const vo
  *   z[m][n] = sum_k x[m][k] * W[n][k] + bias[n]
  *   y[m][n] = residual[m][n] + gate[seg][n] * act(z[m][n]),   seg = segment_ids[m]
  * x, codes, scales, biases and the arithmetic of the packed product as in qlinear_forward; everything behind it in
- * fp32, y rounded once.  An activation errs by at most (20 + 7 E) 2^-24 of its value, where e^-E is the exponential
+ * fp32, y rounded once.  An activation errs by at most (20 + 8 E) 2^-24 of its value, where e^-E is the exponential
  * in it (E = |z|, z^2 / 2, 2 |u|), far in its tail too; values under 2^-120 may come out as zero.
  *
  *   bias          [N] of param_dtype (QL_BF16 or QL_F32); NULL: 0
@@ -458,9 +458,9 @@ QL_API ql_status qlinear_norm_residual(const void* x, ql_dtype x_dtype, const vo
  * Above 64 rows the epilogue is the fused kernel's (or, where its K-steps are split, that of their sum), up to 64 the
  * streaming path's reduction.  Up to 8 rows of a weight of at most 32 MiB of codes, 16 of 16 and 32 of 4 (of 8-bit codes
  * 8 and 2) may be one launch without a workspace, which multiplies exact codes, offset by 128, by the bf16 activations in
- * fp32: activations beyond 2^110 may overflow there, and an infinite one makes its row NaN.  Weights of 4-bit codes over two thirds of these sizes and wider than
- * N = 8192 (above 8 rows 4096) are faster on the streaming path: the workspace size is that path's for them, and without
- * such a workspace they are one launch like the others.
+ * fp32: activations beyond 2^110 may overflow there, and an infinite one makes its row NaN.  Weights of 4-bit codes over
+ * two thirds of these sizes and wider than N = 8192 (above 8 rows 4096) are faster on the streaming path: the workspace
+ * size is that path's for them, and without such a workspace they are one launch like the others.
  */
 typedef enum { QL_ACT_NONE = 0, QL_ACT_SILU = 1, QL_ACT_GELU = 2, QL_ACT_GELU_TANH = 3 } ql_activation;
 QL_API size_t qlinear_epilogue_workspace_size(int64_t M, int64_t K, int64_t N, int32_t group);
